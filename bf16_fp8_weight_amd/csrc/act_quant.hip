@@ -61,17 +61,6 @@ __device__ __forceinline__ void act_store8(uint64_t a, uint2 q) {
 constexpr int kActThreads = WT_ACT_THREADS;
 constexpr int kActGroups = kActThreads / 16;  // 16-lane groups per workgroup (unaligned path)
 
-// Max over the L lanes of each aligned L-lane group (DPP within 16-lane rows;
-// lanes read from outside the group take no part), left in every lane.
-template <int L>
-__device__ __forceinline__ uint32_t lanes_max(uint32_t m) {
-  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x0B1, 0xF, 0xF, false));  // quad_perm [1,0,3,2]
-  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x04E, 0xF, 0xF, false));  // quad_perm [2,3,0,1]
-  if (L >= 8) m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x141, 0xF, 0xF, false));  // row_half_mirror
-  if (L >= 16) m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x140, 0xF, 0xF, false));  // row_mirror
-  return m;
-}
-
 template <bool Recip>
 __device__ __forceinline__ uint2 quant8(const uint32_t w[4], const TileQ &t) {
   return make_uint2(quant4<Recip>(w[0], w[1], t), quant4<Recip>(w[2], w[3], t));

@@ -1,0 +1,577 @@
+// adamw.hip -- the AdamW step over many parameter shards: gradient norm and
+// update kernels for gfx950, and the entry points that run them. The
+// definition (formulas, rounding of 8-bit states, random bits) is in wt.h.
+#include <hip/hip_runtime.h>
+
+#include <atomic>
+#include <cmath>
+#include <new>
+#include <string>
+
+#include "adamw.h"
+#include "fp8_math.h"
+#include "hip_util.h"
+#include "plan.h"
+#include "wt.h"
+
+namespace wt {
+namespace {
+
+constexpr int kThreads = 256;
+
+// ------------------------------------------------------------ scalars
+__host__ __device__ inline double int_pow(double b, int64_t t) {
+  double r = 1.0;
+  for (uint64_t k = (uint64_t)t; k; k >>= 1) {
+    if (k & 1) r *= b;
+    b *= b;
+  }
+  return r;
+}
+
+__host__ __device__ inline AdamScalars step_scalars(double lr, double beta1, double beta2, double eps, int64_t step,
+                                                    uint64_t seed) {
+  AdamScalars s;
+  const int64_t t = step < 1 ? 1 : step;
+  s.lr = lr;
+  s.lr_bias1 = lr / (1.0 - int_pow(beta1, t));
+  s.b1 = (float)beta1;
+  s.ib1 = (float)(1.0 - beta1);
+  s.b2 = (float)beta2;
+  s.ib2 = (float)(1.0 - beta2);
+  s.inv_bias2 = (float)(1.0 / sqrt(1.0 - int_pow(beta2, t)));
+  s.eps = (float)eps;
+  uint64_t z = seed + (uint64_t)t * 0x9E3779B97F4A7C15ull;
+  z ^= z >> 32;
+  z *= 0x6A09E667F3BCC909ull;
+  z ^= z >> 29;
+  z *= 0xBB67AE8584CAA73Bull;
+  z ^= z >> 32;
+  s.k0 = (uint32_t)z;
+  s.k1 = (uint32_t)(z >> 32);
+  return s;
+}
+
+struct AdamArgs {
+  const AdamTensor *tensors;
+  const AdamItem *items;
+  const AdamNorm *norm;     // null: no norm was computed
+  const int64_t *step_dev;  // null: `s` holds the step's scalars
+  const float *lr_dev;
+  double lr, beta1, beta2, eps;
+  int64_t step;
+  uint64_t seed;
+  AdamScalars s;
+  float grad_scale;
+};
+
+// ------------------------------------------------------------ random bits
+__device__ __forceinline__ uint32_t mix32(uint32_t x) {
+  x ^= x >> 16;
+  x *= 0x6A09E667u;
+  x ^= x >> 15;
+  x *= 0xBB67AE85u;
+  return x ^ (x >> 16);
+}
+
+// ------------------------------------------------------------ element access
+// Four elements at index i of an array, of which those below `left` exist
+// (left >= 4 when Full). Vector: the array's chunks start at the alignment of
+// one access.
+template <bool Full>
+__device__ __forceinline__ void load_f32(uint64_t a, int64_t i, int64_t left, bool vec, float x[4]) {
+  a += 4ull * (uint64_t)i;
+  if (Full || (vec && left >= 4)) {
+    const float4 v = ld_global<float4>(a);
+    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] = e < left ? ld_global<float>(a + 4 * e) : 0.0f;
+}
+
+template <bool Full>
+__device__ __forceinline__ void store_f32(uint64_t a, int64_t i, int64_t left, bool vec, const float x[4]) {
+  a += 4ull * (uint64_t)i;
+  if (Full || (vec && left >= 4)) {
+    st_global<float4>(a, make_float4(x[0], x[1], x[2], x[3]));
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (e < left) st_global<float>(a + 4 * e, x[e]);
+}
+
+template <bool Full>
+__device__ __forceinline__ void load_bf16(uint64_t a, int64_t i, int64_t left, bool vec, float x[4]) {
+  a += 2ull * (uint64_t)i;
+  if (Full || (vec && left >= 4)) {
+    const uint2 v = ld_global<uint2>(a);
+    x[0] = bf16_lo(v.x), x[1] = bf16_hi(v.x), x[2] = bf16_lo(v.y), x[3] = bf16_hi(v.y);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] = e < left ? bf16_lo(ld_global<uint16_t>(a + 2 * e)) : 0.0f;
+}
+
+template <bool Full>
+__device__ __forceinline__ void store_bf16(uint64_t a, int64_t i, int64_t left, bool vec, const uint32_t h[4]) {
+  a += 2ull * (uint64_t)i;
+  if (Full || (vec && left >= 4)) {
+    st_global<uint2>(a, make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16));
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (e < left) st_global<uint16_t>(a + 2 * e, (uint16_t)h[e]);
+}
+
+template <bool Full>
+__device__ __forceinline__ uint32_t load_codes(uint64_t a, int64_t i, int64_t left, bool vec) {
+  a += (uint64_t)i;
+  if (Full || (vec && left >= 4)) return ld_global<uint32_t>(a);
+  uint32_t w = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (e < left) w |= (uint32_t)ld_global<uint8_t>(a + e) << (8 * e);
+  return w;
+}
+
+template <bool Full>
+__device__ __forceinline__ void store_codes(uint64_t a, int64_t i, int64_t left, bool vec, uint32_t w) {
+  a += (uint64_t)i;
+  if (Full || (vec && left >= 4)) {
+    st_global<uint32_t>(a, w);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (e < left) st_global<uint8_t>(a + e, (uint8_t)(w >> (8 * e)));
+}
+
+__device__ __forceinline__ void decode4(uint32_t w, float scale, float x[4]) {
+  x[0] = __builtin_amdgcn_cvt_f32_fp8((int)w, 0) * scale;
+  x[1] = __builtin_amdgcn_cvt_f32_fp8((int)w, 1) * scale;
+  x[2] = __builtin_amdgcn_cvt_f32_fp8((int)w, 2) * scale;
+  x[3] = __builtin_amdgcn_cvt_f32_fp8((int)w, 3) * scale;
+}
+
+__device__ __forceinline__ uint32_t bf16_nearest(float x) {
+  return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x);
+}
+
+// fp32 -> BF16, the magnitude rounded up where the 16 dropped bits plus the
+// random ones reach a whole step; infinities and NaN keep their top bits (a
+// NaN whose payload sits in the dropped bits stays a NaN).
+__device__ __forceinline__ uint32_t bf16_random(float x, uint32_t r16) {
+  const uint32_t b = __float_as_uint(x);
+  if ((b & 0x7F800000u) == 0x7F800000u) return bf16_nearest(x);
+  return (b + r16) >> 16;
+}
+
+constexpr uint32_t kFiniteEnd = 0x7F800000u;  // magnitude bits from here up: infinity, NaN
+constexpr float kTinyAmax = 0x1p-100f;        // below: the block is held as zeros
+
+// Scale of a block from its amax bits, and the factor x -> code units.
+__device__ __forceinline__ void state_scale(uint32_t amax_bits, float *scale, float *inv) {
+  const float amax = __uint_as_float(amax_bits);
+  const bool live = amax >= kTinyAmax;
+  *scale = live ? amax / 448.0f : 1.0f;
+  *inv = live ? 448.0f / amax : 0.0f;
+}
+
+// Four values as E4M3 codes: |x| inv + rho rounded down in units of the
+// format. v_cvt_sr_fp8_f32 adds the top 20 bits of its random operand below
+// the kept mantissa bits and cuts, subnormal codes included (equal to the
+// definition on 4.2 M random values over the whole range); it does not
+// saturate, so the value is cut at 448 first.
+template <bool Root>
+__device__ __forceinline__ uint32_t encode4(const float x[4], float inv, const uint32_t w[4]) {
+  int q = 0;
+  float y[4];
+  uint32_t bad = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (Root) {
+      y[e] = fminf(x[e] * inv, 448.0f);
+      if (x[e] > 0.0f && inv > 0.0f) y[e] = fmaxf(y[e], 0x1p-9f);
+    } else {
+      y[e] = __builtin_amdgcn_fmed3f(x[e] * inv, -448.0f, 448.0f);
+    }
+    bad |= (__float_as_uint(x[e]) & 0x7FFFFFFFu) >= kFiniteEnd ? 0xFFu << (8 * e) : 0u;
+  }
+#define WT_RND(e) (int)(Root ? w[e] & 0xFFFF0000u : w[e] << 16)
+  q = __builtin_amdgcn_cvt_sr_fp8_f32(y[0], WT_RND(0), q, 0);
+  q = __builtin_amdgcn_cvt_sr_fp8_f32(y[1], WT_RND(1), q, 1);
+  q = __builtin_amdgcn_cvt_sr_fp8_f32(y[2], WT_RND(2), q, 2);
+  q = __builtin_amdgcn_cvt_sr_fp8_f32(y[3], WT_RND(3), q, 3);
+#undef WT_RND
+  return ((uint32_t)q & ~bad) | (bad & 0x7F7F7F7Fu);
+}
+
+__device__ __forceinline__ uint32_t finite_bits(float x) {
+  const uint32_t b = __float_as_uint(x) & 0x7FFFFFFFu;
+  return b < kFiniteEnd ? b : 0u;
+}
+
+// ------------------------------------------------------------ update
+// One item: 4096 elements of one tensor, 256 threads. Sixteen lanes share a
+// 128-element block, lane l owning its 4-element chunks l and l + 16, so each
+// access of a wave covers consecutive bytes (fp32 256, BF16 128, codes 64 per
+// block) and the block's amax is a DPP max over a row of 16 lanes.
+template <int Bits, bool Full>
+__device__ __forceinline__ void update_item(const AdamTensor &t, uint32_t chunk, const AdamScalars &s, float gs) {
+  const uint32_t tid = threadIdx.x, l = tid & 15;
+  const bool vec = t.flags & kAdamVector;
+  const bool gbf = t.flags & kAdamGradBf16, has_master = t.flags & kAdamMaster, has_param = t.flags & kAdamParam;
+  const float decay = (float)(1.0 - s.lr * (double)t.lr_mul * (double)t.weight_decay);
+  const float rate = (float)(s.lr_bias1 * (double)t.lr_mul);
+#pragma unroll
+  for (int it = 0; it < kAdamItem / (kThreads / 16 * kAdamBlock); ++it) {
+    const uint32_t b = chunk * (kAdamItem / kAdamBlock) + (uint32_t)it * (kThreads / 16) + (tid >> 4);
+    const int64_t i0 = (int64_t)b * kAdamBlock + 4 * l;
+    float g[8], p[8], m[8], v[8], sm = 1.0f, sv = 1.0f;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int64_t i = i0 + 64 * c, left = t.n - i;
+      if (gbf) load_bf16<Full>(t.grad, i, left, vec, g + 4 * c);
+      else load_f32<Full>(t.grad, i, left, vec, g + 4 * c);
+      if (has_master) load_f32<Full>(t.master, i, left, vec, p + 4 * c);
+      else load_bf16<Full>(t.param, i, left, vec, p + 4 * c);
+      if (Bits == 32) {
+        load_f32<Full>(t.m, i, left, vec, m + 4 * c);
+        load_f32<Full>(t.v, i, left, vec, v + 4 * c);
+      }
+    }
+    if (Bits == 8) {
+      if (Full || (int64_t)b * kAdamBlock < t.n) {
+        sm = ld_global<float>(t.m_scale + 4ull * b);
+        sv = ld_global<float>(t.v_scale + 4ull * b);
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int64_t i = i0 + 64 * c, left = t.n - i;
+        decode4(load_codes<Full>(t.m, i, left, vec), sm, m + 4 * c);
+        decode4(load_codes<Full>(t.v, i, left, vec), sv, v + 4 * c);
+      }
+    }
+    uint32_t am = 0, av = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float x = g[e] * gs;
+      m[e] = fmaf(s.b1, m[e], s.ib1 * x);
+      if (Bits == 8) v[e] *= v[e];
+      v[e] = fmaf(s.b2, v[e], s.ib2 * (x * x));
+      const float root = sqrtf(v[e]);
+      const float u = m[e] / fmaf(root, s.inv_bias2, s.eps);
+      p[e] = fmaf(-rate, u, p[e] * decay);
+      if (Bits == 8) {
+        v[e] = root;
+        am = max(am, finite_bits(m[e]));
+        av = max(av, finite_bits(root));
+      }
+    }
+    uint32_t w[8];
+    if (Bits == 8 || !has_master) {
+      const uint32_t key = mix32((t.block0 + b) ^ s.k0) + s.k1;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = mix32(key + (4 * l + 64 * (e >> 2) + (e & 3)) * 0x9E3779B9u);
+    }
+    if (Bits == 8) {
+      float im, iv;
+      am = lanes_max<16>(am);  // every lane of the row takes part
+      av = lanes_max<16>(av);
+      state_scale(am, &sm, &im);
+      state_scale(av, &sv, &iv);
+      if (l == 0 && (Full || (int64_t)b * kAdamBlock < t.n)) {
+        st_global<float>(t.m_scale + 4ull * b, sm);
+        st_global<float>(t.v_scale + 4ull * b, sv);
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int64_t i = i0 + 64 * c, left = t.n - i;
+        store_codes<Full>(t.m, i, left, vec, encode4<false>(m + 4 * c, im, w + 4 * c));
+        store_codes<Full>(t.v, i, left, vec, encode4<true>(v + 4 * c, iv, w + 4 * c));
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int64_t i = i0 + 64 * c, left = t.n - i;
+      if (Bits == 32) {
+        store_f32<Full>(t.m, i, left, vec, m + 4 * c);
+        store_f32<Full>(t.v, i, left, vec, v + 4 * c);
+      }
+      if (has_master) store_f32<Full>(t.master, i, left, vec, p + 4 * c);
+      if (has_param) {
+        uint32_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          h[e] = has_master ? bf16_nearest(p[4 * c + e]) : bf16_random(p[4 * c + e], (w[4 * c + e] * 0x9E3779B9u) >> 16);
+        store_bf16<Full>(t.param, i, left, vec, h);
+      }
+    }
+  }
+}
+
+template <int Bits>
+__global__ void __launch_bounds__(kThreads) adamw_update_kernel(AdamArgs a) {
+  const AdamItem item = ld_table(a.items, blockIdx.x);
+  const AdamTensor t = ld_table(a.tensors, item.tensor);
+  float gs = a.grad_scale;
+  if (a.norm) {
+    if (a.norm->skip) return;
+    gs *= a.norm->clip;
+  }
+  AdamScalars s = a.s;
+  if (a.step_dev || a.lr_dev)
+    s = step_scalars(a.lr_dev ? (double)*a.lr_dev : a.lr, a.beta1, a.beta2, a.eps, a.step_dev ? *a.step_dev : a.step,
+                     a.seed);
+  if ((t.flags & kAdamVector) && ((int64_t)item.chunk + 1) * kAdamItem <= t.n)
+    update_item<Bits, true>(t, item.chunk, s, gs);
+  else
+    update_item<Bits, false>(t, item.chunk, s, gs);
+}
+
+// ------------------------------------------------------------ norm
+template <bool Full>
+__device__ __forceinline__ float item_squares(const AdamTensor &t, uint32_t chunk) {
+  const bool vec = t.flags & kAdamVector, gbf = t.flags & kAdamGradBf16;
+  float sum = 0.0f;
+#pragma unroll
+  for (int c = 0; c < kAdamItem / (4 * kThreads); ++c) {
+    const int64_t i = (int64_t)chunk * kAdamItem + 4 * (c * kThreads + (int)threadIdx.x), left = t.n - i;
+    float g[4];
+    if (gbf) load_bf16<Full>(t.grad, i, left, vec, g);
+    else load_f32<Full>(t.grad, i, left, vec, g);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum = fmaf(g[e], g[e], sum);
+  }
+  return sum;
+}
+
+__device__ __forceinline__ double block_sum(double x, double *lds) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) x += __shfl_xor(x, d);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
+  __syncthreads();
+  return (lds[0] + lds[1]) + (lds[2] + lds[3]);
+}
+
+// Sum of the squares of every gradient: each workgroup adds its items
+// (fp32 over a thread's 16 elements of an item, fp64 beyond), and the last
+// one to finish adds the workgroups' sums in a fixed order.
+__global__ void __launch_bounds__(kThreads)
+    adamw_norm_kernel(const AdamTensor *tensors, const AdamItem *items, uint32_t n_items, double *partials,
+                      AdamNorm *norm, float grad_scale, double max_norm, float *norm_out) {
+  __shared__ double lds[4];
+  __shared__ uint32_t last;
+  double sum = 0.0;
+  for (uint32_t k = blockIdx.x; k < n_items; k += gridDim.x) {
+    const AdamItem item = ld_table(items, k);
+    const AdamTensor t = ld_table(tensors, item.tensor);
+    if ((t.flags & kAdamVector) && ((int64_t)item.chunk + 1) * kAdamItem <= t.n)
+      sum += (double)item_squares<true>(t, item.chunk);
+    else
+      sum += (double)item_squares<false>(t, item.chunk);
+  }
+  sum = block_sum(sum, lds);
+  if (threadIdx.x == 0) {
+    __hip_atomic_store(&partials[blockIdx.x], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    last = __hip_atomic_fetch_add(&norm->count, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!last) return;
+  sum = 0.0;
+  for (uint32_t k = threadIdx.x; k < gridDim.x; k += kThreads)
+    sum += __hip_atomic_load(&partials[k], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  sum = block_sum(sum, lds);
+  if (threadIdx.x == 0) {
+    const double n = sqrt(sum) * fabs((double)grad_scale);
+    const bool finite = n <= 3.4028234663852886e38;
+    double clip = 1.0;
+    if (max_norm > 0.0 && max_norm < n + 1e-6) clip = max_norm / (n + 1e-6);
+    norm->clip = (float)clip;
+    norm->skip = finite ? 0u : 1u;
+    norm->count = 0u;
+    if (norm_out) *norm_out = (float)n;
+  }
+}
+
+}  // namespace
+}  // namespace wt
+
+using namespace wt;
+
+struct wt_adamw {
+  AdamLayout L;
+  AdamOffsets at{};
+  int device = 0;
+  uint8_t *mem = nullptr;
+  std::atomic<bool> busy{false};
+};
+
+namespace {
+
+wt_status fail(const std::string &m, wt_status st) {
+  set_thread_error("wt_adamw: " + m);
+  return st;
+}
+
+wt_status check_tensors(const wt_adamw_tensor *t, size_t n, bool s8, int device, std::string *err) {
+  for (size_t i = 0; i < n; ++i) {
+    if (t[i].n == 0) continue;
+    const uint64_t e = (uint64_t)t[i].n, nb = (e + kAdamBlock - 1) / kAdamBlock;
+    const struct {
+      const void *p;
+      uint64_t bytes;
+      const char *what;
+    } parts[] = {{t[i].param, 2 * e, "param"},
+                 {t[i].master, 4 * e, "master"},
+                 {t[i].grad, (t[i].grad_dtype == WT_DT_BF16 ? 2 : 4) * e, "grad"},
+                 {t[i].m, (s8 ? 1 : 4) * e, "m"},
+                 {t[i].v, (s8 ? 1 : 4) * e, "v"},
+                 {s8 ? t[i].m_scale : nullptr, 4 * nb, "m_scale"},
+                 {s8 ? t[i].v_scale : nullptr, 4 * nb, "v_scale"}};
+    for (const auto &q : parts) {
+      if (!q.p) continue;
+      const wt_status st = check_memory(q.p, q.bytes, WT_MEM_DEVICE, device,
+                                        "tensor " + std::to_string(i) + ": " + q.what, err);
+      if (st != WT_OK) return st;
+    }
+  }
+  return WT_OK;
+}
+
+wt_status create_impl(const wt_adamw_tensor *tensors, size_t n, const wt_adamw_options &o, wt_adamw *a) {
+  std::string err;
+  wt_status st = build_adamw(tensors, n, o, &a->L, &err);
+  if (st != WT_OK) return fail(err, st);
+  int count = 0, dev = o.device;
+  hipError_t e = hipGetDeviceCount(&count);
+  if (e == hipSuccess && dev < 0) e = hipGetDevice(&dev);
+  if (e != hipSuccess) return fail(hip_msg("device query", e), WT_E_HIP);
+  if (dev >= count) return fail("no such device", WT_E_INVAL);
+  a->device = dev;
+  DeviceGuard guard(dev);
+  st = check_tensors(tensors, n, o.state_bits == 8, dev, &err);
+  if (st != WT_OK) return fail(err, st);
+  a->at = adamw_offsets(a->L);
+  e = hipMalloc((void **)&a->mem, a->at.bytes);
+  if (e == hipErrorOutOfMemory) return fail("device allocation failed", WT_E_NOMEM);
+  if (e == hipSuccess) e = hipMemset(a->mem, 0, a->at.bytes);
+  if (e == hipSuccess && !a->L.tensors.empty())
+    e = hipMemcpy(a->mem + a->at.tensors, a->L.tensors.data(), a->L.tensors.size() * sizeof(AdamTensor),
+                  hipMemcpyHostToDevice);
+  if (e == hipSuccess && !a->L.items.empty())
+    e = hipMemcpy(a->mem + a->at.items, a->L.items.data(), a->L.items.size() * sizeof(AdamItem),
+                  hipMemcpyHostToDevice);
+  if (e == hipSuccess) e = hipDeviceSynchronize();  // the tables are there before a step on any stream
+  if (e != hipSuccess) return fail(hip_msg("device tables", e), WT_E_HIP);
+  // the launch needs only their numbers from here on
+  std::vector<AdamItem>().swap(a->L.items);
+  return WT_OK;
+}
+
+wt_status step_impl(wt_adamw *a, const wt_adamw_hyper *h, hipStream_t stream) {
+  std::string err;
+  wt_status st = check_adamw_hyper(h, &err);
+  if (st != WT_OK) return fail(err, st);
+  DeviceGuard guard(a->device);
+  const uint32_t n_items = (uint32_t)a->L.info.n_items;
+  AdamArgs k{};
+  k.tensors = (const AdamTensor *)(a->mem + a->at.tensors);
+  k.items = (const AdamItem *)(a->mem + a->at.items);
+  k.step_dev = h->step_dev;
+  k.lr_dev = h->lr_dev;
+  k.lr = h->lr;
+  k.beta1 = h->beta1;
+  k.beta2 = h->beta2;
+  k.eps = h->eps;
+  k.step = h->step;
+  k.seed = h->seed;
+  k.s = step_scalars(h->lr, h->beta1, h->beta2, h->eps, h->step, h->seed);
+  k.grad_scale = (float)h->grad_scale;
+  if (h->max_norm > 0 || h->norm_out) {
+    AdamNorm *norm = (AdamNorm *)(a->mem + a->at.norm);
+    const uint32_t grid = n_items < 1 ? 1 : n_items < kAdamNormGrid ? n_items : kAdamNormGrid;
+    hipLaunchKernelGGL(adamw_norm_kernel, dim3(grid), dim3(kThreads), 0, stream, k.tensors, k.items, n_items,
+                       (double *)(a->mem + a->at.partials), norm, k.grad_scale, h->max_norm, h->norm_out);
+    k.norm = norm;
+  }
+  if (n_items > 0) {
+    if (a->L.state_bits == 8)
+      hipLaunchKernelGGL((adamw_update_kernel<8>), dim3(n_items), dim3(kThreads), 0, stream, k);
+    else
+      hipLaunchKernelGGL((adamw_update_kernel<32>), dim3(n_items), dim3(kThreads), 0, stream, k);
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return fail(hip_msg("launch", e), WT_E_HIP);
+  return WT_OK;
+}
+
+void free_adamw(wt_adamw *a) {
+  if (a->mem) {
+    DeviceGuard guard(a->device);
+    (void)hipDeviceSynchronize();
+    (void)hipFree(a->mem);
+  }
+  delete a;
+}
+
+}  // namespace
+
+extern "C" {
+
+wt_status wt_adamw_create(const wt_adamw_tensor *tensors, size_t n_tensors, const wt_adamw_options *opts,
+                          wt_adamw **out) {
+  if (!out) return WT_E_INVAL;
+  *out = nullptr;
+  wt_adamw *a = nullptr;
+  wt_status st;
+  try {
+    a = new wt_adamw();
+    st = create_impl(tensors, n_tensors, resolve_adamw_opts(opts), a);
+  } catch (const std::bad_alloc &) {
+    set_thread_error("host allocation failed");
+    st = WT_E_NOMEM;
+  } catch (...) {
+    set_thread_error("internal error");
+    st = WT_E_INVAL;
+  }
+  if (st == WT_OK)
+    *out = a;
+  else if (a)
+    free_adamw(a);
+  return st;
+}
+
+wt_status wt_adamw_step(wt_adamw *adamw, const wt_adamw_hyper *hyper, void *stream) {
+  if (!adamw) return WT_E_INVAL;
+  bool expected = false;
+  if (!adamw->busy.compare_exchange_strong(expected, true)) {
+    set_thread_error("wt_adamw: a step of this handle is being enqueued by another thread");
+    return WT_E_STATE;
+  }
+  wt_status st;
+  try {
+    st = step_impl(adamw, hyper, (hipStream_t)stream);
+  } catch (...) {
+    set_thread_error("internal error");
+    st = WT_E_INVAL;
+  }
+  adamw->busy.store(false);
+  return st;
+}
+
+wt_status wt_adamw_get_info(const wt_adamw *adamw, wt_adamw_info *info) {
+  if (!adamw || !info) return WT_E_INVAL;
+  *info = adamw->L.info;
+  return WT_OK;
+}
+
+void wt_adamw_destroy(wt_adamw *adamw) {
+  if (adamw) free_adamw(adamw);
+}
+
+}  // extern "C"

@@ -26,6 +26,8 @@ WT_DST_ZERO_COPY = 0
 WT_DST_STAGED = 1
 WT_LOAD_AUTO, WT_LOAD_PLAIN, WT_LOAD_STREAM = range(3)
 WT_GROUP_AUTO, WT_GROUP_SINGLE, WT_GROUP_PAIR = range(3)
+WT_DT_F32 = 0
+WT_DT_BF16 = 1
 
 EXPORTS = [
     "wt_plan_options_init", "wt_plan_check", "wt_plan_schedule", "wt_plan_create", "wt_prepare",
@@ -34,6 +36,8 @@ EXPORTS = [
     "wt_schedule_build", "wt_schedule_info", "wt_schedule_output", "wt_schedule_tasks", "wt_schedule_destroy",
     "wt_plan_set_progress", "wt_plan_task_unit", "wt_progress_wait", "wt_quantize_act_b128",
     "wt_plan_create_noalloc",
+    "wt_adamw_options_init", "wt_adamw_hyper_init", "wt_adamw_check", "wt_adamw_create", "wt_adamw_step",
+    "wt_adamw_get_info", "wt_adamw_destroy",
 ]
 
 
@@ -113,6 +117,38 @@ class wt_schedule_options(ctypes.Structure):
     _fields_ = [("align", ctypes.c_uint64), ("n_sources", ctypes.c_int32), ("reserved", ctypes.c_int32 * 5)]
 
 
+class wt_adamw_tensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "master", "grad", "m", "v", "m_scale", "v_scale")] + [
+        ("n", ctypes.c_int64),
+        ("grad_dtype", ctypes.c_int32),
+        ("lr_mul", ctypes.c_float),
+        ("weight_decay", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class wt_adamw_options(ctypes.Structure):
+    _fields_ = [("state_bits", ctypes.c_int32), ("device", ctypes.c_int32), ("reserved", ctypes.c_int32 * 6)]
+
+
+class wt_adamw_hyper(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "grad_scale", "max_norm")] + [
+        ("step", ctypes.c_int64),
+        ("seed", ctypes.c_uint64),
+        ("step_dev", ctypes.c_void_p),
+        ("lr_dev", ctypes.c_void_p),
+        ("norm_out", ctypes.c_void_p),
+    ]
+
+
+class wt_adamw_info(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in (
+        "n_tensors", "n_elements", "n_blocks", "n_items", "n_vector_tensors", "table_bytes")]
+
+    def as_dict(self):
+        return {n: int(getattr(self, n)) for n, _ in self._fields_}
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -161,6 +197,20 @@ def _load() -> ctypes.CDLL:
     L.wt_plan_task_unit.argtypes = [vp, sz, P(i32)]
     L.wt_quantize_act_b128.restype = ctypes.c_int
     L.wt_quantize_act_b128.argtypes = [vp, i64, i64, i64, vp, i64, vp, i64, vp, i64, vp]
+    L.wt_adamw_options_init.restype = None
+    L.wt_adamw_options_init.argtypes = [P(wt_adamw_options)]
+    L.wt_adamw_hyper_init.restype = None
+    L.wt_adamw_hyper_init.argtypes = [P(wt_adamw_hyper)]
+    L.wt_adamw_check.restype = ctypes.c_int
+    L.wt_adamw_check.argtypes = [P(wt_adamw_tensor), sz, P(wt_adamw_options), P(wt_adamw_info)]
+    L.wt_adamw_create.restype = ctypes.c_int
+    L.wt_adamw_create.argtypes = [P(wt_adamw_tensor), sz, P(wt_adamw_options), P(vp)]
+    L.wt_adamw_step.restype = ctypes.c_int
+    L.wt_adamw_step.argtypes = [vp, P(wt_adamw_hyper), vp]
+    L.wt_adamw_get_info.restype = ctypes.c_int
+    L.wt_adamw_get_info.argtypes = [vp, P(wt_adamw_info)]
+    L.wt_adamw_destroy.restype = None
+    L.wt_adamw_destroy.argtypes = [vp]
     L.wt_progress_wait.restype = ctypes.c_int
     L.wt_progress_wait.argtypes = [vp, ctypes.c_uint64, ctypes.c_uint64]
     return L
@@ -386,6 +436,127 @@ class Schedule:
         if getattr(self, "handle", 0):
             lib.wt_schedule_destroy(self.handle)
             self.handle = 0
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+# ------------------------------------------------------------- optimizer step
+def wt_adamw_options_init() -> wt_adamw_options:
+    o = wt_adamw_options()
+    lib.wt_adamw_options_init(ctypes.byref(o))
+    return o
+
+
+def wt_adamw_hyper_init() -> wt_adamw_hyper:
+    h = wt_adamw_hyper()
+    lib.wt_adamw_hyper_init(ctypes.byref(h))
+    return h
+
+
+class AdamWTable:
+    """A ctypes table of wt_adamw_tensor from dicts with its field names
+    (addresses as integers, 0 or missing = NULL; lr_mul 1 and weight_decay 0
+    unless given)."""
+
+    def __init__(self, tensors: Sequence[dict]):
+        self.n = len(tensors)
+        self.arr = (wt_adamw_tensor * max(1, self.n))()
+        for a, t in zip(self.arr, tensors):
+            for f in ("param", "master", "grad", "m", "v", "m_scale", "v_scale"):
+                setattr(a, f, t.get(f) or None)
+            a.n = t["n"]
+            a.grad_dtype = t.get("grad_dtype", WT_DT_F32)
+            a.lr_mul = t.get("lr_mul", 1.0)
+            a.weight_decay = t.get("weight_decay", 0.0)
+
+
+def wt_adamw_check(table: AdamWTable, opts: Optional[wt_adamw_options] = None) -> dict:
+    info = wt_adamw_info()
+    _check(lib.wt_adamw_check(table.arr, table.n, ctypes.byref(opts) if opts else None, ctypes.byref(info)))
+    return info.as_dict()
+
+
+def wt_adamw_create(table: AdamWTable, opts: Optional[wt_adamw_options] = None) -> int:
+    out = ctypes.c_void_p(0)
+    _check(lib.wt_adamw_create(table.arr, table.n, ctypes.byref(opts) if opts else None, ctypes.byref(out)))
+    return out.value
+
+
+def wt_adamw_step(adamw: int, hyper: wt_adamw_hyper, stream: int = 0) -> None:
+    _check(lib.wt_adamw_step(adamw, ctypes.byref(hyper), stream or None))
+
+
+def wt_adamw_get_info(adamw: int) -> dict:
+    info = wt_adamw_info()
+    _check(lib.wt_adamw_get_info(adamw, ctypes.byref(info)))
+    return info.as_dict()
+
+
+def wt_adamw_destroy(adamw: int) -> None:
+    lib.wt_adamw_destroy(adamw)
+
+
+class AdamW:
+    """Owns a wt_adamw handle for a table of parameter shards (dicts, see
+    AdamWTable). `keep`: whatever owns the memory the table points to, held
+    until close()."""
+
+    def __init__(self, tensors: Sequence[dict], state_bits: int = 32, device: int = -1, keep=None):
+        o = wt_adamw_options_init()
+        o.state_bits, o.device = state_bits, device
+        self.keep = keep
+        self.handle = wt_adamw_create(AdamWTable(tensors), o)
+
+    @classmethod
+    def for_workload(cls, wl, grads, state_bits: int = 32, master: bool = True, weight_decay: float = 0.0) -> "AdamW":
+        """The step over a device workload's shards, in place, so that a Plan of
+        the same workload transfers what it writes. grads: one tensor per
+        non-empty shard, in the order of outputs, parts and shards (fp32 or
+        BF16). Makes zero states and, with `master`, fp32 copies of the shards
+        (`keep` holds them: dicts of tensors by field name)."""
+        import torch
+
+        shards = [s for o in wl.outputs for p in o.parts for s, r in zip(p.shards, p.shard_rows) if r]
+        if len(grads) != len(shards):
+            raise ValueError(f"{len(grads)} gradients for {len(shards)} non-empty shards")
+        table, keep = [], []
+        for s, g in zip(shards, grads):
+            n = s.numel()
+            if g.numel() != n or not g.is_contiguous() or g.dtype not in (torch.float32, torch.bfloat16):
+                raise ValueError("a gradient is a contiguous fp32 or BF16 tensor of its shard's size")
+            t = {"param": s, "grad": g}
+            if master:
+                t["master"] = s.reshape(-1).float()
+            for f in ("m", "v"):
+                t[f] = torch.zeros(n, dtype=torch.float32 if state_bits == 32 else torch.uint8, device=s.device)
+                if state_bits == 8:
+                    t[f + "_scale"] = torch.ones(-(-n // 128), dtype=torch.float32, device=s.device)
+            keep.append(t)
+            table.append(dict({f: x.data_ptr() for f, x in t.items()}, n=n, weight_decay=weight_decay,
+                              grad_dtype=WT_DT_BF16 if g.dtype == torch.bfloat16 else WT_DT_F32))
+        return cls(table, state_bits, device=shards[0].device.index if shards else -1, keep=(wl, keep))
+
+    def step(self, hyper: wt_adamw_hyper, stream: int = 0) -> None:
+        wt_adamw_step(self.handle, hyper, stream)
+
+    def info(self) -> dict:
+        return wt_adamw_get_info(self.handle)
+
+    def close(self) -> None:
+        if getattr(self, "handle", 0):
+            wt_adamw_destroy(self.handle)
+            self.handle = 0
+        self.keep = None
+
+    def __enter__(self) -> "AdamW":
+        return self
+
+    def __exit__(self, *exc) -> None:
+        self.close()
 
     def __del__(self):
         try:

@@ -404,6 +404,141 @@ wt_status wt_quantize_act_b128(const void *x, int64_t n_rows, int64_t cols, int6
                                const int32_t *row_index, int64_t n_out, void *q, int64_t q_row_stride,
                                void *scales, int64_t scale_row_stride, void *stream);
 
+/* ---- AdamW over many parameter shards ----
+ * The optimizer step that produces what wt_prepare transfers ("Weight transfer
+ * for RL post-training in under 2 seconds", section "High-level workflow":
+ * after each training step the training GPUs send their parameters). One call
+ * updates every shard of a rank in place, in one launch (two when the
+ * gradients are clipped by their global norm), so a prepare enqueued behind it
+ * on the same stream reads the new weights.
+ *
+ * Per element, with g = grad * grad_scale * clip and t = the step's number:
+ *   m' = beta1 m + (1 - beta1) g        v' = beta2 v + (1 - beta2) g^2
+ *   u  = (m' / (1 - beta1^t)) / (sqrt(v' / (1 - beta2^t)) + eps)
+ *   p' = p - lr lr_mul (weight_decay p + u)
+ * all in fp32. p is the fp32 master copy if the tensor has one (the BF16 shard
+ * then receives p' rounded to nearest even), else the BF16 shard itself.
+ * clip = min(1, max_norm / (norm + 1e-6)), norm = grad_scale * sqrt(the sum of
+ * grad^2 over every tensor); 1 when max_norm is 0.
+ *
+ * Rounded states. Where fewer than 32 bits carry a value from step to step
+ * (8-bit states, a BF16 shard without a master), rounding to nearest would
+ * drop every change below half a step of the format and the state would stand
+ * still; those values are rounded up or down with the probabilities that keep
+ * their mean: x in units of its format becomes floor(|x| + rho), with 16
+ * random bits rho = r / 65536. The bits come from `seed`, the step's number
+ * and the element's place in the table, so a run repeats exactly.
+ *
+ * 8-bit states: m and sqrt(v) (the root halves the range of exponents) are
+ * held as OCP E4M3 codes with one fp32 scale per 128 consecutive elements of
+ * the tensor (the last block may be shorter): scale = amax / 448, code =
+ * x / scale rounded as above. A block whose amax is below 2^-100 holds zeros
+ * with scale 1. A positive sqrt(v) never rounds to zero (the smallest code
+ * stands for it), which keeps u bounded. A value that is not finite is held as
+ * the NaN code and takes no part in its block's amax, so it stays with its
+ * element. States start as zeros (codes 0; the scales must be finite).
+ *
+ * Random bits of element i of a tensor: block b = the tensor's first block +
+ * i / 128 (blocks are numbered through the table, ceil(n / 128) per tensor),
+ * j = i mod 128, and with mix(x): x ^= x >> 16; x *= 0x6A09E667; x ^= x >> 15;
+ * x *= 0xBB67AE85; x ^= x >> 16 (32-bit),
+ *   w = mix(mix(b ^ k0) + k1 + j * 0x9E3779B9);
+ * m takes w's low 16 bits, sqrt(v) the high 16, a BF16 shard the high 16 of
+ * w * 0x9E3779B9. (k0, k1) are the low and high half of z = seed +
+ * t * 0x9E3779B97F4A7C15; z ^= z >> 32; z *= 0x6A09E667F3BCC909; z ^= z >> 29;
+ * z *= 0xBB67AE8584CAA73B; z ^= z >> 32 (64-bit). */
+
+/* Element types of gradients and router logits. */
+enum { WT_DT_F32 = 0, WT_DT_BF16 = 1 };
+
+/* One parameter shard: n consecutive elements (n may be 0). Device memory;
+ * every range the step writes must be disjoint from every other range of the
+ * table (two tensors may share a gradient). */
+typedef struct wt_adamw_tensor {
+  void *param;      /* BF16 shard, 2-byte aligned, or NULL (the fp32 master is then all there is) */
+  float *master;    /* fp32 copy, or NULL (then param is the only copy) */
+  const void *grad; /* grad_dtype */
+  void *m;          /* first moment: fp32, or E4M3 codes */
+  void *v;          /* second moment as fp32, or its root as E4M3 codes */
+  float *m_scale;   /* 8-bit states: ceil(n / 128) scales; ignored otherwise */
+  float *v_scale;
+  int64_t n;
+  int32_t grad_dtype;
+  float lr_mul;       /* >= 0; multiplies the step's learning rate */
+  float weight_decay; /* >= 0 */
+  int32_t reserved;
+} wt_adamw_tensor;
+
+typedef struct wt_adamw_options {
+  int32_t state_bits; /* 32 (default) or 8 */
+  int32_t device;     /* HIP device ordinal; -1 (default) = current device */
+  int32_t reserved[6];
+} wt_adamw_options;
+
+/* What one step takes. wt_adamw_hyper_init() fills the defaults. */
+typedef struct wt_adamw_hyper {
+  double lr;         /* 1e-3 */
+  double beta1;      /* 0.9; 0 <= beta < 1 */
+  double beta2;      /* 0.999 */
+  double eps;        /* 1e-8; at least 1e-30 */
+  double grad_scale; /* 1: every gradient is multiplied by it (1 / loss scale, 1 / accumulated steps) */
+  double max_norm;   /* 0: no clipping; > 0: the norm the gradients are clipped to */
+  int64_t step;      /* number of this step, from 1 */
+  uint64_t seed;     /* of the random bits */
+  /* Device memory, may be NULL. step_dev / lr_dev: the step's number and the
+   * learning rate are read there when the step runs instead of from `step` and
+   * `lr`, so that a captured step can be replayed with new ones. norm_out
+   * receives the gradients' norm (before clipping). */
+  const int64_t *step_dev;
+  const float *lr_dev;
+  float *norm_out;
+} wt_adamw_hyper;
+
+typedef struct wt_adamw_info {
+  int64_t n_tensors;        /* with n > 0 */
+  int64_t n_elements;
+  int64_t n_blocks;         /* 128-element blocks */
+  int64_t n_items;          /* work items of the launch */
+  int64_t n_vector_tensors; /* tensors whose addresses allow 4-element accesses */
+  int64_t table_bytes;      /* device memory the handle holds */
+} wt_adamw_info;
+
+typedef struct wt_adamw wt_adamw;
+
+void wt_adamw_options_init(wt_adamw_options *opts);
+void wt_adamw_hyper_init(wt_adamw_hyper *hyper);
+
+/* Validates a table exactly as wt_adamw_create does and describes the handle,
+ * without touching any GPU. opts (defaults) and info may be NULL. WT_E_INVAL:
+ * NULL pointers, sizes or factors out of range; WT_E_ALIGN; WT_E_OVERLAP. */
+wt_status wt_adamw_check(const wt_adamw_tensor *tensors, size_t n_tensors, const wt_adamw_options *opts,
+                         wt_adamw_info *info);
+
+/* Builds the step's device tables. The table is copied; the tensors stay the
+ * caller's and must outlive the handle at the same addresses. On failure *out
+ * is NULL and wt_plan_last_error(NULL) says why (likewise for the calls
+ * below). */
+wt_status wt_adamw_create(const wt_adamw_tensor *tensors, size_t n_tensors, const wt_adamw_options *opts,
+                          wt_adamw **out);
+
+/* Enqueues one step on `stream` (of the handle's device); returns without
+ * waiting. When the norm is computed (max_norm > 0 or norm_out) and is not
+ * finite, the step changes nothing but norm_out, so that one bad batch can be
+ * left out. No allocation happens here, and a step may be captured: a replay
+ * repeats it with the hyper values of the capture, apart from step_dev and
+ * lr_dev (a step_dev below 1 counts as 1). The steps of one handle must be
+ * ordered one behind the other, replays included: they update the same memory
+ * and share the handle's workspace. WT_E_STATE if another thread is inside the
+ * call with this handle; WT_E_INVAL for hyper values out of range; WT_E_HIP if
+ * a launch fails. */
+wt_status wt_adamw_step(wt_adamw *adamw, const wt_adamw_hyper *hyper, void *stream);
+
+wt_status wt_adamw_get_info(const wt_adamw *adamw, wt_adamw_info *info);
+
+/* Waits for the handle's device, then frees what the handle owns. A graph that
+ * holds captured steps must not be launched after this. NULL is ignored. */
+void wt_adamw_destroy(wt_adamw *adamw);
+
 /* ---- Completion counters ----
  * Host-visible words that the GPU writes as parts of a replay finish, so a
  * host thread can start moving a part of the destination region (the one-sided

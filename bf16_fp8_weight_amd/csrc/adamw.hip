@@ -214,6 +214,17 @@ __device__ __forceinline__ uint32_t finite_bits(float x) {
   return b < kFiniteEnd ? b : 0u;
 }
 
+// b x + ib y, each product and the sum rounded by itself (no fused multiply
+// and add): what the stored states are made of is the same, bit for bit, as
+// separate fp32 operations in any program give. A moment that came out one
+// bit off would now and then round to the other code, and a code that heads
+// its block moves the block's next scale by a whole step.
+__device__ __forceinline__ float blend(float b, float x, float ib, float y) {
+#pragma clang fp contract(off)
+  const float p = b * x, q = ib * y;
+  return p + q;
+}
+
 // ------------------------------------------------------------ update
 // One item: 4096 elements of one tensor, 256 threads. Sixteen lanes share a
 // 128-element block, lane l owning its 4-element chunks l and l + 16, so each
@@ -259,9 +270,9 @@ __device__ __forceinline__ void update_item(const AdamTensor &t, uint32_t chunk,
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float x = g[e] * gs;
-      m[e] = fmaf(s.b1, m[e], s.ib1 * x);
+      m[e] = blend(s.b1, m[e], s.ib1, x);
       if (Bits == 8) v[e] *= v[e];
-      v[e] = fmaf(s.b2, v[e], s.ib2 * (x * x));
+      v[e] = blend(s.b2, v[e], s.ib2, x * x);
       const float root = sqrtf(v[e]);
       const float u = m[e] / fmaf(root, s.inv_bias2, s.eps);
       p[e] = fmaf(-rate, u, p[e] * decay);

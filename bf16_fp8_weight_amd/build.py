@@ -17,7 +17,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libwt.so")
 
 SOURCES = ["plan.cpp", "schedule.cpp", "host_api.cpp", "runtime.cpp", "prep_kernels.hip", "progress.hip", "act_quant.hip",
-           "adamw.cpp", "adamw.hip"]
+           "adamw.cpp", "adamw.hip", "router.hip", "dispatch.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

@@ -1,0 +1,40 @@
+// wave.h -- reductions over a 64-lane wavefront by DPP. Every lane takes part
+// (all 64 must be active); the result is uniform. The order of a sum is fixed.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+namespace wt {
+
+template <int Ctrl, int RowMask>
+__device__ __forceinline__ float dpp_f32(float old, float x) {
+  return __int_as_float(
+      __builtin_amdgcn_update_dpp(__float_as_int(old), __float_as_int(x), Ctrl, RowMask, 0xF, false));
+}
+
+__device__ __forceinline__ float lane63(float x) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 63));
+}
+
+// A NaN takes no part in the maximum (of a number and a NaN the number wins).
+__device__ __forceinline__ float wave_max(float m) {
+  m = fmaxf(m, dpp_f32<0x0B1, 0xF>(m, m));  // quad_perm [1,0,3,2]
+  m = fmaxf(m, dpp_f32<0x04E, 0xF>(m, m));  // quad_perm [2,3,0,1]
+  m = fmaxf(m, dpp_f32<0x141, 0xF>(m, m));  // row_half_mirror
+  m = fmaxf(m, dpp_f32<0x140, 0xF>(m, m));  // row_mirror: every row of 16 has its maximum
+  m = fmaxf(m, dpp_f32<0x142, 0xA>(m, m));  // rows 1 and 3 take in rows 0 and 2
+  m = fmaxf(m, dpp_f32<0x143, 0xC>(m, m));  // rows 2 and 3 take in row 1
+  return lane63(m);
+}
+
+__device__ __forceinline__ float wave_sum(float x) {
+  x += dpp_f32<0x0B1, 0xF>(0.0f, x);
+  x += dpp_f32<0x04E, 0xF>(0.0f, x);
+  x += dpp_f32<0x141, 0xF>(0.0f, x);
+  x += dpp_f32<0x140, 0xF>(0.0f, x);
+  x += dpp_f32<0x142, 0xA>(0.0f, x);
+  x += dpp_f32<0x143, 0xC>(0.0f, x);
+  return lane63(x);
+}
+
+}  // namespace wt

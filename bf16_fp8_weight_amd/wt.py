@@ -28,6 +28,8 @@ WT_LOAD_AUTO, WT_LOAD_PLAIN, WT_LOAD_STREAM = range(3)
 WT_GROUP_AUTO, WT_GROUP_SINGLE, WT_GROUP_PAIR = range(3)
 WT_DT_F32 = 0
 WT_DT_BF16 = 1
+WT_SCORE_SIGMOID = 0
+WT_SCORE_SOFTMAX = 1
 
 EXPORTS = [
     "wt_plan_options_init", "wt_plan_check", "wt_plan_schedule", "wt_plan_create", "wt_prepare",
@@ -38,6 +40,8 @@ EXPORTS = [
     "wt_plan_create_noalloc",
     "wt_adamw_options_init", "wt_adamw_hyper_init", "wt_adamw_check", "wt_adamw_create", "wt_adamw_step",
     "wt_adamw_get_info", "wt_adamw_destroy",
+    "wt_router_desc_init", "wt_router_workspace_bytes", "wt_router_forward", "wt_router_backward",
+    "wt_dispatch_workspace_bytes", "wt_dispatch_rows",
 ]
 
 
@@ -115,6 +119,24 @@ class wt_dst_meta(ctypes.Structure):
 
 class wt_schedule_options(ctypes.Structure):
     _fields_ = [("align", ctypes.c_uint64), ("n_sources", ctypes.c_int32), ("reserved", ctypes.c_int32 * 5)]
+
+
+class wt_router_desc(ctypes.Structure):
+    _fields_ = [
+        ("n_tokens", ctypes.c_int64),
+        ("n_experts", ctypes.c_int32),
+        ("top_k", ctypes.c_int32),
+        ("logits", ctypes.c_void_p),
+        ("logits_stride", ctypes.c_int64),
+        ("logits_dtype", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("normalize", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("bias", ctypes.c_void_p),
+        ("seq_offsets", ctypes.c_void_p),
+        ("n_seqs", ctypes.c_int32),
+        ("balance_coef", ctypes.c_float),
+    ]
 
 
 class wt_adamw_tensor(ctypes.Structure):
@@ -197,6 +219,18 @@ def _load() -> ctypes.CDLL:
     L.wt_plan_task_unit.argtypes = [vp, sz, P(i32)]
     L.wt_quantize_act_b128.restype = ctypes.c_int
     L.wt_quantize_act_b128.argtypes = [vp, i64, i64, i64, vp, i64, vp, i64, vp, i64, vp]
+    L.wt_router_desc_init.restype = None
+    L.wt_router_desc_init.argtypes = [P(wt_router_desc)]
+    L.wt_router_workspace_bytes.restype = ctypes.c_int
+    L.wt_router_workspace_bytes.argtypes = [P(wt_router_desc), P(sz)]
+    L.wt_router_forward.restype = ctypes.c_int
+    L.wt_router_forward.argtypes = [P(wt_router_desc), vp, vp, vp, vp, vp, vp, sz, vp]
+    L.wt_router_backward.restype = ctypes.c_int
+    L.wt_router_backward.argtypes = [P(wt_router_desc), vp, vp, vp, vp, vp, i64, vp]
+    L.wt_dispatch_workspace_bytes.restype = ctypes.c_int
+    L.wt_dispatch_workspace_bytes.argtypes = [i64, i32, i32, P(sz)]
+    L.wt_dispatch_rows.restype = ctypes.c_int
+    L.wt_dispatch_rows.argtypes = [vp, i64, i32, i32, i32, i64, vp, vp, vp, vp, vp, sz, vp]
     L.wt_adamw_options_init.restype = None
     L.wt_adamw_options_init.argtypes = [P(wt_adamw_options)]
     L.wt_adamw_hyper_init.restype = None
@@ -442,6 +476,46 @@ class Schedule:
             self.close()
         except Exception:
             pass
+
+
+# ------------------------------------------------------------- expert router
+# Addresses as integers (0 = NULL); see include/wt.h.
+def wt_router_desc_init() -> wt_router_desc:
+    d = wt_router_desc()
+    lib.wt_router_desc_init(ctypes.byref(d))
+    return d
+
+
+def wt_router_workspace_bytes(desc: wt_router_desc) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib.wt_router_workspace_bytes(ctypes.byref(desc), ctypes.byref(n)))
+    return n.value
+
+
+def wt_router_forward(desc: wt_router_desc, index: int, weight: int, counts: int, seq_counts: int, loss: int,
+                      workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    _check(lib.wt_router_forward(ctypes.byref(desc), index or None, weight or None, counts or None,
+                                 seq_counts or None, loss or None, workspace or None, workspace_bytes, stream or None))
+
+
+def wt_router_backward(desc: wt_router_desc, index: int, seq_counts: int, dweight: int, dloss: int, dlogits: int,
+                       dlogits_stride: int, stream: int = 0) -> None:
+    _check(lib.wt_router_backward(ctypes.byref(desc), index or None, seq_counts or None, dweight or None,
+                                  dloss or None, dlogits or None, dlogits_stride, stream or None))
+
+
+def wt_dispatch_workspace_bytes(n_tokens: int, top_k: int, n_experts: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib.wt_dispatch_workspace_bytes(n_tokens, top_k, n_experts, ctypes.byref(n)))
+    return n.value
+
+
+def wt_dispatch_rows(index: int, n_tokens: int, top_k: int, n_experts: int, row_align: int, n_rows: int,
+                     row_token: int, pair_row: int, offsets: int, counts: int, workspace: int, workspace_bytes: int,
+                     stream: int = 0) -> None:
+    _check(lib.wt_dispatch_rows(index or None, n_tokens, top_k, n_experts, row_align, n_rows, row_token or None,
+                                pair_row or None, offsets or None, counts or None, workspace or None, workspace_bytes,
+                                stream or None))
 
 
 # ------------------------------------------------------------- optimizer step

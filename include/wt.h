@@ -404,6 +404,108 @@ wt_status wt_quantize_act_b128(const void *x, int64_t n_rows, int64_t cols, int6
                                const int32_t *row_index, int64_t n_out, void *q, int64_t q_row_stride,
                                void *scales, int64_t scale_row_stride, void *stream);
 
+/* Element types of gradients and router logits. */
+enum { WT_DT_F32 = 0, WT_DT_BF16 = 1 };
+
+/* ---- Expert router: selection, per-expert counts and the balance loss ----
+ * What decides where a token's activations are dispatched ("Enabling
+ * trillion-parameter models on AWS EFA", dispatch/combine evaluation: each
+ * token goes to its top-k experts) and, in training, the loss that keeps the
+ * experts evenly used, with the gradient of both.
+ *
+ * For token t with logits x_e (fp32 or BF16, computed in fp32):
+ *   score s_e = 1 / (1 + exp(-x_e))   (WT_SCORE_SIGMOID)
+ *             = exp(x_e) / sum_j exp(x_j)   (WT_SCORE_SOFTMAX)
+ *   selected: the top_k experts by s_e + bias_e (by x_e without a bias), in
+ *     falling order, ties to the lower index. Near-ties are decided in fp64.
+ *   weight_k = scale s_k, with `normalize` scale s_k / (sum over the selected
+ *     s + 1e-20). The bias takes part in the selection alone.
+ *   probability p_e = s_e (softmax), s_e / (sum_j s_j + 1e-20) (sigmoid)
+ * An expert whose logit is -infinity or NaN is never selected (a way to switch
+ * experts off); where fewer than top_k are left, the remaining places hold
+ * index -1 and weight 0. A token with no expert left has probabilities 0. A
+ * NaN logit still reaches the loss as NaN, and with softmax the weights (with
+ * softmax and a bias no key of such a token is a number, and none is selected).
+ *
+ * Sequences: seq_offsets holds n_seqs + 1 token numbers, rising from >= 0 to
+ * <= n_tokens; sequence q is the tokens [seq_offsets[q], seq_offsets[q + 1]).
+ * Tokens before the first and behind the last sequence are padding: index -1,
+ * weight 0, gradient 0, counted nowhere. NULL: one sequence of all tokens
+ * (n_seqs = 1). With T_q tokens and c_{q,e} selections of expert e in sequence q,
+ *   loss = balance_coef / n_seqs * sum_q sum_e f_{q,e} P_{q,e},
+ *   f_{q,e} = n_experts c_{q,e} / (top_k T_q), P_{q,e} = mean over q of p_e
+ * (an empty sequence adds 0). Offsets that fall or leave [0, n_tokens] give
+ * meaningless results but no access outside the arrays. Sums run in a fixed
+ * order: a call repeats bit for bit. */
+enum { WT_SCORE_SIGMOID = 0, WT_SCORE_SOFTMAX = 1 };
+
+typedef struct wt_router_desc {
+  int64_t n_tokens;       /* 0 <= n_tokens < 2^31 / top_k */
+  int32_t n_experts;      /* 1 .. 1024 */
+  int32_t top_k;          /* 1 .. min(n_experts, 32) */
+  const void *logits;     /* n_tokens rows, device */
+  int64_t logits_stride;  /* elements from row to row, >= n_experts */
+  int32_t logits_dtype;   /* WT_DT_F32 or WT_DT_BF16 */
+  int32_t score;
+  int32_t normalize;      /* 0 or 1 */
+  float scale;            /* of the weights; finite */
+  const float *bias;      /* n_experts, or NULL */
+  const int32_t *seq_offsets; /* n_seqs + 1, or NULL */
+  int32_t n_seqs;         /* 1 .. 2^20 */
+  float balance_coef;     /* finite */
+} wt_router_desc;
+
+/* Zeroes, then top_k = n_seqs = 1 and scale = 1. */
+void wt_router_desc_init(wt_router_desc *desc);
+
+/* Bytes of workspace wt_router_forward needs (16-byte aligned device memory).
+ * It need not be cleared; calls that may run at the same time need one each. */
+wt_status wt_router_workspace_bytes(const wt_router_desc *desc, size_t *bytes);
+
+/* index [n_tokens x top_k] int32 and weight [n_tokens x top_k] fp32 are dense;
+ * counts [n_experts] and seq_counts [n_seqs x n_experts] int32 receive the
+ * selections per expert over all sequences and per sequence; loss one fp32.
+ * counts may be NULL. Errors as for wt_quantize_act_b128; WT_E_RANGE if the
+ * workspace is too small. */
+wt_status wt_router_forward(const wt_router_desc *desc, int32_t *index, float *weight, int32_t *counts,
+                            int32_t *seq_counts, float *loss, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gradient of <dweight, weight> + dloss * loss with respect to the logits
+ * (counts and selection are constants of it). index and seq_counts as
+ * wt_router_forward wrote them (an index outside [0, n_experts) counts as -1;
+ * an expert twice in a row adds up); dweight [n_tokens x top_k] fp32, NULL: no
+ * gradient of the weights; dloss one fp32 on the device, NULL: no gradient of
+ * the loss (seq_counts may then be NULL). dlogits: n_tokens rows of n_experts
+ * values of logits_dtype, dlogits_stride elements apart; it may be the logits'
+ * own memory when the strides agree. */
+wt_status wt_router_backward(const wt_router_desc *desc, const int32_t *index, const int32_t *seq_counts,
+                             const float *dweight, const float *dloss, void *dlogits, int64_t dlogits_stride,
+                             void *stream);
+
+/* ---- Rows of a dispatch ----
+ * Groups token copies by expert: the row_index that wt_quantize_act_b128
+ * gathers by (same page: the sender shuffles tokens into send buffers so that
+ * each peer receives one write), and where each copy went.
+ *
+ * index: [n_tokens x top_k] int32 experts as wt_router_forward writes them;
+ *   values outside [0, n_experts) are no copy.
+ * Expert e's copies take the rows [offsets[e], offsets[e] + counts[e]) in the
+ * order of (token, place); offsets[e + 1] = offsets[e] + counts[e] rounded up
+ * to a multiple of row_align, offsets[0] = 0.
+ * row_token [n_rows] int32: the token of each row, -1 for rows that hold none
+ *   (padding to row_align, and everything from offsets[n_experts] on). n_rows
+ *   = n_tokens top_k + min(n_experts, n_tokens top_k) (row_align - 1) always
+ *   suffices; copies whose row is >= n_rows are dropped.
+ * pair_row [n_tokens x top_k] int32: each copy's row, -1 for none or dropped.
+ * offsets [n_experts + 1] and counts [n_experts] int32 (not cut by n_rows).
+ * row_token, pair_row and counts may be NULL. n_tokens top_k < 2^31 and the
+ * last offset must stay below 2^31 (n_tokens top_k + n_experts (row_align - 1)
+ * < 2^31); n_experts 1 .. 1024, row_align 1 .. 4096. */
+wt_status wt_dispatch_workspace_bytes(int64_t n_tokens, int32_t top_k, int32_t n_experts, size_t *bytes);
+wt_status wt_dispatch_rows(const int32_t *index, int64_t n_tokens, int32_t top_k, int32_t n_experts,
+                           int32_t row_align, int64_t n_rows, int32_t *row_token, int32_t *pair_row,
+                           int32_t *offsets, int32_t *counts, void *workspace, size_t workspace_bytes, void *stream);
+
 /* ---- AdamW over many parameter shards ----
  * The optimizer step that produces what wt_prepare transfers ("Weight transfer
  * for RL post-training in under 2 seconds", section "High-level workflow":
@@ -447,9 +549,6 @@ wt_status wt_quantize_act_b128(const void *x, int64_t n_rows, int64_t cols, int6
  * w * 0x9E3779B9. (k0, k1) are the low and high half of z = seed +
  * t * 0x9E3779B97F4A7C15; z ^= z >> 32; z *= 0x6A09E667F3BCC909; z ^= z >> 29;
  * z *= 0xBB67AE8584CAA73B; z ^= z >> 32 (64-bit). */
-
-/* Element types of gradients and router logits. */
-enum { WT_DT_F32 = 0, WT_DT_BF16 = 1 };
 
 /* One parameter shard: n consecutive elements (n may be 0). Device memory;
  * every range the step writes must be disjoint from every other range of the

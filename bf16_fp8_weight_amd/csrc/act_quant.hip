@@ -16,6 +16,7 @@
 #include <hip/hip_runtime.h>
 
 #include "fp8_math.h"
+#include "wave.h"
 #include "wt_internal.h"
 
 namespace wt {

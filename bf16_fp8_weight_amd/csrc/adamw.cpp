@@ -36,7 +36,8 @@ AdamOffsets adamw_offsets(const AdamLayout &L) {
   AdamOffsets o{};
   o.tensors = 0;
   o.items = align256(o.tensors + L.tensors.size() * sizeof(AdamTensor));
-  o.partials = align256(o.items + L.items.size() * sizeof(AdamItem));
+  o.grads = align256(o.items + L.items.size() * sizeof(AdamItem));
+  o.partials = align256(o.grads + L.grads.size() * sizeof(AdamGradItem));
   o.norm = align256(o.partials + kAdamNormGrid * sizeof(double));
   o.bytes = align256(o.norm + sizeof(AdamNorm));
   return o;
@@ -126,7 +127,11 @@ wt_status build_adamw(const wt_adamw_tensor *t, size_t n, const wt_adamw_options
       return WT_E_INVAL;
     }
     const uint32_t k = (uint32_t)L->tensors.size();
-    for (uint64_t c = 0; c < (e + kAdamItem - 1) / kAdamItem; ++c) L->items.push_back({k, (uint32_t)c});
+    for (uint64_t c = 0; c < (e + kAdamItem - 1) / kAdamItem; ++c) {
+      const uint64_t first = c * kAdamItem;
+      L->items.push_back({k, (uint32_t)c});
+      L->grads.push_back({d.grad + gsize * first, (uint32_t)std::min<uint64_t>(kAdamItem, e - first), d.flags});
+    }
     L->tensors.push_back(d);
     L->info.n_elements += a.n;
   }

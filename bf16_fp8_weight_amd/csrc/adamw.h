@@ -12,8 +12,11 @@
 namespace wt {
 
 constexpr int kAdamBlock = 128;   // elements that share one scale of an 8-bit state
-constexpr int kAdamItem = 4096;   // elements of one work item (one workgroup)
-constexpr int kAdamNormGrid = 1024;  // most workgroups of the norm kernel (one partial sum each)
+#ifndef ADAM_ITEM
+#define ADAM_ITEM 2048
+#endif
+constexpr int kAdamItem = ADAM_ITEM;   // elements of one work item (one workgroup)
+constexpr int kAdamNormGrid = 2048;  // most workgroups of the norm kernel (one partial sum each)
 
 enum : uint32_t {
   kAdamGradBf16 = 1,
@@ -39,10 +42,17 @@ struct AdamItem {
   uint32_t chunk;
 };
 
+// The same elements as the norm kernel reads them, address resolved.
+struct AdamGradItem {
+  uint64_t grad;   // address of the item's first gradient
+  uint32_t count;  // elements
+  uint32_t flags;  // of the tensor
+};
+
 // The step's scalars as the kernels use them.
 struct AdamScalars {
-  double lr;         // learning rate
-  double lr_bias1;   // lr / (1 - beta1^t)
+  float lr;          // learning rate
+  float lr_bias1;    // lr / (1 - beta1^t)
   float b1, ib1;     // beta1, 1 - beta1
   float b2, ib2;
   float inv_bias2;   // 1 / sqrt(1 - beta2^t)
@@ -54,20 +64,20 @@ struct AdamScalars {
 struct AdamNorm {
   float clip;
   uint32_t skip;  // the norm is not finite: the step changes nothing
-  uint32_t count; // workgroups of the norm kernel that have finished (0 between steps)
-  uint32_t pad;
+  uint32_t pad[2];
 };
 
 struct AdamLayout {
   std::vector<AdamTensor> tensors;  // those with elements
   std::vector<AdamItem> items;
+  std::vector<AdamGradItem> grads;  // one per item
   int32_t state_bits = 32;
   wt_adamw_info info{};
 };
 
 // Byte offsets of the parts of a handle's one device allocation.
 struct AdamOffsets {
-  uint64_t tensors, items, partials, norm, bytes;
+  uint64_t tensors, items, grads, partials, norm, bytes;
 };
 AdamOffsets adamw_offsets(const AdamLayout &L);
 

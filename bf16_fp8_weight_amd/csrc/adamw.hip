@@ -12,12 +12,44 @@
 #include "fp8_math.h"
 #include "hip_util.h"
 #include "plan.h"
+#include "wave.h"
 #include "wt.h"
 
 namespace wt {
 namespace {
 
 constexpr int kThreads = 256;
+#ifndef ADAM_NTL
+#define ADAM_NTL 1
+#endif
+#ifndef ADAM_NTS
+#define ADAM_NTS 1
+#endif
+#ifndef ADAM_SB
+#define ADAM_SB 1
+#endif
+#if ADAM_SB
+#define ADAM_BARRIER __builtin_amdgcn_sched_barrier(0)
+#else
+#define ADAM_BARRIER (void)0
+#endif
+#ifndef ADAM_WPE
+#define ADAM_WPE 1
+#endif
+typedef uint32_t adam_u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t adam_u32x2 __attribute__((ext_vector_type(2)));
+template <class T> __device__ __forceinline__ T ld_stream(uint64_t a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  if (ADAM_NTL) return __builtin_nontemporal_load((const __attribute__((address_space(1))) T *)(uintptr_t)a);
+#endif
+  return ld_global<T>(a);
+}
+template <class T> __device__ __forceinline__ void st_stream(uint64_t a, T v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  if (ADAM_NTS) { __builtin_nontemporal_store(v, (__attribute__((address_space(1))) T *)(uintptr_t)a); return; }
+#endif
+  st_global<T>(a, v);
+}
 
 // ------------------------------------------------------------ scalars
 __host__ __device__ inline double int_pow(double b, int64_t t) {
@@ -33,8 +65,8 @@ __host__ __device__ inline AdamScalars step_scalars(double lr, double beta1, dou
                                                     uint64_t seed) {
   AdamScalars s;
   const int64_t t = step < 1 ? 1 : step;
-  s.lr = lr;
-  s.lr_bias1 = lr / (1.0 - int_pow(beta1, t));
+  s.lr = (float)lr;
+  s.lr_bias1 = (float)(lr / (1.0 - int_pow(beta1, t)));
   s.b1 = (float)beta1;
   s.ib1 = (float)(1.0 - beta1);
   s.b2 = (float)beta2;
@@ -74,6 +106,9 @@ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
   return x ^ (x >> 16);
 }
 
+// Random word of element j of a block whose key is mix32(block ^ k0) + k1.
+__device__ __forceinline__ uint32_t random_word(uint32_t key, uint32_t j) { return mix32(key + j * 0x9E3779B9u); }
+
 // ------------------------------------------------------------ element access
 // Four elements at index i of an array, of which those below `left` exist
 // (left >= 4 when Full). Vector: the array's chunks start at the alignment of
@@ -82,8 +117,8 @@ template <bool Full>
 __device__ __forceinline__ void load_f32(uint64_t a, int64_t i, int64_t left, bool vec, float x[4]) {
   a += 4ull * (uint64_t)i;
   if (Full || (vec && left >= 4)) {
-    const float4 v = ld_global<float4>(a);
-    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    const adam_u32x4 v = ld_stream<adam_u32x4>(a);
+    x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
     return;
   }
 #pragma unroll
@@ -94,7 +129,8 @@ template <bool Full>
 __device__ __forceinline__ void store_f32(uint64_t a, int64_t i, int64_t left, bool vec, const float x[4]) {
   a += 4ull * (uint64_t)i;
   if (Full || (vec && left >= 4)) {
-    st_global<float4>(a, make_float4(x[0], x[1], x[2], x[3]));
+    const adam_u32x4 v = {__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])};
+    st_stream<adam_u32x4>(a, v);
     return;
   }
 #pragma unroll
@@ -106,7 +142,7 @@ template <bool Full>
 __device__ __forceinline__ void load_bf16(uint64_t a, int64_t i, int64_t left, bool vec, float x[4]) {
   a += 2ull * (uint64_t)i;
   if (Full || (vec && left >= 4)) {
-    const uint2 v = ld_global<uint2>(a);
+    const adam_u32x2 v = ld_stream<adam_u32x2>(a);
     x[0] = bf16_lo(v.x), x[1] = bf16_hi(v.x), x[2] = bf16_lo(v.y), x[3] = bf16_hi(v.y);
     return;
   }
@@ -118,7 +154,8 @@ template <bool Full>
 __device__ __forceinline__ void store_bf16(uint64_t a, int64_t i, int64_t left, bool vec, const uint32_t h[4]) {
   a += 2ull * (uint64_t)i;
   if (Full || (vec && left >= 4)) {
-    st_global<uint2>(a, make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16));
+    const adam_u32x2 v = {h[0] | h[1] << 16, h[2] | h[3] << 16};
+    st_stream<adam_u32x2>(a, v);
     return;
   }
 #pragma unroll
@@ -129,7 +166,7 @@ __device__ __forceinline__ void store_bf16(uint64_t a, int64_t i, int64_t left, 
 template <bool Full>
 __device__ __forceinline__ uint32_t load_codes(uint64_t a, int64_t i, int64_t left, bool vec) {
   a += (uint64_t)i;
-  if (Full || (vec && left >= 4)) return ld_global<uint32_t>(a);
+  if (Full || (vec && left >= 4)) return ld_stream<uint32_t>(a);
   uint32_t w = 0;
 #pragma unroll
   for (int e = 0; e < 4; ++e)
@@ -141,7 +178,7 @@ template <bool Full>
 __device__ __forceinline__ void store_codes(uint64_t a, int64_t i, int64_t left, bool vec, uint32_t w) {
   a += (uint64_t)i;
   if (Full || (vec && left >= 4)) {
-    st_global<uint32_t>(a, w);
+    st_stream<uint32_t>(a, w);
     return;
   }
 #pragma unroll
@@ -172,33 +209,62 @@ __device__ __forceinline__ uint32_t bf16_random(float x, uint32_t r16) {
 constexpr uint32_t kFiniteEnd = 0x7F800000u;  // magnitude bits from here up: infinity, NaN
 constexpr float kTinyAmax = 0x1p-100f;        // below: the block is held as zeros
 
-// Scale of a block from its amax bits, and the factor x -> code units.
+// Square root, correctly rounded for x in [2^-100, 2^127) (equal to sqrtf on
+// every mantissa of two binades, tests compare the states it makes bit for
+// bit), one bit off at most below; NaN for 0 and for subnormal x, which the
+// caller's slow path takes. Five instructions against sqrtf's seventeen.
+__device__ __forceinline__ float fast_sqrt(float x) {
+  const float y = __builtin_amdgcn_rsqf(x);
+  const float g = x * y;
+  return fmaf(fmaf(-g, g, x), 0.5f * y, g);
+}
+
+// Magnitude bits from which a block takes the slow path: 2^125 and more
+// (448 / amax is near the end of the normal range), infinity, NaN.
+constexpr uint32_t kPlainEnd = 0x7E000000u;
+
+// Scale of a block, amax / 448, and the factor x -> code units, 448 / amax,
+// both correctly rounded: an approximate reciprocal (exact for the constant)
+// and its residual, after Markstein. Equal to IEEE division on every mantissa
+// for amax in [2^-100, 2^125).
 __device__ __forceinline__ void state_scale(uint32_t amax_bits, float *scale, float *inv) {
-  const float amax = __uint_as_float(amax_bits);
-  const bool live = amax >= kTinyAmax;
-  *scale = live ? amax / 448.0f : 1.0f;
-  *inv = live ? 448.0f / amax : 0.0f;
+  const float a = __uint_as_float(amax_bits);
+  const bool live = a >= kTinyAmax;
+  constexpr float r448 = 1.0f / 448.0f;
+  const float s0 = a * r448;
+  const float s = fmaf(fmaf(-s0, 448.0f, a), r448, s0);
+  float r = __builtin_amdgcn_rcpf(a);
+  r = fmaf(fmaf(-a, r, 1.0f), r, r);
+  const float i0 = 448.0f * r;
+  const float i = fmaf(fmaf(-i0, a, 448.0f), r, i0);
+  *scale = live ? s : 1.0f;
+  *inv = live ? i : 0.0f;
+}
+
+__device__ __forceinline__ void state_scale_slow(uint32_t amax_bits, float *scale, float *inv) {
+  const float a = __uint_as_float(amax_bits);
+  const bool live = a >= kTinyAmax;
+  *scale = live ? a / 448.0f : 1.0f;
+  *inv = live ? 448.0f / a : 0.0f;
 }
 
 // Four values as E4M3 codes: |x| inv + rho rounded down in units of the
 // format. v_cvt_sr_fp8_f32 adds the top 20 bits of its random operand below
 // the kept mantissa bits and cuts, subnormal codes included (equal to the
-// definition on 4.2 M random values over the whole range); it does not
-// saturate, so the value is cut at 448 first.
-template <bool Root>
+// definition on 4.2 M random values over the whole range). It does not
+// saturate, and need not: |x| inv exceeds 448 by two roundings at most, two
+// units of those 20 bits, and with 16 random bits the sum stays below the
+// next code. Root: a positive root never rounds to zero.
+template <bool Root, bool Slow>
 __device__ __forceinline__ uint32_t encode4(const float x[4], float inv, const uint32_t w[4]) {
   int q = 0;
   float y[4];
   uint32_t bad = 0;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    if (Root) {
-      y[e] = fminf(x[e] * inv, 448.0f);
-      if (x[e] > 0.0f && inv > 0.0f) y[e] = fmaxf(y[e], 0x1p-9f);
-    } else {
-      y[e] = __builtin_amdgcn_fmed3f(x[e] * inv, -448.0f, 448.0f);
-    }
-    bad |= (__float_as_uint(x[e]) & 0x7FFFFFFFu) >= kFiniteEnd ? 0xFFu << (8 * e) : 0u;
+    y[e] = x[e] * inv;
+    if (Root && (!Slow || (x[e] > 0.0f && inv > 0.0f))) y[e] = fmaxf(y[e], 0x1p-9f);
+    if (Slow && (__float_as_uint(x[e]) & 0x7FFFFFFFu) >= kFiniteEnd) bad |= 0xFFu << (8 * e);
   }
 #define WT_RND(e) (int)(Root ? w[e] & 0xFFFF0000u : w[e] << 16)
   q = __builtin_amdgcn_cvt_sr_fp8_f32(y[0], WT_RND(0), q, 0);
@@ -235,8 +301,8 @@ __device__ __forceinline__ void update_item(const AdamTensor &t, uint32_t chunk,
   const uint32_t tid = threadIdx.x, l = tid & 15;
   const bool vec = t.flags & kAdamVector;
   const bool gbf = t.flags & kAdamGradBf16, has_master = t.flags & kAdamMaster, has_param = t.flags & kAdamParam;
-  const float decay = (float)(1.0 - s.lr * (double)t.lr_mul * (double)t.weight_decay);
-  const float rate = (float)(s.lr_bias1 * (double)t.lr_mul);
+  const float decay = fmaf(-(s.lr * t.lr_mul), t.weight_decay, 1.0f);
+  const float rate = s.lr_bias1 * t.lr_mul;
 #pragma unroll
   for (int it = 0; it < kAdamItem / (kThreads / 16 * kAdamBlock); ++it) {
     const uint32_t b = chunk * (kAdamItem / kAdamBlock) + (uint32_t)it * (kThreads / 16) + (tid >> 4);
@@ -266,6 +332,8 @@ __device__ __forceinline__ void update_item(const AdamTensor &t, uint32_t chunk,
         decode4(load_codes<Full>(t.v, i, left, vec), sv, v + 4 * c);
       }
     }
+    // moments and the root of the second
+    float root[8];
     uint32_t am = 0, av = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -273,59 +341,86 @@ __device__ __forceinline__ void update_item(const AdamTensor &t, uint32_t chunk,
       m[e] = blend(s.b1, m[e], s.ib1, x);
       if (Bits == 8) v[e] *= v[e];
       v[e] = blend(s.b2, v[e], s.ib2, x * x);
-      const float root = sqrtf(v[e]);
-      const float u = m[e] / fmaf(root, s.inv_bias2, s.eps);
-      p[e] = fmaf(-rate, u, p[e] * decay);
+      root[e] = Bits == 8 ? fast_sqrt(v[e]) : sqrtf(v[e]);
       if (Bits == 8) {
-        v[e] = root;
-        am = max(am, finite_bits(m[e]));
-        av = max(av, finite_bits(root));
+        am = max(am, __float_as_uint(m[e]) & 0x7FFFFFFFu);
+        av = max(av, __float_as_uint(root[e]) & 0x7FFFFFFFu);
       }
     }
-    uint32_t w[8];
-    if (Bits == 8 || !has_master) {
-      const uint32_t key = mix32((t.block0 + b) ^ s.k0) + s.k1;
+    // some lane of the wave has a zero or subnormal v, a huge value, an infinity or NaN
+    const bool slow = Bits == 8 && __any(max(am, av) >= kPlainEnd);
+    if (slow) {
+      am = av = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = mix32(key + (4 * l + 64 * (e >> 2) + (e & 3)) * 0x9E3779B9u);
+      for (int e = 0; e < 8; ++e) {
+        root[e] = sqrtf(v[e]);
+        am = max(am, finite_bits(m[e]));
+        av = max(av, finite_bits(root[e]));
+      }
+    }
+    if (Bits == 32) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        store_f32<Full>(t.m, i0 + 64 * c, t.n - i0 - 64 * c, vec, m + 4 * c);
+        store_f32<Full>(t.v, i0 + 64 * c, t.n - i0 - 64 * c, vec, v + 4 * c);
+      }
+    }
+    const uint32_t key = Bits == 8 || !has_master ? mix32((t.block0 + b) ^ s.k0) + s.k1 : 0u;
+    // parameters; 1 / d by v_rcp_f32 (one bit): d lies in the normal range, and what the update is off by is far
+    // below a rounding of p
+    ADAM_BARRIER;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int64_t i = i0 + 64 * c, left = t.n - i;
+      uint32_t h[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int k = 4 * c + e;
+        const float u = m[k] * __builtin_amdgcn_rcpf(fmaf(root[k], s.inv_bias2, s.eps));
+        p[k] = fmaf(-rate, u, p[k] * decay);
+        h[e] = has_master ? bf16_nearest(p[k]) : bf16_random(p[k], (random_word(key, 4 * l + 64 * c + e) * 0x9E3779B9u) >> 16);
+      }
+      if (has_master) store_f32<Full>(t.master, i, left, vec, p + 4 * c);
+      if (has_param) store_bf16<Full>(t.param, i, left, vec, h);
     }
     if (Bits == 8) {
       float im, iv;
       am = lanes_max<16>(am);  // every lane of the row takes part
       av = lanes_max<16>(av);
-      state_scale(am, &sm, &im);
-      state_scale(av, &sv, &iv);
+      if (!slow) {
+        state_scale(am, &sm, &im);
+        state_scale(av, &sv, &iv);
+      } else {
+        state_scale_slow(am, &sm, &im);
+        state_scale_slow(av, &sv, &iv);
+      }
       if (l == 0 && (Full || (int64_t)b * kAdamBlock < t.n)) {
         st_global<float>(t.m_scale + 4ull * b, sm);
         st_global<float>(t.v_scale + 4ull * b, sv);
       }
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
+        ADAM_BARRIER;
         const int64_t i = i0 + 64 * c, left = t.n - i;
-        store_codes<Full>(t.m, i, left, vec, encode4<false>(m + 4 * c, im, w + 4 * c));
-        store_codes<Full>(t.v, i, left, vec, encode4<true>(v + 4 * c, iv, w + 4 * c));
-      }
-    }
+        uint32_t w[4], cm, cv;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int64_t i = i0 + 64 * c, left = t.n - i;
-      if (Bits == 32) {
-        store_f32<Full>(t.m, i, left, vec, m + 4 * c);
-        store_f32<Full>(t.v, i, left, vec, v + 4 * c);
-      }
-      if (has_master) store_f32<Full>(t.master, i, left, vec, p + 4 * c);
-      if (has_param) {
-        uint32_t h[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          h[e] = has_master ? bf16_nearest(p[4 * c + e]) : bf16_random(p[4 * c + e], (w[4 * c + e] * 0x9E3779B9u) >> 16);
-        store_bf16<Full>(t.param, i, left, vec, h);
+        for (int e = 0; e < 4; ++e) w[e] = random_word(key, 4 * l + 64 * c + e);
+        if (!slow) {
+          cm = encode4<false, false>(m + 4 * c, im, w);
+          cv = encode4<true, false>(root + 4 * c, iv, w);
+        } else {
+          cm = encode4<false, true>(m + 4 * c, im, w);
+          cv = encode4<true, true>(root + 4 * c, iv, w);
+        }
+        store_codes<Full>(t.m, i, left, vec, cm);
+        store_codes<Full>(t.v, i, left, vec, cv);
       }
     }
   }
 }
 
 template <int Bits>
-__global__ void __launch_bounds__(kThreads) adamw_update_kernel(AdamArgs a) {
+__global__ void __launch_bounds__(kThreads, ADAM_WPE) adamw_update_kernel(AdamArgs a) {
   const AdamItem item = ld_table(a.items, blockIdx.x);
   const AdamTensor t = ld_table(a.tensors, item.tensor);
   float gs = a.grad_scale;
@@ -345,12 +440,12 @@ __global__ void __launch_bounds__(kThreads) adamw_update_kernel(AdamArgs a) {
 
 // ------------------------------------------------------------ norm
 template <bool Full>
-__device__ __forceinline__ float item_squares(const AdamTensor &t, uint32_t chunk) {
+__device__ __forceinline__ float item_squares(const AdamGradItem &t) {
   const bool vec = t.flags & kAdamVector, gbf = t.flags & kAdamGradBf16;
   float sum = 0.0f;
 #pragma unroll
   for (int c = 0; c < kAdamItem / (4 * kThreads); ++c) {
-    const int64_t i = (int64_t)chunk * kAdamItem + 4 * (c * kThreads + (int)threadIdx.x), left = t.n - i;
+    const int64_t i = 4 * (c * kThreads + (int)threadIdx.x), left = (int64_t)t.count - i;
     float g[4];
     if (gbf) load_bf16<Full>(t.grad, i, left, vec, g);
     else load_f32<Full>(t.grad, i, left, vec, g);
@@ -369,43 +464,39 @@ __device__ __forceinline__ double block_sum(double x, double *lds) {
   return (lds[0] + lds[1]) + (lds[2] + lds[3]);
 }
 
-// Sum of the squares of every gradient: each workgroup adds its items
-// (fp32 over a thread's 16 elements of an item, fp64 beyond), and the last
-// one to finish adds the workgroups' sums in a fixed order.
+// Sum of the squares of every gradient, per workgroup: fp32 over a thread's
+// elements of an item, fp64 beyond.
 __global__ void __launch_bounds__(kThreads)
-    adamw_norm_kernel(const AdamTensor *tensors, const AdamItem *items, uint32_t n_items, double *partials,
-                      AdamNorm *norm, float grad_scale, double max_norm, float *norm_out) {
+    adamw_norm_kernel(const AdamGradItem *items, uint32_t n_items, double *partials) {
   __shared__ double lds[4];
-  __shared__ uint32_t last;
   double sum = 0.0;
+  AdamGradItem next = blockIdx.x < n_items ? ld_table(items, blockIdx.x) : AdamGradItem{0, 0, 0};
   for (uint32_t k = blockIdx.x; k < n_items; k += gridDim.x) {
-    const AdamItem item = ld_table(items, k);
-    const AdamTensor t = ld_table(tensors, item.tensor);
-    if ((t.flags & kAdamVector) && ((int64_t)item.chunk + 1) * kAdamItem <= t.n)
-      sum += (double)item_squares<true>(t, item.chunk);
-    else
-      sum += (double)item_squares<false>(t, item.chunk);
+    const AdamGradItem t = next;
+    if (k + gridDim.x < n_items) next = ld_table(items, k + gridDim.x);
+    sum += (double)((t.flags & kAdamVector) && t.count == kAdamItem ? item_squares<true>(t) : item_squares<false>(t));
   }
   sum = block_sum(sum, lds);
-  if (threadIdx.x == 0) {
-    __hip_atomic_store(&partials[blockIdx.x], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    last = __hip_atomic_fetch_add(&norm->count, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
-  }
-  __syncthreads();
-  if (!last) return;
-  sum = 0.0;
-  for (uint32_t k = threadIdx.x; k < gridDim.x; k += kThreads)
-    sum += __hip_atomic_load(&partials[k], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (threadIdx.x == 0) partials[blockIdx.x] = sum;
+}
+
+// The norm and what follows from it, from the workgroups' sums in a fixed
+// order. A launch of its own: a counter that tells the norm kernel's last
+// workgroup cost 20 ns per workgroup, one after the other.
+__global__ void __launch_bounds__(kThreads)
+    adamw_clip_kernel(const double *partials, uint32_t n, AdamNorm *norm, float grad_scale, double max_norm,
+                      float *norm_out) {
+  __shared__ double lds[4];
+  double sum = 0.0;
+  for (uint32_t k = threadIdx.x; k < n; k += kThreads) sum += partials[k];
   sum = block_sum(sum, lds);
   if (threadIdx.x == 0) {
-    const double n = sqrt(sum) * fabs((double)grad_scale);
-    const bool finite = n <= 3.4028234663852886e38;
+    const double r = sqrt(sum) * fabs((double)grad_scale);
     double clip = 1.0;
-    if (max_norm > 0.0 && max_norm < n + 1e-6) clip = max_norm / (n + 1e-6);
+    if (max_norm > 0.0 && max_norm < r + 1e-6) clip = max_norm / (r + 1e-6);
     norm->clip = (float)clip;
-    norm->skip = finite ? 0u : 1u;
-    norm->count = 0u;
-    if (norm_out) *norm_out = (float)n;
+    norm->skip = r <= 3.4028234663852886e38 ? 0u : 1u;  // false for NaN
+    if (norm_out) *norm_out = (float)r;
   }
 }
 
@@ -477,10 +568,14 @@ wt_status create_impl(const wt_adamw_tensor *tensors, size_t n, const wt_adamw_o
   if (e == hipSuccess && !a->L.items.empty())
     e = hipMemcpy(a->mem + a->at.items, a->L.items.data(), a->L.items.size() * sizeof(AdamItem),
                   hipMemcpyHostToDevice);
+  if (e == hipSuccess && !a->L.grads.empty())
+    e = hipMemcpy(a->mem + a->at.grads, a->L.grads.data(), a->L.grads.size() * sizeof(AdamGradItem),
+                  hipMemcpyHostToDevice);
   if (e == hipSuccess) e = hipDeviceSynchronize();  // the tables are there before a step on any stream
   if (e != hipSuccess) return fail(hip_msg("device tables", e), WT_E_HIP);
   // the launch needs only their numbers from here on
   std::vector<AdamItem>().swap(a->L.items);
+  std::vector<AdamGradItem>().swap(a->L.grads);
   return WT_OK;
 }
 
@@ -506,8 +601,11 @@ wt_status step_impl(wt_adamw *a, const wt_adamw_hyper *h, hipStream_t stream) {
   if (h->max_norm > 0 || h->norm_out) {
     AdamNorm *norm = (AdamNorm *)(a->mem + a->at.norm);
     const uint32_t grid = n_items < 1 ? 1 : n_items < kAdamNormGrid ? n_items : kAdamNormGrid;
-    hipLaunchKernelGGL(adamw_norm_kernel, dim3(grid), dim3(kThreads), 0, stream, k.tensors, k.items, n_items,
-                       (double *)(a->mem + a->at.partials), norm, k.grad_scale, h->max_norm, h->norm_out);
+    double *partials = (double *)(a->mem + a->at.partials);
+    hipLaunchKernelGGL(adamw_norm_kernel, dim3(grid), dim3(kThreads), 0, stream,
+                       (const AdamGradItem *)(a->mem + a->at.grads), n_items, partials);
+    hipLaunchKernelGGL(adamw_clip_kernel, dim3(1), dim3(kThreads), 0, stream, partials, grid, norm, k.grad_scale,
+                       h->max_norm, h->norm_out);
     k.norm = norm;
   }
   if (n_items > 0) {

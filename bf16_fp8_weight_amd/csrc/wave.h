@@ -1,10 +1,25 @@
-// wave.h -- reductions over a 64-lane wavefront by DPP. Every lane takes part
-// (all 64 must be active); the result is uniform. The order of a sum is fixed.
+// wave.h -- reductions over a 64-lane wavefront or groups of its lanes by DPP.
+// Every lane of the group has to be active. The order of a sum is fixed.
 #pragma once
 
 #include <hip/hip_runtime.h>
 
+#include <cstdint>
+
 namespace wt {
+
+// Max over the L lanes of each aligned L-lane group (DPP within 16-lane rows;
+// lanes read from outside the group take no part), left in every lane.
+template <int L>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t m) {
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x0B1, 0xF, 0xF, false));  // quad_perm [1,0,3,2]
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x04E, 0xF, 0xF, false));  // quad_perm [2,3,0,1]
+  if (L >= 8) m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x141, 0xF, 0xF, false));  // row_half_mirror
+  if (L >= 16) m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x140, 0xF, 0xF, false));  // row_mirror
+  return m;
+}
+
+// Over the whole wavefront; the result is uniform.
 
 template <int Ctrl, int RowMask>
 __device__ __forceinline__ float dpp_f32(float old, float x) {

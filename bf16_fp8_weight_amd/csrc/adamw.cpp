@@ -59,6 +59,7 @@ wt_status build_adamw(const wt_adamw_tensor *t, size_t n, const wt_adamw_options
   L->state_bits = o.state_bits;
   const bool s8 = o.state_bits == 8;
   std::vector<Range> ranges;
+  const uint64_t item = (uint64_t)adam_item(o.state_bits);
   uint64_t blocks = 0, items = 0;
   for (size_t i = 0; i < n; ++i) {
     const wt_adamw_tensor &a = t[i];
@@ -121,16 +122,16 @@ wt_status build_adamw(const wt_adamw_tensor *t, size_t n, const wt_adamw_options
                      d.m % (4 * ssize) == 0 && d.v % (4 * ssize) == 0;
     if (vec) d.flags |= kAdamVector, L->info.n_vector_tensors++;
     blocks += nb;
-    items += (e + kAdamItem - 1) / kAdamItem;
+    items += (e + item - 1) / item;
     if (blocks >> 32 || items >> 31) {
       *err = at + "the table holds too many elements";
       return WT_E_INVAL;
     }
     const uint32_t k = (uint32_t)L->tensors.size();
-    for (uint64_t c = 0; c < (e + kAdamItem - 1) / kAdamItem; ++c) {
-      const uint64_t first = c * kAdamItem;
+    for (uint64_t c = 0; c < (e + item - 1) / item; ++c) {
+      const uint64_t first = c * item;
       L->items.push_back({k, (uint32_t)c});
-      L->grads.push_back({d.grad + gsize * first, (uint32_t)std::min<uint64_t>(kAdamItem, e - first), d.flags});
+      L->grads.push_back({d.grad + gsize * first, (uint32_t)std::min<uint64_t>(item, e - first), d.flags});
     }
     L->tensors.push_back(d);
     L->info.n_elements += a.n;

@@ -12,10 +12,10 @@
 namespace wt {
 
 constexpr int kAdamBlock = 128;   // elements that share one scale of an 8-bit state
-#ifndef ADAM_ITEM
-#define ADAM_ITEM 2048
-#endif
-constexpr int kAdamItem = ADAM_ITEM;   // elements of one work item (one workgroup)
+// Elements of one work item (one workgroup, eight to a thread). Measured on
+// MI355X over 176 M elements: 32-bit states 880 / 848 / 942 us with 256 / 512 /
+// 1024 threads, 8-bit states 470 / 497 us with 256 / 512 (their registers).
+constexpr int adam_item(int state_bits) { return state_bits == 32 ? 4096 : 2048; }
 constexpr int kAdamNormGrid = 2048;  // most workgroups of the norm kernel (one partial sum each)
 
 enum : uint32_t {
@@ -36,7 +36,7 @@ struct AdamTensor {
 };
 static_assert(sizeof(AdamTensor) == 80, "AdamTensor layout");
 
-// Elements [4096 chunk, +4096) of one tensor.
+// Elements [item chunk, item (chunk + 1)) of one tensor.
 struct AdamItem {
   uint32_t tensor;
   uint32_t chunk;
@@ -60,11 +60,10 @@ struct AdamScalars {
   uint32_t k0, k1;   // keys of the step's random bits
 };
 
-// Outcome of the norm kernel, read by the update kernel behind it.
+// What the update kernel takes from the norm.
 struct AdamNorm {
   float clip;
   uint32_t skip;  // the norm is not finite: the step changes nothing
-  uint32_t pad[2];
 };
 
 struct AdamLayout {

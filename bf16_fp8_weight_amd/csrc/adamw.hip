@@ -18,37 +18,29 @@
 namespace wt {
 namespace {
 
-constexpr int kThreads = 256;
-#ifndef ADAM_NTL
-#define ADAM_NTL 1
-#endif
-#ifndef ADAM_NTS
-#define ADAM_NTS 1
-#endif
-#ifndef ADAM_SB
-#define ADAM_SB 1
-#endif
-#if ADAM_SB
-#define ADAM_BARRIER __builtin_amdgcn_sched_barrier(0)
+constexpr int kThreads = 256;  // of the norm kernel
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// A step reads and writes each byte once: streaming (non-temporal) accesses.
+// Measured on MI355X over 176 M elements, plain / loads / stores / both: 32-bit
+// states 930 / 916 / 929 / 888 us, 8-bit 510 / 522 / 501 / 492 us.
+template <class T>
+__device__ __forceinline__ T ld_stream(uint64_t a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  return __builtin_nontemporal_load((gcptr<T>)(uintptr_t)a);
 #else
-#define ADAM_BARRIER (void)0
-#endif
-#ifndef ADAM_WPE
-#define ADAM_WPE 1
-#endif
-typedef uint32_t adam_u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t adam_u32x2 __attribute__((ext_vector_type(2)));
-template <class T> __device__ __forceinline__ T ld_stream(uint64_t a) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  if (ADAM_NTL) return __builtin_nontemporal_load((const __attribute__((address_space(1))) T *)(uintptr_t)a);
-#endif
   return ld_global<T>(a);
-}
-template <class T> __device__ __forceinline__ void st_stream(uint64_t a, T v) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  if (ADAM_NTS) { __builtin_nontemporal_store(v, (__attribute__((address_space(1))) T *)(uintptr_t)a); return; }
 #endif
+}
+template <class T>
+__device__ __forceinline__ void st_stream(uint64_t a, T v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_nontemporal_store(v, (gptr<T>)(uintptr_t)a);
+#else
   st_global<T>(a, v);
+#endif
 }
 
 // ------------------------------------------------------------ scalars
@@ -117,7 +109,7 @@ template <bool Full>
 __device__ __forceinline__ void load_f32(uint64_t a, int64_t i, int64_t left, bool vec, float x[4]) {
   a += 4ull * (uint64_t)i;
   if (Full || (vec && left >= 4)) {
-    const adam_u32x4 v = ld_stream<adam_u32x4>(a);
+    const u32x4 v = ld_stream<u32x4>(a);
     x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
     return;
   }
@@ -129,8 +121,8 @@ template <bool Full>
 __device__ __forceinline__ void store_f32(uint64_t a, int64_t i, int64_t left, bool vec, const float x[4]) {
   a += 4ull * (uint64_t)i;
   if (Full || (vec && left >= 4)) {
-    const adam_u32x4 v = {__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])};
-    st_stream<adam_u32x4>(a, v);
+    const u32x4 v = {__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])};
+    st_stream<u32x4>(a, v);
     return;
   }
 #pragma unroll
@@ -142,7 +134,7 @@ template <bool Full>
 __device__ __forceinline__ void load_bf16(uint64_t a, int64_t i, int64_t left, bool vec, float x[4]) {
   a += 2ull * (uint64_t)i;
   if (Full || (vec && left >= 4)) {
-    const adam_u32x2 v = ld_stream<adam_u32x2>(a);
+    const u32x2 v = ld_stream<u32x2>(a);
     x[0] = bf16_lo(v.x), x[1] = bf16_hi(v.x), x[2] = bf16_lo(v.y), x[3] = bf16_hi(v.y);
     return;
   }
@@ -154,8 +146,8 @@ template <bool Full>
 __device__ __forceinline__ void store_bf16(uint64_t a, int64_t i, int64_t left, bool vec, const uint32_t h[4]) {
   a += 2ull * (uint64_t)i;
   if (Full || (vec && left >= 4)) {
-    const adam_u32x2 v = {h[0] | h[1] << 16, h[2] | h[3] << 16};
-    st_stream<adam_u32x2>(a, v);
+    const u32x2 v = {h[0] | h[1] << 16, h[2] | h[3] << 16};
+    st_stream<u32x2>(a, v);
     return;
   }
 #pragma unroll
@@ -292,8 +284,7 @@ __device__ __forceinline__ float blend(float b, float x, float ib, float y) {
 }
 
 // ------------------------------------------------------------ update
-// One item: 4096 elements of one tensor, 256 threads. Sixteen lanes share a
-// 128-element block, lane l owning its 4-element chunks l and l + 16, so each
+// One item, eight elements to a thread. Sixteen lanes share a 128-element block, lane l owning its 4-element chunks l and l + 16, so each
 // access of a wave covers consecutive bytes (fp32 256, BF16 128, codes 64 per
 // block) and the block's amax is a DPP max over a row of 16 lanes.
 template <int Bits, bool Full>
@@ -303,124 +294,119 @@ __device__ __forceinline__ void update_item(const AdamTensor &t, uint32_t chunk,
   const bool gbf = t.flags & kAdamGradBf16, has_master = t.flags & kAdamMaster, has_param = t.flags & kAdamParam;
   const float decay = fmaf(-(s.lr * t.lr_mul), t.weight_decay, 1.0f);
   const float rate = s.lr_bias1 * t.lr_mul;
+  const uint32_t b = chunk * (adam_item(Bits) / kAdamBlock) + (tid >> 4);
+  const int64_t i0 = (int64_t)b * kAdamBlock + 4 * l;
+  float g[8], p[8], m[8], v[8], sm = 1.0f, sv = 1.0f;
 #pragma unroll
-  for (int it = 0; it < kAdamItem / (kThreads / 16 * kAdamBlock); ++it) {
-    const uint32_t b = chunk * (kAdamItem / kAdamBlock) + (uint32_t)it * (kThreads / 16) + (tid >> 4);
-    const int64_t i0 = (int64_t)b * kAdamBlock + 4 * l;
-    float g[8], p[8], m[8], v[8], sm = 1.0f, sv = 1.0f;
+  for (int c = 0; c < 2; ++c) {
+    const int64_t i = i0 + 64 * c, left = t.n - i;
+    if (gbf) load_bf16<Full>(t.grad, i, left, vec, g + 4 * c);
+    else load_f32<Full>(t.grad, i, left, vec, g + 4 * c);
+    if (has_master) load_f32<Full>(t.master, i, left, vec, p + 4 * c);
+    else load_bf16<Full>(t.param, i, left, vec, p + 4 * c);
+    if (Bits == 32) {
+      load_f32<Full>(t.m, i, left, vec, m + 4 * c);
+      load_f32<Full>(t.v, i, left, vec, v + 4 * c);
+    }
+  }
+  if (Bits == 8) {
+    if (Full || (int64_t)b * kAdamBlock < t.n) {
+      sm = ld_global<float>(t.m_scale + 4ull * b);
+      sv = ld_global<float>(t.v_scale + 4ull * b);
+    }
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int64_t i = i0 + 64 * c, left = t.n - i;
-      if (gbf) load_bf16<Full>(t.grad, i, left, vec, g + 4 * c);
-      else load_f32<Full>(t.grad, i, left, vec, g + 4 * c);
-      if (has_master) load_f32<Full>(t.master, i, left, vec, p + 4 * c);
-      else load_bf16<Full>(t.param, i, left, vec, p + 4 * c);
-      if (Bits == 32) {
-        load_f32<Full>(t.m, i, left, vec, m + 4 * c);
-        load_f32<Full>(t.v, i, left, vec, v + 4 * c);
-      }
+      decode4(load_codes<Full>(t.m, i, left, vec), sm, m + 4 * c);
+      decode4(load_codes<Full>(t.v, i, left, vec), sv, v + 4 * c);
     }
-    if (Bits == 8) {
-      if (Full || (int64_t)b * kAdamBlock < t.n) {
-        sm = ld_global<float>(t.m_scale + 4ull * b);
-        sv = ld_global<float>(t.v_scale + 4ull * b);
-      }
+  }
+  // moments and the root of the second
+  float root[8];
+  uint32_t am = 0, av = 0;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int64_t i = i0 + 64 * c, left = t.n - i;
-        decode4(load_codes<Full>(t.m, i, left, vec), sm, m + 4 * c);
-        decode4(load_codes<Full>(t.v, i, left, vec), sv, v + 4 * c);
-      }
+  for (int e = 0; e < 8; ++e) {
+    const float x = g[e] * gs;
+    m[e] = blend(s.b1, m[e], s.ib1, x);
+    if (Bits == 8) v[e] *= v[e];
+    v[e] = blend(s.b2, v[e], s.ib2, x * x);
+    root[e] = Bits == 8 ? fast_sqrt(v[e]) : sqrtf(v[e]);
+    if (Bits == 8) {
+      am = max(am, __float_as_uint(m[e]) & 0x7FFFFFFFu);
+      av = max(av, __float_as_uint(root[e]) & 0x7FFFFFFFu);
     }
-    // moments and the root of the second
-    float root[8];
-    uint32_t am = 0, av = 0;
+  }
+  // some lane of the wave has a zero or subnormal v, a huge value, an infinity or NaN
+  const bool slow = Bits == 8 && __any(max(am, av) >= kPlainEnd);
+  if (slow) {
+    am = av = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float x = g[e] * gs;
-      m[e] = blend(s.b1, m[e], s.ib1, x);
-      if (Bits == 8) v[e] *= v[e];
-      v[e] = blend(s.b2, v[e], s.ib2, x * x);
-      root[e] = Bits == 8 ? fast_sqrt(v[e]) : sqrtf(v[e]);
-      if (Bits == 8) {
-        am = max(am, __float_as_uint(m[e]) & 0x7FFFFFFFu);
-        av = max(av, __float_as_uint(root[e]) & 0x7FFFFFFFu);
-      }
+      root[e] = sqrtf(v[e]);
+      am = max(am, finite_bits(m[e]));
+      av = max(av, finite_bits(root[e]));
     }
-    // some lane of the wave has a zero or subnormal v, a huge value, an infinity or NaN
-    const bool slow = Bits == 8 && __any(max(am, av) >= kPlainEnd);
-    if (slow) {
-      am = av = 0;
+  }
+  if (Bits == 32) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        root[e] = sqrtf(v[e]);
-        am = max(am, finite_bits(m[e]));
-        av = max(av, finite_bits(root[e]));
-      }
+    for (int c = 0; c < 2; ++c) {
+      store_f32<Full>(t.m, i0 + 64 * c, t.n - i0 - 64 * c, vec, m + 4 * c);
+      store_f32<Full>(t.v, i0 + 64 * c, t.n - i0 - 64 * c, vec, v + 4 * c);
     }
-    if (Bits == 32) {
+  }
+  const uint32_t key = Bits == 8 || !has_master ? mix32((t.block0 + b) ^ s.k0) + s.k1 : 0u;
+  // parameters; 1 / d by v_rcp_f32 (one bit): d lies in the normal range, and what the update is off by is far
+  // below a rounding of p
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        store_f32<Full>(t.m, i0 + 64 * c, t.n - i0 - 64 * c, vec, m + 4 * c);
-        store_f32<Full>(t.v, i0 + 64 * c, t.n - i0 - 64 * c, vec, v + 4 * c);
-      }
+  for (int c = 0; c < 2; ++c) {
+    const int64_t i = i0 + 64 * c, left = t.n - i;
+    uint32_t h[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int k = 4 * c + e;
+      const float u = m[k] * __builtin_amdgcn_rcpf(fmaf(root[k], s.inv_bias2, s.eps));
+      p[k] = fmaf(-rate, u, p[k] * decay);
+      h[e] = has_master ? bf16_nearest(p[k]) : bf16_random(p[k], (random_word(key, 4 * l + 64 * c + e) * 0x9E3779B9u) >> 16);
     }
-    const uint32_t key = Bits == 8 || !has_master ? mix32((t.block0 + b) ^ s.k0) + s.k1 : 0u;
-    // parameters; 1 / d by v_rcp_f32 (one bit): d lies in the normal range, and what the update is off by is far
-    // below a rounding of p
-    ADAM_BARRIER;
+    if (has_master) store_f32<Full>(t.master, i, left, vec, p + 4 * c);
+    if (has_param) store_bf16<Full>(t.param, i, left, vec, h);
+  }
+  if (Bits == 8) {
+    float im, iv;
+    am = lanes_max<16>(am);  // every lane of the row takes part
+    av = lanes_max<16>(av);
+    if (!slow) {
+      state_scale(am, &sm, &im);
+      state_scale(av, &sv, &iv);
+    } else {
+      state_scale_slow(am, &sm, &im);
+      state_scale_slow(av, &sv, &iv);
+    }
+    if (l == 0 && (Full || (int64_t)b * kAdamBlock < t.n)) {
+      st_global<float>(t.m_scale + 4ull * b, sm);
+      st_global<float>(t.v_scale + 4ull * b, sv);
+    }
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int64_t i = i0 + 64 * c, left = t.n - i;
-      uint32_t h[4];
+      uint32_t w[4], cm, cv;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int k = 4 * c + e;
-        const float u = m[k] * __builtin_amdgcn_rcpf(fmaf(root[k], s.inv_bias2, s.eps));
-        p[k] = fmaf(-rate, u, p[k] * decay);
-        h[e] = has_master ? bf16_nearest(p[k]) : bf16_random(p[k], (random_word(key, 4 * l + 64 * c + e) * 0x9E3779B9u) >> 16);
-      }
-      if (has_master) store_f32<Full>(t.master, i, left, vec, p + 4 * c);
-      if (has_param) store_bf16<Full>(t.param, i, left, vec, h);
-    }
-    if (Bits == 8) {
-      float im, iv;
-      am = lanes_max<16>(am);  // every lane of the row takes part
-      av = lanes_max<16>(av);
+      for (int e = 0; e < 4; ++e) w[e] = random_word(key, 4 * l + 64 * c + e);
       if (!slow) {
-        state_scale(am, &sm, &im);
-        state_scale(av, &sv, &iv);
+        cm = encode4<false, false>(m + 4 * c, im, w);
+        cv = encode4<true, false>(root + 4 * c, iv, w);
       } else {
-        state_scale_slow(am, &sm, &im);
-        state_scale_slow(av, &sv, &iv);
+        cm = encode4<false, true>(m + 4 * c, im, w);
+        cv = encode4<true, true>(root + 4 * c, iv, w);
       }
-      if (l == 0 && (Full || (int64_t)b * kAdamBlock < t.n)) {
-        st_global<float>(t.m_scale + 4ull * b, sm);
-        st_global<float>(t.v_scale + 4ull * b, sv);
-      }
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        ADAM_BARRIER;
-        const int64_t i = i0 + 64 * c, left = t.n - i;
-        uint32_t w[4], cm, cv;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = random_word(key, 4 * l + 64 * c + e);
-        if (!slow) {
-          cm = encode4<false, false>(m + 4 * c, im, w);
-          cv = encode4<true, false>(root + 4 * c, iv, w);
-        } else {
-          cm = encode4<false, true>(m + 4 * c, im, w);
-          cv = encode4<true, true>(root + 4 * c, iv, w);
-        }
-        store_codes<Full>(t.m, i, left, vec, cm);
-        store_codes<Full>(t.v, i, left, vec, cv);
-      }
+      store_codes<Full>(t.m, i, left, vec, cm);
+      store_codes<Full>(t.v, i, left, vec, cv);
     }
   }
 }
 
 template <int Bits>
-__global__ void __launch_bounds__(kThreads, ADAM_WPE) adamw_update_kernel(AdamArgs a) {
+__global__ void __launch_bounds__(adam_item(Bits) / 8) adamw_update_kernel(AdamArgs a) {
   const AdamItem item = ld_table(a.items, blockIdx.x);
   const AdamTensor t = ld_table(a.tensors, item.tensor);
   float gs = a.grad_scale;
@@ -432,19 +418,19 @@ __global__ void __launch_bounds__(kThreads, ADAM_WPE) adamw_update_kernel(AdamAr
   if (a.step_dev || a.lr_dev)
     s = step_scalars(a.lr_dev ? (double)*a.lr_dev : a.lr, a.beta1, a.beta2, a.eps, a.step_dev ? *a.step_dev : a.step,
                      a.seed);
-  if ((t.flags & kAdamVector) && ((int64_t)item.chunk + 1) * kAdamItem <= t.n)
+  if ((t.flags & kAdamVector) && ((int64_t)item.chunk + 1) * adam_item(Bits) <= t.n)
     update_item<Bits, true>(t, item.chunk, s, gs);
   else
     update_item<Bits, false>(t, item.chunk, s, gs);
 }
 
 // ------------------------------------------------------------ norm
-template <bool Full>
+template <int Item, bool Full>
 __device__ __forceinline__ float item_squares(const AdamGradItem &t) {
   const bool vec = t.flags & kAdamVector, gbf = t.flags & kAdamGradBf16;
   float sum = 0.0f;
 #pragma unroll
-  for (int c = 0; c < kAdamItem / (4 * kThreads); ++c) {
+  for (int c = 0; c < Item / (4 * kThreads); ++c) {
     const int64_t i = 4 * (c * kThreads + (int)threadIdx.x), left = (int64_t)t.count - i;
     float g[4];
     if (gbf) load_bf16<Full>(t.grad, i, left, vec, g);
@@ -466,6 +452,7 @@ __device__ __forceinline__ double block_sum(double x, double *lds) {
 
 // Sum of the squares of every gradient, per workgroup: fp32 over a thread's
 // elements of an item, fp64 beyond.
+template <int Item>
 __global__ void __launch_bounds__(kThreads)
     adamw_norm_kernel(const AdamGradItem *items, uint32_t n_items, double *partials) {
   __shared__ double lds[4];
@@ -474,21 +461,28 @@ __global__ void __launch_bounds__(kThreads)
   for (uint32_t k = blockIdx.x; k < n_items; k += gridDim.x) {
     const AdamGradItem t = next;
     if (k + gridDim.x < n_items) next = ld_table(items, k + gridDim.x);
-    sum += (double)((t.flags & kAdamVector) && t.count == kAdamItem ? item_squares<true>(t) : item_squares<false>(t));
+    const bool full = (t.flags & kAdamVector) && t.count == Item;
+    sum += (double)(full ? item_squares<Item, true>(t) : item_squares<Item, false>(t));
   }
   sum = block_sum(sum, lds);
   if (threadIdx.x == 0) partials[blockIdx.x] = sum;
 }
 
 // The norm and what follows from it, from the workgroups' sums in a fixed
-// order. A launch of its own: a counter that tells the norm kernel's last
-// workgroup cost 20 ns per workgroup, one after the other.
+// order. A launch of its own costs 4 us; having the norm kernel's last
+// workgroup do it cost 27 us (1024 workgroups) to 45 us (2048), whether they
+// counted on one counter or on one per 64: each one's release writes back
+// its XCD's L2.
 __global__ void __launch_bounds__(kThreads)
     adamw_clip_kernel(const double *partials, uint32_t n, AdamNorm *norm, float grad_scale, double max_norm,
                       float *norm_out) {
   __shared__ double lds[4];
-  double sum = 0.0;
-  for (uint32_t k = threadIdx.x; k < n; k += kThreads) sum += partials[k];
+  double x[kAdamNormGrid / kThreads], sum = 0.0;
+#pragma unroll
+  for (uint32_t k = 0; k < kAdamNormGrid / kThreads; ++k)
+    x[k] = k * kThreads + threadIdx.x < n ? partials[k * kThreads + threadIdx.x] : 0.0;
+#pragma unroll
+  for (uint32_t k = 0; k < kAdamNormGrid / kThreads; ++k) sum += x[k];
   sum = block_sum(sum, lds);
   if (threadIdx.x == 0) {
     const double r = sqrt(sum) * fabs((double)grad_scale);
@@ -601,18 +595,19 @@ wt_status step_impl(wt_adamw *a, const wt_adamw_hyper *h, hipStream_t stream) {
   if (h->max_norm > 0 || h->norm_out) {
     AdamNorm *norm = (AdamNorm *)(a->mem + a->at.norm);
     const uint32_t grid = n_items < 1 ? 1 : n_items < kAdamNormGrid ? n_items : kAdamNormGrid;
+    const auto kernel = a->L.state_bits == 8 ? adamw_norm_kernel<adam_item(8)> : adamw_norm_kernel<adam_item(32)>;
     double *partials = (double *)(a->mem + a->at.partials);
-    hipLaunchKernelGGL(adamw_norm_kernel, dim3(grid), dim3(kThreads), 0, stream,
-                       (const AdamGradItem *)(a->mem + a->at.grads), n_items, partials);
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(kThreads), 0, stream, (const AdamGradItem *)(a->mem + a->at.grads),
+                       n_items, partials);
     hipLaunchKernelGGL(adamw_clip_kernel, dim3(1), dim3(kThreads), 0, stream, partials, grid, norm, k.grad_scale,
                        h->max_norm, h->norm_out);
     k.norm = norm;
   }
   if (n_items > 0) {
     if (a->L.state_bits == 8)
-      hipLaunchKernelGGL((adamw_update_kernel<8>), dim3(n_items), dim3(kThreads), 0, stream, k);
+      hipLaunchKernelGGL((adamw_update_kernel<8>), dim3(n_items), dim3(adam_item(8) / 8), 0, stream, k);
     else
-      hipLaunchKernelGGL((adamw_update_kernel<32>), dim3(n_items), dim3(kThreads), 0, stream, k);
+      hipLaunchKernelGGL((adamw_update_kernel<32>), dim3(n_items), dim3(adam_item(32) / 8), 0, stream, k);
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return fail(hip_msg("launch", e), WT_E_HIP);

@@ -510,7 +510,7 @@ wt_status wt_dispatch_rows(const int32_t *index, int64_t n_tokens, int32_t top_k
  * The optimizer step that produces what wt_prepare transfers ("Weight transfer
  * for RL post-training in under 2 seconds", section "High-level workflow":
  * after each training step the training GPUs send their parameters). One call
- * updates every shard of a rank in place, in one launch (two when the
+ * updates every shard of a rank in place, in one launch (three when the
  * gradients are clipped by their global norm), so a prepare enqueued behind it
  * on the same stream reads the new weights.
  *

@@ -494,3 +494,34 @@ def test_step_then_prepare_of_the_same_shards(wt, bits):
         s.synchronize()
     assert all((a != b).float().mean() > 0.5 for a, b in zip(old, shards))
     assert_images_equal(dst.cpu().numpy(), oracle_image_threaded(wl), wl)
+
+
+@pytest.mark.parametrize("grad", ["fp32", "bf16"])
+@pytest.mark.parametrize("exponent", [-20, 0, 16])
+def test_stored_states_equal_separate_fp32_operations(wt, grad, exponent):
+    # codes and scales bit for bit: every product, sum, root and quotient rounded by itself, as numpy's fp32 does
+    n = 128 * 700 + 55
+    t = Tensor(n, 8, grad, True, True, seed=21 + exponent, spread=2.0)
+    f = np.float32
+    for k, up in (("grad", 1), ("m_scale", 1), ("v_scale", 1)):
+        x = torch.from_numpy(t.read(k).view(np.int16) if t.dtype[k] == torch.bfloat16 else t.read(k))
+        x = x.view(torch.bfloat16) if t.dtype[k] == torch.bfloat16 else x
+        t.set(k, x * 2.0 ** exponent)
+    h = hyper(wt, seed=99)
+    before, after = run(wt, [t], h, 8)
+    b, a = before[0], after[0]
+    g = (R.bf16_value(b["grad"]).astype(f) if grad == "bf16" else b["grad"]) * f(h.grad_scale)
+    m = R.E4M3[b["m"]].astype(f) * R.per_block(b["m_scale"], n)
+    r = R.E4M3[b["v"]].astype(f) * R.per_block(b["v_scale"], n)
+    m = f(h.beta1) * m + f(1 - h.beta1) * g
+    root = np.sqrt(f(h.beta2) * (r * r) + f(1 - h.beta2) * (g * g))
+    assert m.dtype == root.dtype == f
+    w = R.words(h.seed, h.step, 0, n)
+    for name, x, bits in (("m", m, w & np.uint64(0xFFFF)), ("v", root, w >> np.uint64(16))):
+        amax = R.block_amax(x.astype(np.float64)).astype(f)
+        assert np.array_equal(a[name + "_scale"], amax / f(448)), name
+        y = np.abs(x * R.per_block(f(448) / amax, n))
+        if name == "v":
+            y = np.where(x > 0, np.maximum(y, f(2.0 ** -9)), y)
+        want = R.e4m3_up(np.minimum(y, f(448)).astype(np.float64), bits.astype(np.float64) / 65536)
+        assert np.array_equal(np.abs(R.E4M3[a[name]]), want), name

@@ -1,10 +1,14 @@
 // dispatch.hip -- the row map of a dispatch: token copies grouped by expert
 // in a stable order. The definition is in wt.h.
 //
-// Three launches: each workgroup counts its tile of copies per expert; one
-// workgroup turns the tiles' counts into each tile's first row per expert;
-// each workgroup ranks its copies and writes both maps. Every rank comes from
-// counts and lane masks, never from the order of atomics.
+// A copy's row = its expert's first row + the copies of that expert in the
+// tiles before its own, in the waves before its own, and in the lanes before
+// its own. Counts come from integer histograms and lane masks, never from the
+// order of atomics. Up to kRowsSingle copies one workgroup does everything (one
+// launch); beyond, a first launch counts each tile and the second one's
+// workgroups each add up what they need of the (at most 64) tiles' counts,
+// which costs them 2 us of L2 reads side by side where a scan kernel between
+// the two took 12 us alone.
 #include <hip/hip_runtime.h>
 
 #include <string>
@@ -16,11 +20,17 @@
 namespace wt {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
 constexpr int kMaxExperts = 1024;
-constexpr int kTile = 2048;  // copies of one workgroup
-constexpr int kScanThreads = 1024;
+constexpr int kMaxTiles = 64;
+#ifndef ROWS_TILE
+#define ROWS_TILE 2048
+#endif
+#ifndef ROWS_SINGLE
+#define ROWS_SINGLE 8192
+#endif
+constexpr int64_t kRowsTile = ROWS_TILE;       // copies of one workgroup, more where there would be over 64 tiles
+constexpr int64_t kRowsSingle = ROWS_SINGLE;
+constexpr int64_t kRowsSingleFill = 65536;     // rows that one workgroup may have to fill
 
 struct RowsArgs {
   const int32_t *index;
@@ -28,67 +38,30 @@ struct RowsArgs {
   int32_t top_k, n_experts, align;
   int64_t n_rows;
   int32_t *row_token, *pair_row, *offsets, *counts;
-  int32_t *tile_rows;  // [tile][expert]: counts, then first rows
-  int32_t *used;       // [expert]: copies (also where counts is NULL)
+  int32_t *tile_counts;  // [tile][expert]
+  int64_t tile;          // copies of a tile, a multiple of 64 times the workgroup's waves
   int32_t n_tiles;
 };
+
+// Waves of a workgroup: their histograms take 4 bytes per expert each.
+int waves_for(int n_experts) { return n_experts <= 512 ? 16 : 8; }
 
 __device__ __forceinline__ int expert_at(const RowsArgs &a, int64_t i, int64_t end) {
   const int e = i < end ? a.index[i] : -1;
   return e >= 0 && e < a.n_experts ? e : -1;
 }
 
-// Copies per expert of pairs [lo, hi), one histogram per wave: wave w takes
-// the w-th quarter of the tile, so that ranks follow the pairs' order.
-__device__ __forceinline__ void count_tile(const RowsArgs &a, int64_t lo, int64_t hi, int (*hist)[kMaxExperts]) {
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  for (int e = threadIdx.x; e < kWaves * kMaxExperts; e += kThreads) (&hist[0][0])[e] = 0;
+__global__ void __launch_bounds__(1024) rows_count_kernel(RowsArgs a) {
+  extern __shared__ int lds[];
+  const int64_t lo = blockIdx.x * a.tile, hi = lo + a.tile < a.n_pairs ? lo + a.tile : a.n_pairs;
+  for (int e = threadIdx.x; e < a.n_experts; e += blockDim.x) lds[e] = 0;
   __syncthreads();
-  const int64_t from = lo + wave * (kTile / kWaves), to = from + kTile / kWaves < hi ? from + kTile / kWaves : hi;
-  for (int64_t i = from + lane; i < to; i += 64) {
-    const int e = expert_at(a, i, to);
-    if (e >= 0) atomicAdd(&hist[wave][e], 1);
+  for (int64_t i = lo + threadIdx.x; i < hi; i += blockDim.x) {
+    const int e = expert_at(a, i, hi);
+    if (e >= 0) atomicAdd(&lds[e], 1);
   }
   __syncthreads();
-}
-
-__global__ void __launch_bounds__(kThreads) rows_count_kernel(RowsArgs a) {
-  __shared__ int hist[kWaves][kMaxExperts];
-  const int64_t lo = (int64_t)blockIdx.x * kTile, hi = lo + kTile < a.n_pairs ? lo + kTile : a.n_pairs;
-  count_tile(a, lo, hi, hist);
-  for (int e = threadIdx.x; e < a.n_experts; e += kThreads)
-    a.tile_rows[(int64_t)blockIdx.x * a.n_experts + e] = (hist[0][e] + hist[1][e]) + (hist[2][e] + hist[3][e]);
-}
-
-// One workgroup, thread e for expert e: the copies of every tile before it,
-// then the experts' first rows (a scan over the padded counts).
-__global__ void __launch_bounds__(kScanThreads) rows_scan_kernel(RowsArgs a) {
-  __shared__ int scan[kScanThreads];
-  const int e = threadIdx.x;
-  int total = 0;
-  if (e < a.n_experts)
-    for (int32_t t = 0; t < a.n_tiles; ++t) {
-      int32_t *p = a.tile_rows + (int64_t)t * a.n_experts + e;
-      const int c = *p;
-      *p = total;
-      total += c;
-    }
-  const int padded = (total + a.align - 1) / a.align * a.align;
-  scan[e] = padded;
-  __syncthreads();
-  for (int d = 1; d < kScanThreads; d *= 2) {
-    const int before = e >= d ? scan[e - d] : 0;
-    __syncthreads();
-    scan[e] += before;
-    __syncthreads();
-  }
-  if (e < a.n_experts) {
-    const int start = scan[e] - padded;
-    a.offsets[e] = start;
-    a.used[e] = total;
-    if (a.counts) a.counts[e] = total;
-    if (e == a.n_experts - 1) a.offsets[e + 1] = scan[e];
-  }
+  for (int e = threadIdx.x; e < a.n_experts; e += blockDim.x) a.tile_counts[blockIdx.x * a.n_experts + e] = lds[e];
 }
 
 // Lanes of the wave with the same expert as this one.
@@ -102,48 +75,102 @@ __device__ __forceinline__ uint64_t same_expert(int e) {
   return m;
 }
 
-__global__ void __launch_bounds__(kThreads) rows_place_kernel(RowsArgs a) {
-  __shared__ int next[kWaves][kMaxExperts];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t lo = (int64_t)blockIdx.x * kTile, hi = lo + kTile < a.n_pairs ? lo + kTile : a.n_pairs;
-  if (lo < hi) {
-    count_tile(a, lo, hi, next);
-    // each wave's first row per expert
-    for (int e = threadIdx.x; e < a.n_experts; e += kThreads) {
-      int at = a.offsets[e] + a.tile_rows[(int64_t)blockIdx.x * a.n_experts + e];
-      for (int w = 0; w < kWaves; ++w) {
-        const int c = next[w][e];
-        next[w][e] = at;
-        at += c;
+template <bool Single>
+__global__ void __launch_bounds__(1024) rows_place_kernel(RowsArgs a) {
+  extern __shared__ int lds[];
+  const int E = a.n_experts, waves = blockDim.x >> 6, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  int *next = lds;               // [wave][expert]: counts, then next rows
+  int *before = next + waves * E;  // [expert]: copies in the tiles before
+  int *total = before + E;       // [expert]: copies in all tiles
+  int *start = total + E;        // [expert + 1]: first rows
+  const int64_t lo = blockIdx.x * a.tile, hi = lo + a.tile < a.n_pairs ? lo + a.tile : a.n_pairs;
+  const int64_t part = a.tile / waves, from = lo + wave * part, to = from + part < hi ? from + part : hi;
+  for (int e = threadIdx.x; e < (waves + 2) * E; e += blockDim.x) lds[e] = 0;
+  __syncthreads();
+  for (int64_t i = from + lane; i < to; i += 64) {
+    const int e = expert_at(a, i, to);
+    if (e >= 0) atomicAdd(&next[wave * E + e], 1);
+  }
+  if (!Single) {
+    // thread = (expert, every parts-th tile)
+    const int parts = max(1, (int)blockDim.x / E);
+    for (int at = threadIdx.x; at < parts * E; at += blockDim.x) {
+      const int e = at % E;
+      int b = 0, t = 0;
+#pragma unroll 16
+      for (int k = at / E; k < a.n_tiles; k += parts) {
+        const int c = a.tile_counts[k * E + e];
+        b += k < (int)blockIdx.x ? c : 0;
+        t += c;
       }
+      atomicAdd(&before[e], b);
+      atomicAdd(&total[e], t);
+    }
+  }
+  __syncthreads();
+  if (Single) {
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+      int t = 0;
+      for (int w = 0; w < waves; ++w) t += next[w * E + e];
+      total[e] = t;
     }
     __syncthreads();
-    const int64_t from = lo + wave * (kTile / kWaves), to = from + kTile / kWaves < hi ? from + kTile / kWaves : hi;
-    for (int64_t base = from; base < to; base += 64) {
-      const int64_t i = base + lane;
-      const int e = expert_at(a, i, to);
-      const uint64_t same = same_expert(e);
-      int row = -1;
-      if (e >= 0) {
-        const int before = __popcll(same & (((uint64_t)1 << lane) - 1));
-        row = next[wave][e] + before;
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        if (before == 0) next[wave][e] = row + __popcll(same);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        if (row >= a.n_rows) row = -1;
-        else if (a.row_token) a.row_token[row] = (int32_t)(i / a.top_k);
-      }
-      if (i < to && a.pair_row) a.pair_row[i] = row;
+  }
+  if (wave == 0) {  // scan of the padded counts, a run of experts to each lane
+    const int per = (E + 63) / 64, e0 = lane * per, e1 = min(E, e0 + per);
+    int sum = 0;
+    for (int e = e0; e < e1; ++e) sum += (total[e] + a.align - 1) / a.align * a.align;
+    int scan = sum;
+    for (int d = 1; d < 64; d *= 2) {
+      const int up = __shfl_up(scan, d);
+      if (lane >= d) scan += up;
+    }
+    int at = scan - sum;
+    for (int e = e0; e < e1; ++e) {
+      start[e] = at;
+      at += (total[e] + a.align - 1) / a.align * a.align;
+    }
+    if (lane == 63) start[E] = scan;
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    int at = start[e] + before[e];
+    for (int w = 0; w < waves; ++w) {
+      const int c = next[w * E + e];
+      next[w * E + e] = at;
+      at += c;
+    }
+    if (blockIdx.x == 0) {
+      a.offsets[e] = start[e];
+      if (a.counts) a.counts[e] = total[e];
     }
   }
-  if (!a.row_token) return;
-  // rows that hold no copy: behind each expert's copies, and behind the last expert
-  for (int e = blockIdx.x; e < a.n_experts; e += gridDim.x) {
-    const int64_t end = a.offsets[e + 1] < a.n_rows ? a.offsets[e + 1] : a.n_rows;
-    for (int64_t r = (int64_t)a.offsets[e] + a.used[e] + threadIdx.x; r < end; r += kThreads) a.row_token[r] = -1;
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[E] = start[E];
+  __syncthreads();
+  for (int64_t base = from; base < to; base += 64) {
+    const int64_t i = base + lane;
+    const int e = expert_at(a, i, to);
+    const uint64_t same = same_expert(e);
+    int row = -1;
+    if (e >= 0) {
+      const int rank = __popcll(same & (((uint64_t)1 << lane) - 1));
+      row = next[wave * E + e] + rank;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      if (rank == 0) next[wave * E + e] = row + __popcll(same);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      if (row >= a.n_rows) row = -1;
+      else if (a.row_token) a.row_token[row] = (int32_t)((uint32_t)i / (uint32_t)a.top_k);
+    }
+    if (i < to && a.pair_row) a.pair_row[i] = row;
   }
-  for (int64_t r = (int64_t)a.offsets[a.n_experts] + (int64_t)blockIdx.x * kThreads + threadIdx.x; r < a.n_rows;
-       r += (int64_t)gridDim.x * kThreads)
+  if (!a.row_token) return;
+  // rows that hold no copy: behind each expert's copies (a wave per expert), and behind the last expert
+  for (int e = blockIdx.x * waves + wave; e < E; e += gridDim.x * waves) {
+    const int64_t end = start[e + 1] < a.n_rows ? start[e + 1] : a.n_rows;
+    for (int64_t r = (int64_t)start[e] + total[e] + lane; r < end; r += 64) a.row_token[r] = -1;
+  }
+  for (int64_t r = (int64_t)start[E] + blockIdx.x * blockDim.x + threadIdx.x; r < a.n_rows;
+       r += (int64_t)gridDim.x * blockDim.x)
     a.row_token[r] = -1;
 }
 
@@ -159,8 +186,6 @@ wt_status check_sizes(const char *what, int64_t n_tokens, int32_t top_k, int32_t
   return WT_OK;
 }
 
-int64_t tiles_of(int64_t pairs) { return (pairs + kTile - 1) / kTile; }
-
 }  // namespace
 }  // namespace wt
 
@@ -173,7 +198,8 @@ wt_status wt_dispatch_workspace_bytes(int64_t n_tokens, int32_t top_k, int32_t n
   const wt_status st = check_sizes(what, n_tokens, top_k, n_experts);
   if (st != WT_OK) return st;
   if (!bytes) return fail(what, "NULL result");
-  *bytes = (size_t)(4 * (tiles_of(n_tokens * top_k) + 1) * n_experts);
+  const int64_t tiles = (n_tokens * top_k + kRowsTile - 1) / kRowsTile;
+  *bytes = (size_t)(4 * n_experts * (tiles < 1 ? 1 : tiles > kMaxTiles ? kMaxTiles : tiles));
   return WT_OK;
 }
 
@@ -195,6 +221,8 @@ wt_status wt_dispatch_rows(const int32_t *index, int64_t n_tokens, int32_t top_k
          (uintptr_t)workspace) % 4)
       return fail(what, "misaligned pointer", WT_E_ALIGN);
     if (workspace_bytes < need) return fail(what, "workspace too small", WT_E_RANGE);
+    const bool single = pairs <= kRowsSingle && (!row_token || n_rows <= kRowsSingleFill);
+    const int waves = waves_for(n_experts), unit = 64 * waves;
     RowsArgs a{};
     a.index = index;
     a.n_pairs = pairs;
@@ -206,13 +234,21 @@ wt_status wt_dispatch_rows(const int32_t *index, int64_t n_tokens, int32_t top_k
     a.pair_row = pair_row;
     a.offsets = offsets;
     a.counts = counts;
-    a.n_tiles = (int32_t)tiles_of(pairs);
-    a.used = (int32_t *)workspace;
-    a.tile_rows = a.used + n_experts;
+    a.tile_counts = (int32_t *)workspace;
+    a.tile = single ? pairs : pairs <= kRowsTile * kMaxTiles ? kRowsTile : (pairs + kMaxTiles - 1) / kMaxTiles;
+    a.tile = (a.tile + unit - 1) / unit * unit;
+    if (a.tile == 0) a.tile = unit;
+    a.n_tiles = (int32_t)((pairs + a.tile - 1) / a.tile);
     const hipStream_t s = (hipStream_t)stream;
-    if (a.n_tiles > 0) hipLaunchKernelGGL(rows_count_kernel, dim3((uint32_t)a.n_tiles), dim3(kThreads), 0, s, a);
-    hipLaunchKernelGGL(rows_scan_kernel, dim3(1), dim3(kScanThreads), 0, s, a);
-    hipLaunchKernelGGL(rows_place_kernel, dim3(a.n_tiles > 0 ? (uint32_t)a.n_tiles : 1u), dim3(kThreads), 0, s, a);
+    const uint32_t grid = a.n_tiles > 0 ? (uint32_t)a.n_tiles : 1u, threads = 64u * waves;
+    const uint32_t lds = 4u * ((waves + 3) * n_experts + 1);
+    if (single) {
+      hipLaunchKernelGGL((rows_place_kernel<true>), dim3(grid), dim3(threads), lds, s, a);
+    } else {
+      if (a.n_tiles > 0)
+        hipLaunchKernelGGL(rows_count_kernel, dim3(grid), dim3(threads), 4u * n_experts, s, a);
+      hipLaunchKernelGGL((rows_place_kernel<false>), dim3(grid), dim3(threads), lds, s, a);
+    }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return fail(what, hip_msg("launch", e), WT_E_HIP);
     return WT_OK;

@@ -14,10 +14,13 @@
 namespace wt {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 32;
+
+// Waves of a workgroup of the two passes over tokens: 16, 8 where a row of
+// sums per wave would take too much shared memory.
+template <int NJ>
+constexpr int kWavesOf = NJ <= 6 ? 16 : 8;
 
 struct RouterArgs {
   uint64_t logits;
@@ -38,15 +41,19 @@ __device__ __forceinline__ int32_t seq_start(const RouterArgs &a, int32_t q) {
   return x < 0 ? 0 : x > a.n_tokens ? a.n_tokens : x;
 }
 
-// Lowest q with seq_start(q + 1) > t, or n_seqs.
+// Lowest q with seq_start(q + 1) > t, or n_seqs: a search that probes 64
+// places at once, so that up to 64 sequences cost one load.
 __device__ __forceinline__ int32_t seq_of(const RouterArgs &a, int32_t t) {
+  const int lane = threadIdx.x & 63;
   int32_t lo = 0, hi = a.n_seqs;
-  while (lo < hi) {
-    const int32_t mid = (lo + hi) >> 1;
-    if (seq_start(a, mid + 1) > t) hi = mid;
-    else lo = mid + 1;
+  while (hi - lo > 64) {
+    const int32_t step = (hi - lo + 63) >> 6, at = min(lo + (lane + 1) * step, hi);
+    const int n = __popcll(__ballot(seq_start(a, at) <= t));
+    lo = min(lo + n * step, hi);
+    hi = min(lo + step, hi);
   }
-  return lo;
+  const bool behind = lo + lane < hi && seq_start(a, lo + lane + 1) <= t;
+  return lo + __popcll(__ballot(behind));
 }
 
 // The runs of a workgroup's tokens [t, end) that belong to one sequence, or
@@ -56,15 +63,18 @@ struct Runs {
   __device__ Runs(const RouterArgs &a, int32_t first, int32_t last) : t(first), end(last), q(seq_of(a, first)) {}
   __device__ bool next(const RouterArgs &a, int32_t *lo, int32_t *hi, int32_t *seq) {
     if (t >= end) return false;
-    while (q < a.n_seqs && seq_start(a, q + 1) <= t) ++q;
+    int32_t start = end, stop = end;
+    for (; q < a.n_seqs; ++q) {
+      start = seq_start(a, q);
+      stop = seq_start(a, q + 1);
+      if (stop > t) break;
+    }
     *lo = t;
-    const int32_t start = q < a.n_seqs ? seq_start(a, q) : end;
     if (q >= a.n_seqs || start > t) {
       *seq = -1;
-      *hi = start < end ? start : end;
+      *hi = q < a.n_seqs && start < end ? start : end;
     } else {
       *seq = q;
-      const int32_t stop = seq_start(a, q + 1);
       *hi = stop < end ? stop : end;
     }
     t = *hi;
@@ -85,14 +95,24 @@ __device__ __forceinline__ void load_row(const RouterArgs &a, int64_t t, int lan
   }
 }
 
+__device__ __forceinline__ float load_logit(const RouterArgs &a, int64_t t, int e) {
+  const uint64_t row = a.logits + (a.bf16 ? 2ull : 4ull) * (uint64_t)(t * a.stride);
+  return a.bf16 ? bf16_lo(ld_global<uint16_t>(row + 2ull * e)) : ld_global<float>(row + 4ull * e);
+}
+
 // What turns a logit into its score (softmax: exp(x - top) inv) and a score
 // into its probability (sigmoid: s inv).
 struct Norm {
   float top, inv;
 };
 
+// exp(x) as 2^(x log2 e): the rounding of the product makes it off by |x|
+// 2^-24 of the result, so by less than 2^-24 of 1 / e at the most where the
+// result is below 1 (all there is here: 1 / (1 + exp) and exp(x - top)).
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
+
 __device__ __forceinline__ float score_of(const RouterArgs &a, const Norm &n, float x) {
-  return a.softmax ? expf(x - n.top) * n.inv : 1.0f / (1.0f + expf(-x));
+  return a.softmax ? fast_exp(x - n.top) * n.inv : __builtin_amdgcn_rcpf(1.0f + fast_exp(-x));
 }
 
 template <int NJ>
@@ -124,40 +144,42 @@ __device__ __forceinline__ Norm scores(const RouterArgs &a, const float x[NJ], f
 
 __device__ __forceinline__ bool selectable(float x) { return x > -INFINITY; }  // false for NaN
 
-// Two keys closer than this may stand in the wrong order: a score carries at
-// most 4 fp32 roundings (exponential, sum, quotient, product: below 5e-7 of
-// it) and the sum with the bias one of the key.
-__device__ __forceinline__ float near_tie(float key) { return 2e-6f * (1.0f + fabsf(key)); }
+// Top and sum of a softmax in 64 bits.
+__device__ __forceinline__ void softmax64(const RouterArgs &a, int64_t t, int lane, double *top, double *z) {
+  double m = -INFINITY, sum = 0.0;
+  for (int e = lane; e < a.n_experts; e += 64) {
+    const float x = load_logit(a, t, e);
+    m = fmax(m, selectable(x) ? (double)x : -INFINITY);
+  }
+  for (int d = 32; d; d >>= 1) m = fmax(m, __shfl_xor(m, d));
+  for (int e = lane; e < a.n_experts; e += 64) sum += exp((double)load_logit(a, t, e) - m);
+  for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+  *top = m;
+  *z = sum;
+}
 
-// Selection in 64 bits for a token with two keys too close to order in 32
-// (out of line, from the logits again: it is rare and must cost no registers).
-template <int NJ>
-__device__ __attribute__((noinline)) int select_exact(const RouterArgs &a, int64_t t, int lane) {
-  float x[NJ];
-  double k[NJ];
-  load_row<NJ>(a, t, lane, x);
-  double top = -INFINITY, z = 0.0;
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) top = fmax(top, selectable(x[j]) ? (double)x[j] : -INFINITY);
-  for (int d = 32; d; d >>= 1) top = fmax(top, __shfl_xor(top, d));
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    k[j] = a.softmax ? exp((double)x[j] - top) : 1.0 / (1.0 + exp(-(double)x[j]));
-    z += selectable(x[j]) ? k[j] : 0.0;
-  }
-  for (int d = 32; d; d >>= 1) z += __shfl_xor(z, d);
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    const int e = lane + 64 * j;
-    k[j] = selectable(x[j]) && e < a.n_experts ? (a.softmax ? k[j] / z : k[j]) + (double)a.bias[e] : -INFINITY;
-  }
+// An expert's key in 64 bits (-infinity: not selectable).
+__device__ __forceinline__ double exact_key(const RouterArgs &a, int64_t t, int e, double top, double z) {
+  const double x = (double)load_logit(a, t, e);
+  double key = x;
+  if (a.bias) key = (a.softmax ? exp(x - top) / z : 1.0 / (1.0 + exp(-x))) + (double)a.bias[e];
+  return x > -INFINITY && key > -INFINITY ? key : -INFINITY;
+}
+
+// Selection one expert after the other, keys in 64 bits and from memory each
+// time: for tokens with more equal keys than there are lanes.
+__device__ __forceinline__ int select_rounds(const RouterArgs &a, int64_t t, int lane, double top, double z) {
   int index = -1;
+  double last = INFINITY;
+  int last_e = -1;
   for (int r = 0; r < a.top_k; ++r) {
+    // the greatest key behind the last one taken, and of equals the lowest expert
     double best = -INFINITY;
     int at = kMaxExperts;
-#pragma unroll
-    for (int j = NJ - 1; j >= 0; --j)
-      if (k[j] >= best && k[j] > -INFINITY) best = k[j], at = lane + 64 * j;
+    for (int e = lane; e < a.n_experts; e += 64) {
+      const double k = exact_key(a, t, e, top, z);
+      if ((k < last || (k == last && e > last_e)) && k > best) best = k, at = e;
+    }
     for (int d = 32; d; d >>= 1) {
       const double ob = __shfl_xor(best, d);
       const int oa = __shfl_xor(at, d);
@@ -165,64 +187,173 @@ __device__ __attribute__((noinline)) int select_exact(const RouterArgs &a, int64
     }
     if (at >= kMaxExperts) break;
     if (lane == r) index = at;
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-      if (lane + 64 * j == at) k[j] = -INFINITY;
+    last = best;
+    last_e = at;
   }
   return index;
 }
 
-// Selection: lane r < top_k receives the r-th expert (-1: none left).
-// A round takes the greatest key over the wave and, by ballots in the order
-// of the expert's number, the lowest expert that has it. With a bias the keys
-// carry roundings: rounds go on behind the last place until a different key
-// shows that its border is safe, and a near tie decides in 64 bits.
+// Two keys closer than this may stand in the wrong order, in units of 2^-24
+// of which a key carries: for the sigmoid 0.8 from the exponential (see
+// fast_exp; its own last bit counts s (1 - s) <= 1/4), 1 from the sum and 2
+// from v_rcp_f32; for softmax, of the score, 2 from the exponential, 1 / e from
+// its argument, 24 from the sum over the experts, 2 from quotient and product;
+// and 1 of the key from the sum with the bias. Twice that for a pair.
+__device__ __forceinline__ float near_tie(const RouterArgs &a, float key, float score) {
+  return 0x1p-23f * ((a.softmax ? 0.5f + 28.0f * score : 3.8f) + fabsf(key));
+}
+
+// A wave's candidates of a selection.
+struct Candidates {
+  uint32_t key[64];
+  float score[64];
+  uint16_t expert[64];
+};
+
+// fp32 to an unsigned number of the same order; both zeros alike.
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t b = __float_as_uint(x + 0.0f);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float from_ordered(uint32_t u) {
+  return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
+}
+
+// Packs the experts whose keys reach lo to one per lane, in the order of their
+// numbers; returns how many there are (those beyond 64 are left out).
 template <int NJ>
-__device__ __forceinline__ int select_topk(const RouterArgs &a, int64_t t, const float x[NJ], const float s[NJ],
-                                           const float b[NJ], int lane) {
-  float k[NJ];
+__device__ __forceinline__ int collect(const uint32_t k[NJ], const float s[NJ], uint32_t lo, int lane, Candidates &c) {
+  int count = 0;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    const bool in = k[j] >= lo;
+    const uint64_t who = __ballot(in);
+    if (who) {
+      const int at = count + __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
+      if (in && at < 64) {
+        c.key[at] = k[j];
+        c.score[at] = s[j];
+        c.expert[at] = (uint16_t)(lane + 64 * j);
+      }
+      count += __popcll(who);
+    }
+  }
+  wave_lds_fence();
+  return count;
+}
+
+// Selection: lane r < top_k receives the r-th expert (-1: none left) and its
+// score. False where it could not be decided.
+//
+// A threshold is sought that at least top_k + 1 of the 64 lanes' greatest keys
+// reach, and few more (bisection on the ordered keys, a compare and a count
+// of a lane mask per step). The experts whose keys reach it, at most 64, are
+// packed to one per lane in the order of their numbers, and each counts the
+// ones before it (greater key, or the same key and a lower lane): its rank.
+// About 115 vector instructions a token of 384 experts, where taking the
+// greatest key top_k times takes 35 each time.
+//
+// With a bias the keys carry roundings. Where two neighbours of the first
+// top_k + 1 (or of a run of equals across that border and the next behind it)
+// are too close and not of the same logit and bias, the token is not decided;
+// neither is one with more than 64 candidates. Exact takes such a token again:
+// all experts that may belong to the first top_k ranked by keys in 64 bits.
+template <int NJ, bool Exact>
+__device__ __forceinline__ bool select_topk(const RouterArgs &a, int64_t t, const float x[NJ], const float s[NJ],
+                                            const float b[NJ], int lane, Candidates &c, int *index, float *score) {
+  uint32_t k[NJ], h = 0;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
     const float key = a.bias ? s[j] + b[j] : x[j];
-    k[j] = selectable(x[j]) && selectable(key) ? key : -INFINITY;  // never NaN from here on
+    k[j] = selectable(x[j]) && selectable(key) ? ordered(key) : 0u;
+    h = max(h, k[j]);
   }
-  int index = -1;
-  bool close = false;
-  float key0 = 0.0f, x0 = 0.0f, b0 = 0.0f;
-  for (int r = 0;; ++r) {
-    if (!a.bias && r == a.top_k) break;
-    float m = k[0];
-#pragma unroll
-    for (int j = 1; j < NJ; ++j) m = fmaxf(m, k[j]);
-    m = wave_max(m);
-    if (m == -INFINITY) break;
-    int at = 0;
-    float xr = 0.0f, br = 0.0f;
-    bool found = false;
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-      if (!found) {
-        const uint64_t who = __ballot(k[j] == m);
-        if (who) {
-          const int l = __builtin_ctzll(who);
-          found = true;
-          at = l + 64 * j;
-          if (a.bias) {
-            xr = __shfl(x[j], l);
-            br = __shfl(b[j], l);
-          }
-          if (lane == l) k[j] = -INFINITY;
-        }
-      }
-    if (a.bias) {
-      const bool same = r > 0 && xr == x0 && br == b0;
-      if (r > 0 && !same && key0 - m <= near_tie(key0)) close = true;
-      if (r >= a.top_k && !same) break;
-      key0 = m, x0 = xr, b0 = br;
+  const uint32_t top = wave_max_u32(h);
+  *index = -1;
+  *score = 0.0f;
+  if (top == 0) return true;
+  const int need = a.top_k + 1;
+  // keys down to a quarter of the greatest, or all there are
+  uint32_t lo = top > 0x01000000u ? top - 0x01000000u : 1u, hi = top;
+  int n = __popcll(__ballot(h >= lo));
+  if (n < need) {
+    hi = lo;
+    lo = 1u;
+    n = __popcll(__ballot(h >= lo));
+  }
+  // a lane may hold several keys above lo, so stopping at a few more than needed is enough
+  while (n > need + 2 && hi - lo > 1) {
+    const uint32_t mid = lo + (hi - lo) / 2;
+    const int m = __popcll(__ballot(h >= mid));
+    if (m >= need) lo = mid, n = m;
+    else hi = mid;
+  }
+  int count = collect<NJ>(k, s, lo, lane, c);
+  uint32_t key = lane < count ? c.key[lane] : 0u;
+  int rank = lane < count ? 0 : lane;  // lanes without a candidate stay behind them
+  for (int i = 0; i < min(count, 64); ++i) {
+    const uint32_t other = __builtin_amdgcn_readlane(key, i);
+    rank += lane < count && other > key - (lane > i ? 1u : 0u) ? 1 : 0;
+  }
+  if (count > 64 && !Exact) return false;
+  if (a.bias && !Exact) {
+    // neighbours by rank
+    const float sc = c.score[lane];
+    const int ex = c.expert[lane];
+    wave_lds_fence();
+    c.key[rank] = key;
+    wave_lds_fence();
+    const bool pair = lane + 1 < count;
+    const float k0 = from_ordered(c.key[lane]), k1 = from_ordered(c.key[(lane + 1) & 63]);
+    wave_lds_fence();
+    // the greatest score of a candidate bounds the pair's
+    const float most = a.softmax ? wave_max(lane < count ? sc : 0.0f) : 0.0f;
+    const uint64_t close = __ballot(pair && k0 - k1 <= near_tie(a, k0, most));
+    if (close & ((2ull << (a.top_k - 1)) - 1)) {
+      int from = 0;  // the lane that holds rank `lane`
+      for (int i = 0; i < count; ++i)
+        if (__builtin_amdgcn_readlane(rank, i) == lane) from = i;
+      const float xe = lane < count ? load_logit(a, t, ex) : 0.0f, be = lane < count ? a.bias[ex] : 0.0f;
+      const float x0 = __shfl(xe, from), b0 = __shfl(be, from);
+      const uint64_t same = __ballot(pair && x0 == __shfl_down(x0, 1) && b0 == __shfl_down(b0, 1));
+      const int border = a.top_k - 1 + __builtin_ctzll(~(same >> (a.top_k - 1)));  // first unlike pair from there on
+      const bool open = border + 1 < count ? (close >> border) & 1 : count > a.top_k && lo > 1;
+      if (open || (close & ~same & ((1ull << (a.top_k - 1)) - 1))) return false;
     }
-    if (r < a.top_k && lane == r) index = at;
   }
-  return close ? select_exact<NJ>(a, t, lane) : index;
+  if (Exact) {
+    double top64 = 0.0, z64 = 1.0;
+    if (a.softmax && a.bias) softmax64(a, t, lane, &top64, &z64);
+    if (count <= 64 && count > a.top_k) {  // everything within reach of the last place
+      const float last = from_ordered(__builtin_amdgcn_readlane(key, __builtin_ctzll(__ballot(rank == a.top_k - 1))));
+      const float reach = last - near_tie(a, last, a.softmax ? 1.0f : 0.0f);
+      wave_lds_fence();
+      count = collect<NJ>(k, s, min(lo, ordered(reach)), lane, c);
+    }
+    if (count > 64) {
+      *index = select_rounds(a, t, lane, top64, z64);
+      if (*index >= 0) *score = -1.0f;  // to be taken from the logit
+      return true;
+    }
+    const double mine = lane < count ? exact_key(a, t, c.expert[lane], top64, z64) : 0.0;
+    rank = lane < count ? 0 : lane;
+    for (int i = 0; i < count; ++i) {
+      const double other = __shfl(mine, i);
+      rank += lane < count && (other > mine || (other == mine && i < lane)) ? 1 : 0;
+    }
+  }
+  const float sc = c.score[lane];
+  const uint16_t ex = c.expert[lane];
+  wave_lds_fence();
+  c.score[rank] = sc;
+  c.expert[rank] = ex;
+  wave_lds_fence();
+  if (lane < a.top_k && lane < count) {
+    *index = c.expert[lane];
+    *score = c.score[lane];
+  }
+  wave_lds_fence();
+  return true;
 }
 
 struct ForwardOut {
@@ -232,15 +363,29 @@ struct ForwardOut {
   int32_t *part_c;  // and selections of the tokens that the two share
 };
 
+// What a token's selection leaves: its row of both outputs and its counts.
+__device__ __forceinline__ void put_token(const RouterArgs &a, const ForwardOut &o, int32_t t, int lane, int index,
+                                          float score, int *cnt) {
+  float w = score;
+  if (a.normalize) w /= wave_sum(w) + 1e-20f;
+  if (index >= 0) atomicAdd(&cnt[index], 1);
+  if (lane < a.top_k) {
+    o.index[(int64_t)t * a.top_k + lane] = index;
+    o.weight[(int64_t)t * a.top_k + lane] = w * a.scale;
+  }
+}
+
 // Forward pass over tokens. One wave per token; a workgroup's tile of tokens
 // is cut at the sequences' borders, and the tokens that tile i shares with
 // sequence q leave their sums at row i + q: along the tokens each step to the
 // next pair raises i or q, so no two pairs share a row, no sum needs an
 // atomic, and the order of every sum is fixed.
 template <int NJ>
-__global__ void __launch_bounds__(kThreads) router_forward_kernel(RouterArgs a, ForwardOut o) {
-  __shared__ float sum[kWaves][64 * NJ];
+__global__ void __launch_bounds__(64 * kWavesOf<NJ>) router_forward_kernel(RouterArgs a, ForwardOut o) {
+  constexpr int W = kWavesOf<NJ>, Threads = 64 * W;
+  __shared__ float sum[W][64 * NJ];
   __shared__ int cnt[64 * NJ];
+  __shared__ Candidates cand[W];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int32_t first = blockIdx.x * a.tile;
   const int32_t last = a.n_tokens - first < a.tile ? a.n_tokens : first + a.tile;
@@ -251,93 +396,102 @@ __global__ void __launch_bounds__(kThreads) router_forward_kernel(RouterArgs a, 
   int32_t lo, hi, q;
   while (runs.next(a, &lo, &hi, &q)) {
     if (q < 0) {
-      for (int64_t i = (int64_t)lo * a.top_k + threadIdx.x; i < (int64_t)hi * a.top_k; i += kThreads) {
+      for (int64_t i = (int64_t)lo * a.top_k + threadIdx.x; i < (int64_t)hi * a.top_k; i += Threads) {
         o.index[i] = -1;
         o.weight[i] = 0.0f;
       }
       continue;
     }
-    for (int e = threadIdx.x; e < a.n_experts; e += kThreads) cnt[e] = 0;
+    for (int e = threadIdx.x; e < a.n_experts; e += Threads) cnt[e] = 0;
     __syncthreads();
     float acc[NJ];
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[j] = 0.0f;
-    for (int32_t t = lo + wave; t < hi; t += kWaves) {
-      float x[NJ], s[NJ];
+    uint32_t undecided = 0;  // bit i: token lo + wave + W i (a tile holds at most 8 for a wave)
+    for (int32_t t = lo + wave, i = 0; t < hi; t += W, ++i) {
+      float x[NJ], s[NJ], w;
+      int index;
       load_row<NJ>(a, t, lane, x);
       const Norm n = scores<NJ>(a, x, s);
 #pragma unroll
       for (int j = 0; j < NJ; ++j) acc[j] += a.softmax ? s[j] : s[j] * n.inv;
-      const int index = select_topk<NJ>(a, t, x, s, b, lane);
-      float w = 0.0f;
-      if (index >= 0) {
-        const uint64_t row = a.logits + (a.bf16 ? 2ull : 4ull) * (uint64_t)((int64_t)t * a.stride);
-        w = score_of(a, n, a.bf16 ? bf16_lo(ld_global<uint16_t>(row + 2ull * index)) : ld_global<float>(row + 4ull * index));
-        atomicAdd(&cnt[index], 1);
-      }
-      if (a.normalize) w /= wave_sum(w) + 1e-20f;
-      if (lane < a.top_k) {
-        o.index[(int64_t)t * a.top_k + lane] = index;
-        o.weight[(int64_t)t * a.top_k + lane] = w * a.scale;
-      }
+      if (select_topk<NJ, false>(a, t, x, s, b, lane, cand[wave], &index, &w))
+        put_token(a, o, t, lane, index, w, cnt);
+      else
+        undecided |= 1u << i;
+    }
+    while (undecided) {
+      const int32_t t = lo + wave + W * __builtin_ctz(undecided);
+      undecided &= undecided - 1;
+      float x[NJ], s[NJ], w;
+      int index;
+      load_row<NJ>(a, t, lane, x);
+      const Norm n = scores<NJ>(a, x, s);
+      select_topk<NJ, true>(a, t, x, s, b, lane, cand[wave], &index, &w);
+      if (w < 0.0f) w = score_of(a, n, load_logit(a, t, index));
+      put_token(a, o, t, lane, index, w, cnt);
     }
 #pragma unroll
     for (int j = 0; j < NJ; ++j) sum[wave][lane + 64 * j] = acc[j];
     __syncthreads();
     const int64_t row = ((int64_t)blockIdx.x + q) * a.n_experts;
-    for (int e = threadIdx.x; e < a.n_experts; e += kThreads) {
-      o.part_p[row + e] = (sum[0][e] + sum[1][e]) + (sum[2][e] + sum[3][e]);
+    for (int e = threadIdx.x; e < a.n_experts; e += Threads) {
+      float p = sum[0][e];
+#pragma unroll
+      for (int i = 1; i < W; ++i) p += sum[i][e];
+      o.part_p[row + e] = p;
       o.part_c[row + e] = cnt[e];
     }
     __syncthreads();
   }
 }
 
-constexpr int kChunk = 16;  // experts of one workgroup in the reductions
-
-__device__ __forceinline__ double sum_of_16(double x, double *lds) {
-  // rows of 16 experts: thread = 16 row + expert; sums over the 16 rows
-  lds[threadIdx.x] = x;
-  __syncthreads();
-  for (int d = 8; d; d >>= 1) {
-    if ((int)(threadIdx.x >> 4) < d) lds[threadIdx.x] += lds[threadIdx.x + 16 * d];
-    __syncthreads();
-  }
-  const double r = lds[threadIdx.x & 15];
-  __syncthreads();
-  return r;
-}
+constexpr int kThreads = 256;  // of the reductions
+constexpr int kChunk = 16;     // experts of one of their workgroups
 
 // Per sequence and 16 experts: the tiles' partial sums, the counts, and these
 // experts' part of the loss.
 __global__ void __launch_bounds__(kThreads)
     router_reduce_kernel(RouterArgs a, const float *part_p, const int32_t *part_c, int32_t *seq_counts,
                          double *part_loss) {
-  __shared__ double lds[kThreads];
+  __shared__ double sp[kThreads];
+  __shared__ int sc[kThreads];
   const int32_t q = blockIdx.x, e = blockIdx.y * kChunk + (threadIdx.x & 15), row = threadIdx.x >> 4;
   const int32_t lo = seq_start(a, q), hi = seq_start(a, q + 1);
-  double p = 0.0, c = 0.0;
+  double p = 0.0;
+  int c = 0;
   if (hi > lo && e < a.n_experts) {
     const int32_t last = (hi - 1) / a.tile;
-    for (int32_t i = lo / a.tile + row; i <= last; i += 16) {
+#pragma unroll 4
+    for (int32_t i = lo / a.tile + row; i <= last; i += kThreads / kChunk) {
       const int64_t at = ((int64_t)i + q) * a.n_experts + e;
       p += (double)part_p[at];
-      c += (double)part_c[at];
+      c += part_c[at];
     }
   }
-  p = sum_of_16(p, lds);
-  c = sum_of_16(c, lds);
+  sp[threadIdx.x] = p;
+  sc[threadIdx.x] = c;
+  __syncthreads();
+  if (threadIdx.x >= 64) return;
   double part = 0.0;
-  if (row == 0 && e < a.n_experts) {
-    seq_counts[(int64_t)q * a.n_experts + e] = (int32_t)c;
+  if (threadIdx.x < kChunk && e < a.n_experts) {
+    p = 0.0;
+    c = 0;
+#pragma unroll
+    for (int i = 0; i < kThreads / kChunk; ++i) {
+      p += sp[kChunk * i + threadIdx.x];
+      c += sc[kChunk * i + threadIdx.x];
+    }
+    seq_counts[(int64_t)q * a.n_experts + e] = c;
     const double n = hi > lo ? (double)(hi - lo) : 1.0;
-    part = c * p / (n * n);
+    part = (double)c * p / (n * n);
   }
-  // over the 16 experts: lanes 0..15 of the first wave
-  if (threadIdx.x < 64) {
-    for (int d = 8; d; d >>= 1) part += __shfl_xor(part, d);
-    if (threadIdx.x == 0) part_loss[(int64_t)q * gridDim.y + blockIdx.y] = part;
-  }
+  for (int d = 8; d; d >>= 1) part += __shfl_xor(part, d);
+  if (threadIdx.x == 0) part_loss[(int64_t)q * gridDim.y + blockIdx.y] = part;
+}
+
+__device__ __forceinline__ float loss_of(const RouterArgs &a, double s) {
+  return (float)(s * (double)a.coef * (double)a.n_experts / ((double)a.top_k * (double)a.n_seqs));
 }
 
 // Block 0: the loss from its parts. The others: counts over all sequences of
@@ -345,25 +499,77 @@ __global__ void __launch_bounds__(kThreads)
 __global__ void __launch_bounds__(kThreads)
     router_finish_kernel(RouterArgs a, const int32_t *seq_counts, const double *part_loss, int64_t n_parts,
                          int32_t *counts, float *loss) {
-  __shared__ double lds[kThreads];
+  __shared__ double sp[kThreads / 64];
+  __shared__ int sc[kThreads];
   if (blockIdx.x == 0) {
     double s = 0.0;
     for (int64_t i = threadIdx.x; i < n_parts; i += kThreads) s += part_loss[i];
-    s = sum_of_16(s, lds);
-    if (threadIdx.x < 64) {
-      if (threadIdx.x >= 16) s = 0.0;
-      for (int d = 8; d; d >>= 1) s += __shfl_xor(s, d);
-      if (threadIdx.x == 0)
-        *loss = (float)(s * (double)a.coef * (double)a.n_experts / ((double)a.top_k * (double)a.n_seqs));
-    }
+    for (int d = 32; d; d >>= 1) s += __shfl_xor(s, d);
+    if ((threadIdx.x & 63) == 0) sp[threadIdx.x >> 6] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) *loss = loss_of(a, (sp[0] + sp[1]) + (sp[2] + sp[3]));
     return;
   }
   const int32_t e = (blockIdx.x - 1) * kChunk + (threadIdx.x & 15);
-  double c = 0.0;
+  int c = 0;
   if (e < a.n_experts)
-    for (int32_t q = threadIdx.x >> 4; q < a.n_seqs; q += 16) c += (double)seq_counts[(int64_t)q * a.n_experts + e];
-  c = sum_of_16(c, lds);
-  if (threadIdx.x < 16 && e < a.n_experts) counts[e] = (int32_t)c;
+    for (int32_t q = threadIdx.x >> 4; q < a.n_seqs; q += kThreads / kChunk) c += seq_counts[(int64_t)q * a.n_experts + e];
+  sc[threadIdx.x] = c;
+  __syncthreads();
+  if (threadIdx.x < kChunk && e < a.n_experts) {
+    c = 0;
+    for (int i = 0; i < kThreads / kChunk; ++i) c += sc[kChunk * i + threadIdx.x];
+    counts[e] = c;
+  }
+}
+
+// Both reductions in one workgroup, for few partial sums (a second launch
+// would cost more than the reads one after the other).
+constexpr int kSmallThreads = 1024;
+__global__ void __launch_bounds__(kSmallThreads)
+    router_small_kernel(RouterArgs a, const float *part_p, const int32_t *part_c, int32_t *seq_counts,
+                        int32_t *counts, float *loss) {
+  __shared__ double sp[kSmallThreads];
+  __shared__ int sc[kSmallThreads];
+  const int E = a.n_experts, rows = kSmallThreads / E, e = threadIdx.x % E, row = threadIdx.x / E;
+  double total = 0.0;
+  int all = 0;
+  for (int32_t q = 0; q < a.n_seqs; ++q) {
+    const int32_t lo = seq_start(a, q), hi = seq_start(a, q + 1);
+    double p = 0.0;
+    int c = 0;
+    if (hi > lo && row < rows) {
+      const int32_t last = (hi - 1) / a.tile;
+#pragma unroll 4
+      for (int32_t i = lo / a.tile + row; i <= last; i += rows) {
+        const int64_t at = ((int64_t)i + q) * E + e;
+        p += (double)part_p[at];
+        c += part_c[at];
+      }
+    }
+    sp[threadIdx.x] = p;
+    sc[threadIdx.x] = c;
+    __syncthreads();
+    if (row == 0) {
+      for (int i = 1; i < rows; ++i) {
+        p += sp[i * E + e];
+        c += sc[i * E + e];
+      }
+      seq_counts[(int64_t)q * E + e] = c;
+      all += c;
+      const double n = hi > lo ? (double)(hi - lo) : 1.0;
+      total += (double)c * p / (n * n);
+    }
+    __syncthreads();
+  }
+  if (row == 0 && counts) counts[e] = all;
+  for (int d = 32; d; d >>= 1) total += __shfl_xor(total, d);
+  if ((threadIdx.x & 63) == 0) sp[threadIdx.x >> 6] = total;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < kSmallThreads / 64; ++i) total += sp[i];
+    *loss = loss_of(a, total);
+  }
 }
 
 struct BackwardIo {
@@ -387,8 +593,9 @@ __device__ __forceinline__ void store_logit(const RouterArgs &a, uint64_t row, i
 // sequence and stays in registers; of the weights, the top_k values go to
 // their experts' lanes through the wave's row of shared memory.
 template <int NJ>
-__global__ void __launch_bounds__(kThreads) router_backward_kernel(RouterArgs a, BackwardIo o) {
-  __shared__ float direct[kWaves][64 * NJ];
+__global__ void __launch_bounds__(64 * kWavesOf<NJ>) router_backward_kernel(RouterArgs a, BackwardIo o) {
+  constexpr int W = kWavesOf<NJ>;
+  __shared__ float direct[W][64 * NJ];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   float *mine = direct[wave];
 #pragma unroll
@@ -403,14 +610,13 @@ __global__ void __launch_bounds__(kThreads) router_backward_kernel(RouterArgs a,
 #pragma unroll
     for (int j = 0; j < NJ; ++j) b[j] = 0.0f;
     if (q >= 0 && o.dloss) {
-      const double n = (double)(seq_start(a, q + 1) - seq_start(a, q));
-      const float f =
-          (float)((double)*o.dloss * (double)a.coef * a.n_experts / ((double)a.n_seqs * (double)a.top_k * n * n));
+      const float n = (float)(seq_start(a, q + 1) - seq_start(a, q));
+      const float f = *o.dloss * a.coef * (float)a.n_experts / ((float)a.n_seqs * (float)a.top_k) / n / n;
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
         if (lane + 64 * j < a.n_experts) b[j] = f * (float)o.seq_counts[(int64_t)q * a.n_experts + lane + 64 * j];
     }
-    for (int32_t t = lo + wave; t < hi; t += kWaves) {
+    for (int32_t t = lo + wave; t < hi; t += W) {
       const uint64_t drow = o.dlogits + size * (uint64_t)((int64_t)t * o.dstride);
       if (q < 0) {
 #pragma unroll
@@ -418,26 +624,26 @@ __global__ void __launch_bounds__(kThreads) router_backward_kernel(RouterArgs a,
           if (lane + 64 * j < a.n_experts) store_logit(a, drow, lane + 64 * j, 0.0f);
         continue;
       }
-      const uint64_t row = a.logits + size * (uint64_t)((int64_t)t * a.stride);
       int at = -1;
-      float d = 0.0f, sel = 0.0f;
+      float d = 0.0f, sel = 0.0f, xsel = 0.0f;
       if (o.dweight && lane < a.top_k) {
         at = o.index[(int64_t)t * a.top_k + lane];
         if (at < 0 || at >= a.n_experts) at = -1;
-        else d = o.dweight[(int64_t)t * a.top_k + lane] * a.scale;
+        d = o.dweight[(int64_t)t * a.top_k + lane] * a.scale;
       }
       float x[NJ], s[NJ];
       load_row<NJ>(a, t, lane, x);
+      if (at >= 0) xsel = load_logit(a, t, at);
+      else d = 0.0f;
       const Norm n = scores<NJ>(a, x, s);
       if (o.dweight) {
-        if (at >= 0)
-          sel = score_of(a, n, a.bf16 ? bf16_lo(ld_global<uint16_t>(row + 2ull * at)) : ld_global<float>(row + 4ull * at));
+        if (at >= 0) sel = score_of(a, n, xsel);
         if (a.normalize) {
           const float z = wave_sum(sel) + 1e-20f;
           d = (d - wave_sum(d * sel) / z) / z;
         }
         if (at >= 0) atomicAdd(&mine[at], d);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        wave_lds_fence();
       }
       float g[NJ], dot = 0.0f;
 #pragma unroll
@@ -446,9 +652,9 @@ __global__ void __launch_bounds__(kThreads) router_backward_kernel(RouterArgs a,
         dot += (a.softmax ? b[j] + g[j] : b[j]) * s[j];
       }
       if (o.dweight) {
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        wave_lds_fence();
         if (at >= 0) mine[at] = 0.0f;
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        wave_lds_fence();
       }
       dot = wave_sum(dot);
 #pragma unroll
@@ -464,22 +670,32 @@ __global__ void __launch_bounds__(kThreads) router_backward_kernel(RouterArgs a,
 }
 
 // Tokens of one workgroup.
+#ifndef ROUTER_TILE
+#define ROUTER_TILE 0
+#endif
 int32_t tile_of(int64_t n_tokens) {
-  int32_t tile = 4;
-  while (tile < 64 && n_tokens > (int64_t)tile * 1024) tile *= 2;
-  return tile;
+  if (ROUTER_TILE) return ROUTER_TILE;
+  return n_tokens <= 8192 ? 16 : n_tokens <= 16384 ? 32 : 64;
 }
+
+// Partial sums up to which one workgroup reduces them.
+#ifndef ROUTER_SMALL
+#define ROUTER_SMALL 32768
+#endif
+constexpr int64_t kSmallSums = ROUTER_SMALL;
+constexpr int32_t kSmallSeqs = 8;
 
 int chunks_of(int n_experts) { return (n_experts + kChunk - 1) / kChunk; }
 
 struct Workspace {
-  int64_t part_p, part_c, part_loss, bytes;
+  int64_t rows, part_p, part_c, part_loss, bytes;
 };
 
 Workspace workspace_of(const wt_router_desc &d) {
   const int64_t tile = tile_of(d.n_tokens);
   const int64_t rows = (d.n_tokens + tile - 1) / tile + d.n_seqs;
   Workspace w;
+  w.rows = rows;
   w.part_p = 0;
   w.part_c = 4 * rows * d.n_experts;
   w.part_loss = (w.part_c + 4 * rows * d.n_experts + 15) / 16 * 16;
@@ -594,13 +810,19 @@ wt_status wt_router_forward(const wt_router_desc *desc, int32_t *index, float *w
     const uint32_t tiles = (uint32_t)((a.n_tokens + a.tile - 1) / a.tile), chunks = (uint32_t)chunks_of(a.n_experts);
     if (tiles > 0)
       with_columns(a.n_experts, [&](auto nj) {
-        hipLaunchKernelGGL((router_forward_kernel<decltype(nj)::value>), dim3(tiles), dim3(kThreads), 0, s, a,
+        constexpr int N = decltype(nj)::value;
+        hipLaunchKernelGGL((router_forward_kernel<N>), dim3(tiles), dim3(64 * kWavesOf<N>), 0, s, a,
                            ForwardOut{index, weight, part_p, part_c});
       });
-    hipLaunchKernelGGL(router_reduce_kernel, dim3((uint32_t)a.n_seqs, chunks), dim3(kThreads), 0, s, a, part_p, part_c,
-                       seq_counts, part_loss);
-    hipLaunchKernelGGL(router_finish_kernel, dim3(counts ? 1 + chunks : 1), dim3(kThreads), 0, s, a, seq_counts,
-                       part_loss, (int64_t)a.n_seqs * chunks, counts, loss);
+    if (a.n_seqs <= kSmallSeqs && w.rows * a.n_experts <= kSmallSums) {
+      hipLaunchKernelGGL(router_small_kernel, dim3(1), dim3(kSmallThreads), 0, s, a, part_p, part_c, seq_counts, counts,
+                         loss);
+    } else {
+      hipLaunchKernelGGL(router_reduce_kernel, dim3((uint32_t)a.n_seqs, chunks), dim3(kThreads), 0, s, a, part_p,
+                         part_c, seq_counts, part_loss);
+      hipLaunchKernelGGL(router_finish_kernel, dim3(counts ? 1 + chunks : 1), dim3(kThreads), 0, s, a, seq_counts,
+                         part_loss, (int64_t)a.n_seqs * chunks, counts, loss);
+    }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return fail(what, hip_msg("launch", e), WT_E_HIP);
     return WT_OK;
@@ -634,8 +856,9 @@ wt_status wt_router_backward(const wt_router_desc *desc, const int32_t *index, c
     const uint32_t tiles = (uint32_t)((a.n_tokens + a.tile - 1) / a.tile);
     const BackwardIo io{index, seq_counts, dweight, dloss, (uint64_t)(uintptr_t)dlogits, dlogits_stride};
     with_columns(a.n_experts, [&](auto nj) {
-      hipLaunchKernelGGL((router_backward_kernel<decltype(nj)::value>), dim3(tiles), dim3(kThreads), 0,
-                         (hipStream_t)stream, a, io);
+      constexpr int N = decltype(nj)::value;
+      hipLaunchKernelGGL((router_backward_kernel<N>), dim3(tiles), dim3(64 * kWavesOf<N>), 0, (hipStream_t)stream, a,
+                         io);
     });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return fail(what, hip_msg("launch", e), WT_E_HIP);

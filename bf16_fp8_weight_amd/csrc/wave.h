@@ -42,6 +42,17 @@ __device__ __forceinline__ float wave_max(float m) {
   return lane63(m);
 }
 
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t m) {
+  m = lanes_max<16>(m);
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp((int)m, (int)m, 0x142, 0xA, 0xF, false));
+  m = max(m, (uint32_t)__builtin_amdgcn_update_dpp((int)m, (int)m, 0x143, 0xC, 0xF, false));
+  return (uint32_t)__builtin_amdgcn_readlane((int)m, 63);
+}
+
+// Orders a wave's accesses to shared memory that only this wave touches: what
+// its lanes wrote before is what any of them reads behind.
+__device__ __forceinline__ void wave_lds_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
+
 __device__ __forceinline__ float wave_sum(float x) {
   x += dpp_f32<0x0B1, 0xF>(0.0f, x);
   x += dpp_f32<0x04E, 0xF>(0.0f, x);

@@ -82,22 +82,33 @@ struct Runs {
   }
 };
 
+// The wave's number in its workgroup, known to be uniform: what depends on it
+// (the token, its rows' addresses) then lives in scalar registers.
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
+__device__ __forceinline__ uint64_t row_of(uint64_t base, int64_t t, int64_t stride, bool bf16) {
+  return base + (uint64_t)(t * stride) * (bf16 ? 2u : 4u);
+}
+
+__device__ __forceinline__ float load_at(uint64_t row, uint32_t e, bool bf16) {
+  return bf16 ? bf16_lo(ld_global<uint16_t>(row + 2u * e)) : ld_global<float>(row + 4u * e);
+}
+
+__device__ __forceinline__ float load_logit(const RouterArgs &a, int64_t t, uint32_t e) {
+  return load_at(row_of(a.logits, t, a.stride, a.bf16), e, a.bf16);
+}
+
 // A token's logits: lane l holds experts l, l + 64, ... (-infinity beyond the last).
 template <int NJ>
 __device__ __forceinline__ void load_row(const RouterArgs &a, int64_t t, int lane, float x[NJ]) {
-  const uint64_t row = a.logits + (a.bf16 ? 2ull : 4ull) * (uint64_t)(t * a.stride);
+  const uint64_t row = row_of(a.logits, t, a.stride, a.bf16);
+  if (a.bf16) {
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    const int e = lane + 64 * j;
-    x[j] = -INFINITY;
-    if (e < a.n_experts)
-      x[j] = a.bf16 ? bf16_lo(ld_global<uint16_t>(row + 2ull * e)) : ld_global<float>(row + 4ull * e);
+    for (int j = 0; j < NJ; ++j) x[j] = lane + 64 * j < a.n_experts ? load_at(row, lane + 64 * j, true) : -INFINITY;
+  } else {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) x[j] = lane + 64 * j < a.n_experts ? load_at(row, lane + 64 * j, false) : -INFINITY;
   }
-}
-
-__device__ __forceinline__ float load_logit(const RouterArgs &a, int64_t t, int e) {
-  const uint64_t row = a.logits + (a.bf16 ? 2ull : 4ull) * (uint64_t)(t * a.stride);
-  return a.bf16 ? bf16_lo(ld_global<uint16_t>(row + 2ull * e)) : ld_global<float>(row + 4ull * e);
 }
 
 // What turns a logit into its score (softmax: exp(x - top) inv) and a score
@@ -133,11 +144,11 @@ __device__ __forceinline__ Norm scores(const RouterArgs &a, const float x[NJ], f
   }
   z = wave_sum(z);
   if (a.softmax) {
-    n.inv = z == 0.0f ? 0.0f : 1.0f / z;
+    n.inv = z == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(z);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) s[j] *= n.inv;
   } else {
-    n.inv = 1.0f / (z + 1e-20f);
+    n.inv = __builtin_amdgcn_rcpf(z + 1e-20f);
   }
   return n;
 }
@@ -147,12 +158,16 @@ __device__ __forceinline__ bool selectable(float x) { return x > -INFINITY; }  /
 // Top and sum of a softmax in 64 bits.
 __device__ __forceinline__ void softmax64(const RouterArgs &a, int64_t t, int lane, double *top, double *z) {
   double m = -INFINITY, sum = 0.0;
+#pragma unroll 1
   for (int e = lane; e < a.n_experts; e += 64) {
     const float x = load_logit(a, t, e);
     m = fmax(m, selectable(x) ? (double)x : -INFINITY);
   }
+#pragma unroll 1
   for (int d = 32; d; d >>= 1) m = fmax(m, __shfl_xor(m, d));
+#pragma unroll 1
   for (int e = lane; e < a.n_experts; e += 64) sum += exp((double)load_logit(a, t, e) - m);
+#pragma unroll 1
   for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
   *top = m;
   *z = sum;
@@ -172,14 +187,17 @@ __device__ __forceinline__ int select_rounds(const RouterArgs &a, int64_t t, int
   int index = -1;
   double last = INFINITY;
   int last_e = -1;
+#pragma unroll 1
   for (int r = 0; r < a.top_k; ++r) {
     // the greatest key behind the last one taken, and of equals the lowest expert
     double best = -INFINITY;
     int at = kMaxExperts;
+#pragma unroll 1
     for (int e = lane; e < a.n_experts; e += 64) {
       const double k = exact_key(a, t, e, top, z);
       if ((k < last || (k == last && e > last_e)) && k > best) best = k, at = e;
     }
+#pragma unroll 1
     for (int d = 32; d; d >>= 1) {
       const double ob = __shfl_xor(best, d);
       const int oa = __shfl_xor(at, d);
@@ -311,6 +329,7 @@ __device__ __forceinline__ bool select_topk(const RouterArgs &a, int64_t t, cons
     const uint64_t close = __ballot(pair && k0 - k1 <= near_tie(a, k0, most));
     if (close & ((2ull << (a.top_k - 1)) - 1)) {
       int from = 0;  // the lane that holds rank `lane`
+#pragma unroll 1
       for (int i = 0; i < count; ++i)
         if (__builtin_amdgcn_readlane(rank, i) == lane) from = i;
       const float xe = lane < count ? load_logit(a, t, ex) : 0.0f, be = lane < count ? a.bias[ex] : 0.0f;
@@ -337,6 +356,7 @@ __device__ __forceinline__ bool select_topk(const RouterArgs &a, int64_t t, cons
     }
     const double mine = lane < count ? exact_key(a, t, c.expert[lane], top64, z64) : 0.0;
     rank = lane < count ? 0 : lane;
+#pragma unroll 1
     for (int i = 0; i < count; ++i) {
       const double other = __shfl(mine, i);
       rank += lane < count && (other > mine || (other == mine && i < lane)) ? 1 : 0;
@@ -367,7 +387,7 @@ struct ForwardOut {
 __device__ __forceinline__ void put_token(const RouterArgs &a, const ForwardOut &o, int32_t t, int lane, int index,
                                           float score, int *cnt) {
   float w = score;
-  if (a.normalize) w /= wave_sum(w) + 1e-20f;
+  if (a.normalize) w *= __builtin_amdgcn_rcpf(wave_sum(w) + 1e-20f);
   if (index >= 0) atomicAdd(&cnt[index], 1);
   if (lane < a.top_k) {
     o.index[(int64_t)t * a.top_k + lane] = index;
@@ -375,21 +395,23 @@ __device__ __forceinline__ void put_token(const RouterArgs &a, const ForwardOut 
   }
 }
 
-// Forward pass over tokens. One wave per token; a workgroup's tile of tokens
-// is cut at the sequences' borders, and the tokens that tile i shares with
-// sequence q leave their sums at row i + q: along the tokens each step to the
-// next pair raises i or q, so no two pairs share a row, no sum needs an
-// atomic, and the order of every sum is fixed.
+// Forward pass over tokens, a wave to a token, its next row's loads ahead of
+// it. A workgroup's tile of tokens is cut at the sequences' borders, and the
+// tokens that tile i shares with sequence q leave their sums at row i + q:
+// along the tokens each step to the next pair raises i or q, so no two pairs
+// share a row, no sum needs an atomic, and the order of every sum is fixed.
 template <int NJ>
 __global__ void __launch_bounds__(64 * kWavesOf<NJ>) router_forward_kernel(RouterArgs a, ForwardOut o) {
   constexpr int W = kWavesOf<NJ>, Threads = 64 * W;
   __shared__ float sum[W][64 * NJ];
   __shared__ int cnt[64 * NJ];
   __shared__ Candidates cand[W];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = wave_id();
   const int32_t first = blockIdx.x * a.tile;
   const int32_t last = a.n_tokens - first < a.tile ? a.n_tokens : first + a.tile;
-  float b[NJ];
+  int32_t t = first + wave;  // this wave's next token
+  float ahead[NJ], b[NJ];
+  if (t < last) load_row<NJ>(a, t, lane, ahead);
 #pragma unroll
   for (int j = 0; j < NJ; ++j) b[j] = a.bias && lane + 64 * j < a.n_experts ? a.bias[lane + 64 * j] : 0.0f;
   Runs runs(a, first, last);
@@ -400,6 +422,8 @@ __global__ void __launch_bounds__(64 * kWavesOf<NJ>) router_forward_kernel(Route
         o.index[i] = -1;
         o.weight[i] = 0.0f;
       }
+      while (t < hi) t += W;
+      if (t < last) load_row<NJ>(a, t, lane, ahead);
       continue;
     }
     for (int e = threadIdx.x; e < a.n_experts; e += Threads) cnt[e] = 0;
@@ -407,32 +431,34 @@ __global__ void __launch_bounds__(64 * kWavesOf<NJ>) router_forward_kernel(Route
     float acc[NJ];
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[j] = 0.0f;
-    uint32_t undecided = 0;  // bit i: token lo + wave + W i (a tile holds at most 8 for a wave)
-    for (int32_t t = lo + wave, i = 0; t < hi; t += W, ++i) {
+    uint32_t undecided = 0;  // bit i: the i-th of this wave's tokens in the tile (8 at most)
+    for (; t < hi; t += W) {
       float x[NJ], s[NJ], w;
       int index;
-      load_row<NJ>(a, t, lane, x);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) x[j] = ahead[j];
+      if (t + W < last) load_row<NJ>(a, t + W, lane, ahead);
       const Norm n = scores<NJ>(a, x, s);
 #pragma unroll
       for (int j = 0; j < NJ; ++j) acc[j] += a.softmax ? s[j] : s[j] * n.inv;
       if (select_topk<NJ, false>(a, t, x, s, b, lane, cand[wave], &index, &w))
         put_token(a, o, t, lane, index, w, cnt);
       else
-        undecided |= 1u << i;
-    }
-    while (undecided) {
-      const int32_t t = lo + wave + W * __builtin_ctz(undecided);
-      undecided &= undecided - 1;
-      float x[NJ], s[NJ], w;
-      int index;
-      load_row<NJ>(a, t, lane, x);
-      const Norm n = scores<NJ>(a, x, s);
-      select_topk<NJ, true>(a, t, x, s, b, lane, cand[wave], &index, &w);
-      if (w < 0.0f) w = score_of(a, n, load_logit(a, t, index));
-      put_token(a, o, t, lane, index, w, cnt);
+        undecided |= 1u << ((t - first) / W);
     }
 #pragma unroll
     for (int j = 0; j < NJ; ++j) sum[wave][lane + 64 * j] = acc[j];
+    while (undecided) {
+      const int32_t again = first + wave + W * __builtin_ctz(undecided);
+      undecided &= undecided - 1;
+      float x[NJ], s[NJ], w;
+      int index;
+      load_row<NJ>(a, again, lane, x);
+      const Norm n = scores<NJ>(a, x, s);
+      select_topk<NJ, true>(a, again, x, s, b, lane, cand[wave], &index, &w);
+      if (w < 0.0f) w = score_of(a, n, load_logit(a, again, index));
+      put_token(a, o, again, lane, index, w, cnt);
+    }
     __syncthreads();
     const int64_t row = ((int64_t)blockIdx.x + q) * a.n_experts;
     for (int e = threadIdx.x; e < a.n_experts; e += Threads) {
@@ -581,91 +607,116 @@ struct BackwardIo {
   int64_t dstride;
 };
 
-__device__ __forceinline__ void store_logit(const RouterArgs &a, uint64_t row, int e, float x) {
-  if (a.bf16)
-    st_global<uint16_t>(row + 2ull * e, __builtin_bit_cast(uint16_t, (__bf16)x));
-  else
-    st_global<float>(row + 4ull * e, x);
+template <int NJ>
+__device__ __forceinline__ void store_row(uint64_t row, int n, bool bf16, int lane, const float x[NJ]) {
+  if (bf16) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      if (lane + 64 * j < n) st_global<uint16_t>(row + 2u * (uint32_t)(lane + 64 * j), __builtin_bit_cast(uint16_t, (__bf16)x[j]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      if (lane + 64 * j < n) st_global<float>(row + 4u * (uint32_t)(lane + 64 * j), x[j]);
+  }
 }
 
-// Backward pass: one wave per token, scores recomputed from the logits (which
+// Backward pass, a wave to a token, scores recomputed from the logits (which
 // have to be read anyway). Of the loss, d/dp_e is the same for all tokens of a
-// sequence and stays in registers; of the weights, the top_k values go to
-// their experts' lanes through the wave's row of shared memory.
+// sequence and stays in registers; of the weights, the top_k values meet their
+// experts' lanes in the wave's row of shared memory: first the scores lie
+// there for the selected to be picked up, then the selected's gradients.
+constexpr int kBackWaves = 4;
 template <int NJ>
-__global__ void __launch_bounds__(64 * kWavesOf<NJ>) router_backward_kernel(RouterArgs a, BackwardIo o) {
-  constexpr int W = kWavesOf<NJ>;
-  __shared__ float direct[W][64 * NJ];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  float *mine = direct[wave];
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) mine[lane + 64 * j] = 0.0f;
+__global__ void __launch_bounds__(64 * kBackWaves) router_backward_kernel(RouterArgs a, BackwardIo o) {
+  constexpr int W = kBackWaves;
+  __shared__ float rows[W][64 * NJ];
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  float *row = rows[wave];
   const int32_t first = blockIdx.x * a.tile;
   const int32_t last = a.n_tokens - first < a.tile ? a.n_tokens : first + a.tile;
-  const uint64_t size = a.bf16 ? 2 : 4;
-  Runs runs(a, first, last);
-  int32_t lo, hi, q;
-  while (runs.next(a, &lo, &hi, &q)) {
-    float b[NJ];
+  int32_t t = first + wave;
+  if (t >= last) return;
+  const bool chosen = o.dweight && lane < a.top_k;  // this lane carries a selected expert
+  float ahead[NJ], dw = 0.0f;
+  int at = -1;
+  load_row<NJ>(a, t, lane, ahead);
+  if (chosen) {
+    at = o.index[(int64_t)t * a.top_k + lane];
+    dw = o.dweight[(int64_t)t * a.top_k + lane];
+  }
+  const float dloss = o.dloss ? *o.dloss : 0.0f;
+  int32_t q = seq_of(a, t), start = 0, stop = -1;  // [start, stop): of sequence q, or the padding before or behind
+  bool padding = false;
+  float b[NJ];
+  for (; t < last; t += W) {
+    if (t >= stop) {
+      start = stop = a.n_tokens;
+      for (; q < a.n_seqs; ++q) {
+        start = seq_start(a, q);
+        stop = seq_start(a, q + 1);
+        if (stop > t) break;
+      }
+      padding = q >= a.n_seqs || start > t;
+      if (padding) stop = q < a.n_seqs ? start : a.n_tokens;
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) b[j] = 0.0f;
-    if (q >= 0 && o.dloss) {
-      const float n = (float)(seq_start(a, q + 1) - seq_start(a, q));
-      const float f = *o.dloss * a.coef * (float)a.n_experts / ((float)a.n_seqs * (float)a.top_k) / n / n;
-#pragma unroll
-      for (int j = 0; j < NJ; ++j)
-        if (lane + 64 * j < a.n_experts) b[j] = f * (float)o.seq_counts[(int64_t)q * a.n_experts + lane + 64 * j];
-    }
-    for (int32_t t = lo + wave; t < hi; t += W) {
-      const uint64_t drow = o.dlogits + size * (uint64_t)((int64_t)t * o.dstride);
-      if (q < 0) {
+      for (int j = 0; j < NJ; ++j) b[j] = 0.0f;
+      if (!padding && o.dloss) {
+        const float n = (float)(stop - start);
+        const float f = dloss * a.coef * (float)a.n_experts / ((float)a.n_seqs * (float)a.top_k) / n / n;
+        const int32_t *c = o.seq_counts + (int64_t)q * a.n_experts;
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
-          if (lane + 64 * j < a.n_experts) store_logit(a, drow, lane + 64 * j, 0.0f);
-        continue;
-      }
-      int at = -1;
-      float d = 0.0f, sel = 0.0f, xsel = 0.0f;
-      if (o.dweight && lane < a.top_k) {
-        at = o.index[(int64_t)t * a.top_k + lane];
-        if (at < 0 || at >= a.n_experts) at = -1;
-        d = o.dweight[(int64_t)t * a.top_k + lane] * a.scale;
-      }
-      float x[NJ], s[NJ];
-      load_row<NJ>(a, t, lane, x);
-      if (at >= 0) xsel = load_logit(a, t, at);
-      else d = 0.0f;
-      const Norm n = scores<NJ>(a, x, s);
-      if (o.dweight) {
-        if (at >= 0) sel = score_of(a, n, xsel);
-        if (a.normalize) {
-          const float z = wave_sum(sel) + 1e-20f;
-          d = (d - wave_sum(d * sel) / z) / z;
-        }
-        if (at >= 0) atomicAdd(&mine[at], d);
-        wave_lds_fence();
-      }
-      float g[NJ], dot = 0.0f;
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        g[j] = o.dweight ? mine[lane + 64 * j] : 0.0f;
-        dot += (a.softmax ? b[j] + g[j] : b[j]) * s[j];
-      }
-      if (o.dweight) {
-        wave_lds_fence();
-        if (at >= 0) mine[at] = 0.0f;
-        wave_lds_fence();
-      }
-      dot = wave_sum(dot);
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const int e = lane + 64 * j;
-        if (e >= a.n_experts) continue;
-        const float dx = a.softmax ? s[j] * (b[j] + g[j] - dot)
-                                   : ((b[j] - dot * n.inv) * n.inv + g[j]) * s[j] * (1.0f - s[j]);
-        store_logit(a, drow, e, dx);
+          if (lane + 64 * j < a.n_experts) b[j] = f * (float)c[lane + 64 * j];
       }
     }
+    float x[NJ], s[NJ], g[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) x[j] = ahead[j];
+    const int sel = at >= 0 && at < a.n_experts ? at : -1;
+    float d = sel >= 0 ? dw * a.scale : 0.0f;
+    if (t + W < last) {
+      load_row<NJ>(a, t + W, lane, ahead);
+      if (chosen) {
+        at = o.index[(int64_t)(t + W) * a.top_k + lane];
+        dw = o.dweight[(int64_t)(t + W) * a.top_k + lane];
+      }
+    }
+    const uint64_t drow = row_of(o.dlogits, t, o.dstride, a.bf16);
+    if (padding) {
+      store_row<NJ>(drow, a.n_experts, a.bf16, lane, b);  // zeros
+      continue;
+    }
+    const Norm n = scores<NJ>(a, x, s);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) g[j] = 0.0f;
+    if (o.dweight) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) row[lane + 64 * j] = s[j];
+      wave_lds_fence();
+      const float ss = sel >= 0 ? row[sel] : 0.0f;
+      wave_lds_fence();
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) row[lane + 64 * j] = 0.0f;
+      if (a.normalize) {
+        const float r = __builtin_amdgcn_rcpf(wave_sum(ss) + 1e-20f), ds = wave_sum(d * ss);
+        if (sel >= 0) d = (d - ds * r) * r;
+      }
+      wave_lds_fence();
+      if (sel >= 0) atomicAdd(&row[sel], d);
+      wave_lds_fence();
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) g[j] = row[lane + 64 * j];
+      wave_lds_fence();
+    }
+    float dot = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) dot += (a.softmax ? b[j] + g[j] : b[j]) * s[j];
+    dot = wave_sum(dot);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      g[j] = a.softmax ? s[j] * (b[j] + g[j] - dot)
+                       : ((b[j] - dot * n.inv) * n.inv + g[j]) * s[j] * (1.0f - s[j]);
+    store_row<NJ>(drow, a.n_experts, a.bf16, lane, g);
   }
 }
 
@@ -676,6 +727,13 @@ __global__ void __launch_bounds__(64 * kWavesOf<NJ>) router_backward_kernel(Rout
 int32_t tile_of(int64_t n_tokens) {
   if (ROUTER_TILE) return ROUTER_TILE;
   return n_tokens <= 8192 ? 16 : n_tokens <= 16384 ? 32 : 64;
+}
+#ifndef BACK_TILE
+#define BACK_TILE 0
+#endif
+int32_t back_tile_of(int64_t n_tokens) {
+  if (BACK_TILE) return BACK_TILE;
+  return n_tokens <= 8192 ? 4 : n_tokens <= 16384 ? 8 : 16;
 }
 
 // Partial sums up to which one workgroup reduces them.
@@ -852,12 +910,13 @@ wt_status wt_router_backward(const wt_router_desc *desc, const int32_t *index, c
       return fail(what, "dlogits misaligned", WT_E_ALIGN);
     if (dlogits == desc->logits && dlogits_stride != desc->logits_stride)
       return fail(what, "dlogits on the logits with another stride", WT_E_OVERLAP);
-    const RouterArgs a = args_of(*desc);
+    RouterArgs a = args_of(*desc);
+    a.tile = back_tile_of(a.n_tokens);
     const uint32_t tiles = (uint32_t)((a.n_tokens + a.tile - 1) / a.tile);
     const BackwardIo io{index, seq_counts, dweight, dloss, (uint64_t)(uintptr_t)dlogits, dlogits_stride};
     with_columns(a.n_experts, [&](auto nj) {
       constexpr int N = decltype(nj)::value;
-      hipLaunchKernelGGL((router_backward_kernel<N>), dim3(tiles), dim3(64 * kWavesOf<N>), 0, (hipStream_t)stream, a,
+      hipLaunchKernelGGL((router_backward_kernel<N>), dim3(tiles), dim3(64 * kBackWaves), 0, (hipStream_t)stream, a,
                          io);
     });
     const hipError_t e = hipGetLastError();

@@ -98,17 +98,22 @@ __device__ __forceinline__ float load_logit(const RouterArgs &a, int64_t t, uint
   return load_at(row_of(a.logits, t, a.stride, a.bf16), e, a.bf16);
 }
 
-// A token's logits: lane l holds experts l, l + 64, ... (-infinity beyond the last).
+// A token's logits: lane l holds experts l, l + 64, ... (-infinity beyond the
+// last; those lanes read the last one's address, so that no load waits for a
+// branch).
 template <int NJ>
-__device__ __forceinline__ void load_row(const RouterArgs &a, int64_t t, int lane, float x[NJ]) {
+__device__ __forceinline__ void load_row(const RouterArgs &a, int64_t t, uint32_t lane, float x[NJ]) {
   const uint64_t row = row_of(a.logits, t, a.stride, a.bf16);
+  const uint32_t end = (uint32_t)a.n_experts - 1;
   if (a.bf16) {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) x[j] = lane + 64 * j < a.n_experts ? load_at(row, lane + 64 * j, true) : -INFINITY;
+    for (int j = 0; j < NJ; ++j) x[j] = load_at(row, min(lane + 64 * j, end), true);
   } else {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) x[j] = lane + 64 * j < a.n_experts ? load_at(row, lane + 64 * j, false) : -INFINITY;
+    for (int j = 0; j < NJ; ++j) x[j] = load_at(row, min(lane + 64 * j, end), false);
   }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) x[j] = lane + 64 * j <= end ? x[j] : -INFINITY;
 }
 
 // What turns a logit into its score (softmax: exp(x - top) inv) and a score
@@ -122,14 +127,15 @@ struct Norm {
 // result is below 1 (all there is here: 1 / (1 + exp) and exp(x - top)).
 __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
 
-__device__ __forceinline__ float score_of(const RouterArgs &a, const Norm &n, float x) {
-  return a.softmax ? fast_exp(x - n.top) * n.inv : __builtin_amdgcn_rcpf(1.0f + fast_exp(-x));
+template <bool Softmax>
+__device__ __forceinline__ float score_of(const Norm &n, float x) {
+  return Softmax ? fast_exp(x - n.top) * n.inv : __builtin_amdgcn_rcpf(1.0f + fast_exp(-x));
 }
 
-template <int NJ>
-__device__ __forceinline__ Norm scores(const RouterArgs &a, const float x[NJ], float s[NJ]) {
+template <int NJ, bool Softmax>
+__device__ __forceinline__ Norm scores(const float x[NJ], float s[NJ]) {
   Norm n{0.0f, 1.0f};
-  if (a.softmax) {
+  if (Softmax) {
     float m = x[0];
 #pragma unroll
     for (int j = 1; j < NJ; ++j) m = fmaxf(m, x[j]);
@@ -139,11 +145,11 @@ __device__ __forceinline__ Norm scores(const RouterArgs &a, const float x[NJ], f
   float z = 0.0f;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    s[j] = score_of(a, n, x[j]);
+    s[j] = score_of<Softmax>(n, x[j]);
     z += s[j];
   }
   z = wave_sum(z);
-  if (a.softmax) {
+  if (Softmax) {
     n.inv = z == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(z);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) s[j] *= n.inv;
@@ -217,8 +223,9 @@ __device__ __forceinline__ int select_rounds(const RouterArgs &a, int64_t t, int
 // from v_rcp_f32; for softmax, of the score, 2 from the exponential, 1 / e from
 // its argument, 24 from the sum over the experts, 2 from quotient and product;
 // and 1 of the key from the sum with the bias. Twice that for a pair.
-__device__ __forceinline__ float near_tie(const RouterArgs &a, float key, float score) {
-  return 0x1p-23f * ((a.softmax ? 0.5f + 28.0f * score : 3.8f) + fabsf(key));
+template <bool Softmax>
+__device__ __forceinline__ float near_tie(float key, float score) {
+  return 0x1p-23f * ((Softmax ? 0.5f + 28.0f * score : 3.8f) + fabsf(key));
 }
 
 // A wave's candidates of a selection.
@@ -276,13 +283,13 @@ __device__ __forceinline__ int collect(const uint32_t k[NJ], const float s[NJ], 
 // are too close and not of the same logit and bias, the token is not decided;
 // neither is one with more than 64 candidates. Exact takes such a token again:
 // all experts that may belong to the first top_k ranked by keys in 64 bits.
-template <int NJ, bool Exact>
+template <int NJ, bool Softmax, bool Bias, bool Exact>
 __device__ __forceinline__ bool select_topk(const RouterArgs &a, int64_t t, const float x[NJ], const float s[NJ],
                                             const float b[NJ], int lane, Candidates &c, int *index, float *score) {
   uint32_t k[NJ], h = 0;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    const float key = a.bias ? s[j] + b[j] : x[j];
+    const float key = Bias ? s[j] + b[j] : x[j];
     k[j] = selectable(x[j]) && selectable(key) ? ordered(key) : 0u;
     h = max(h, k[j]);
   }
@@ -314,7 +321,7 @@ __device__ __forceinline__ bool select_topk(const RouterArgs &a, int64_t t, cons
     rank += lane < count && other > key - (lane > i ? 1u : 0u) ? 1 : 0;
   }
   if (count > 64 && !Exact) return false;
-  if (a.bias && !Exact) {
+  if (Bias && !Exact) {
     // neighbours by rank
     const float sc = c.score[lane];
     const int ex = c.expert[lane];
@@ -325,8 +332,8 @@ __device__ __forceinline__ bool select_topk(const RouterArgs &a, int64_t t, cons
     const float k0 = from_ordered(c.key[lane]), k1 = from_ordered(c.key[(lane + 1) & 63]);
     wave_lds_fence();
     // the greatest score of a candidate bounds the pair's
-    const float most = a.softmax ? wave_max(lane < count ? sc : 0.0f) : 0.0f;
-    const uint64_t close = __ballot(pair && k0 - k1 <= near_tie(a, k0, most));
+    const float most = Softmax ? wave_max(lane < count ? sc : 0.0f) : 0.0f;
+    const uint64_t close = __ballot(pair && k0 - k1 <= near_tie<Softmax>(k0, most));
     if (close & ((2ull << (a.top_k - 1)) - 1)) {
       int from = 0;  // the lane that holds rank `lane`
 #pragma unroll 1
@@ -342,10 +349,10 @@ __device__ __forceinline__ bool select_topk(const RouterArgs &a, int64_t t, cons
   }
   if (Exact) {
     double top64 = 0.0, z64 = 1.0;
-    if (a.softmax && a.bias) softmax64(a, t, lane, &top64, &z64);
+    if (Softmax && Bias) softmax64(a, t, lane, &top64, &z64);
     if (count <= 64 && count > a.top_k) {  // everything within reach of the last place
       const float last = from_ordered(__builtin_amdgcn_readlane(key, __builtin_ctzll(__ballot(rank == a.top_k - 1))));
-      const float reach = last - near_tie(a, last, a.softmax ? 1.0f : 0.0f);
+      const float reach = last - near_tie<Softmax>(last, Softmax ? 1.0f : 0.0f);
       wave_lds_fence();
       count = collect<NJ>(k, s, min(lo, ordered(reach)), lane, c);
     }
@@ -400,7 +407,7 @@ __device__ __forceinline__ void put_token(const RouterArgs &a, const ForwardOut 
 // tokens that tile i shares with sequence q leave their sums at row i + q:
 // along the tokens each step to the next pair raises i or q, so no two pairs
 // share a row, no sum needs an atomic, and the order of every sum is fixed.
-template <int NJ>
+template <int NJ, bool Softmax, bool Bias>
 __global__ void __launch_bounds__(64 * kWavesOf<NJ>) router_forward_kernel(RouterArgs a, ForwardOut o) {
   constexpr int W = kWavesOf<NJ>, Threads = 64 * W;
   __shared__ float sum[W][64 * NJ];
@@ -413,7 +420,7 @@ __global__ void __launch_bounds__(64 * kWavesOf<NJ>) router_forward_kernel(Route
   float ahead[NJ], b[NJ];
   if (t < last) load_row<NJ>(a, t, lane, ahead);
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) b[j] = a.bias && lane + 64 * j < a.n_experts ? a.bias[lane + 64 * j] : 0.0f;
+  for (int j = 0; j < NJ; ++j) b[j] = Bias ? a.bias[min(lane + 64 * j, a.n_experts - 1)] : 0.0f;
   Runs runs(a, first, last);
   int32_t lo, hi, q;
   while (runs.next(a, &lo, &hi, &q)) {
@@ -438,10 +445,10 @@ __global__ void __launch_bounds__(64 * kWavesOf<NJ>) router_forward_kernel(Route
 #pragma unroll
       for (int j = 0; j < NJ; ++j) x[j] = ahead[j];
       if (t + W < last) load_row<NJ>(a, t + W, lane, ahead);
-      const Norm n = scores<NJ>(a, x, s);
+      const Norm n = scores<NJ, Softmax>(x, s);
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) acc[j] += a.softmax ? s[j] : s[j] * n.inv;
-      if (select_topk<NJ, false>(a, t, x, s, b, lane, cand[wave], &index, &w))
+      for (int j = 0; j < NJ; ++j) acc[j] += Softmax ? s[j] : s[j] * n.inv;
+      if (select_topk<NJ, Softmax, Bias, false>(a, t, x, s, b, lane, cand[wave], &index, &w))
         put_token(a, o, t, lane, index, w, cnt);
       else
         undecided |= 1u << ((t - first) / W);
@@ -454,9 +461,9 @@ __global__ void __launch_bounds__(64 * kWavesOf<NJ>) router_forward_kernel(Route
       float x[NJ], s[NJ], w;
       int index;
       load_row<NJ>(a, again, lane, x);
-      const Norm n = scores<NJ>(a, x, s);
-      select_topk<NJ, true>(a, again, x, s, b, lane, cand[wave], &index, &w);
-      if (w < 0.0f) w = score_of(a, n, load_logit(a, again, index));
+      const Norm n = scores<NJ, Softmax>(x, s);
+      select_topk<NJ, Softmax, Bias, true>(a, again, x, s, b, lane, cand[wave], &index, &w);
+      if (w < 0.0f) w = score_of<Softmax>(n, load_logit(a, again, index));
       put_token(a, o, again, lane, index, w, cnt);
     }
     __syncthreads();
@@ -626,7 +633,7 @@ __device__ __forceinline__ void store_row(uint64_t row, int n, bool bf16, int la
 // experts' lanes in the wave's row of shared memory: first the scores lie
 // there for the selected to be picked up, then the selected's gradients.
 constexpr int kBackWaves = 4;
-template <int NJ>
+template <int NJ, bool Softmax>
 __global__ void __launch_bounds__(64 * kBackWaves) router_backward_kernel(RouterArgs a, BackwardIo o) {
   constexpr int W = kBackWaves;
   __shared__ float rows[W][64 * NJ];
@@ -666,7 +673,7 @@ __global__ void __launch_bounds__(64 * kBackWaves) router_backward_kernel(Router
         const int32_t *c = o.seq_counts + (int64_t)q * a.n_experts;
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
-          if (lane + 64 * j < a.n_experts) b[j] = f * (float)c[lane + 64 * j];
+          b[j] = f * (float)c[min(lane + 64 * j, a.n_experts - 1)];
       }
     }
     float x[NJ], s[NJ], g[NJ];
@@ -686,7 +693,7 @@ __global__ void __launch_bounds__(64 * kBackWaves) router_backward_kernel(Router
       store_row<NJ>(drow, a.n_experts, a.bf16, lane, b);  // zeros
       continue;
     }
-    const Norm n = scores<NJ>(a, x, s);
+    const Norm n = scores<NJ, Softmax>(x, s);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) g[j] = 0.0f;
     if (o.dweight) {
@@ -710,11 +717,11 @@ __global__ void __launch_bounds__(64 * kBackWaves) router_backward_kernel(Router
     }
     float dot = 0.0f;
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) dot += (a.softmax ? b[j] + g[j] : b[j]) * s[j];
+    for (int j = 0; j < NJ; ++j) dot += (Softmax ? b[j] + g[j] : b[j]) * s[j];
     dot = wave_sum(dot);
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
-      g[j] = a.softmax ? s[j] * (b[j] + g[j] - dot)
+      g[j] = Softmax ? s[j] * (b[j] + g[j] - dot)
                        : ((b[j] - dot * n.inv) * n.inv + g[j]) * s[j] * (1.0f - s[j]);
     store_row<NJ>(drow, a.n_experts, a.bf16, lane, g);
   }
@@ -869,7 +876,9 @@ wt_status wt_router_forward(const wt_router_desc *desc, int32_t *index, float *w
     if (tiles > 0)
       with_columns(a.n_experts, [&](auto nj) {
         constexpr int N = decltype(nj)::value;
-        hipLaunchKernelGGL((router_forward_kernel<N>), dim3(tiles), dim3(64 * kWavesOf<N>), 0, s, a,
+        const auto kernel = a.softmax ? (a.bias ? router_forward_kernel<N, true, true> : router_forward_kernel<N, true, false>)
+                                      : (a.bias ? router_forward_kernel<N, false, true> : router_forward_kernel<N, false, false>);
+        hipLaunchKernelGGL(kernel, dim3(tiles), dim3(64 * kWavesOf<N>), 0, s, a,
                            ForwardOut{index, weight, part_p, part_c});
       });
     if (a.n_seqs <= kSmallSeqs && w.rows * a.n_experts <= kSmallSums) {
@@ -916,8 +925,8 @@ wt_status wt_router_backward(const wt_router_desc *desc, const int32_t *index, c
     const BackwardIo io{index, seq_counts, dweight, dloss, (uint64_t)(uintptr_t)dlogits, dlogits_stride};
     with_columns(a.n_experts, [&](auto nj) {
       constexpr int N = decltype(nj)::value;
-      hipLaunchKernelGGL((router_backward_kernel<N>), dim3(tiles), dim3(64 * kBackWaves), 0, (hipStream_t)stream, a,
-                         io);
+      const auto kernel = a.softmax ? router_backward_kernel<N, true> : router_backward_kernel<N, false>;
+      hipLaunchKernelGGL(kernel, dim3(tiles), dim3(64 * kBackWaves), 0, (hipStream_t)stream, a, io);
     });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return fail(what, hip_msg("launch", e), WT_E_HIP);

@@ -98,22 +98,30 @@ __device__ __forceinline__ float load_logit(const RouterArgs &a, int64_t t, uint
   return load_at(row_of(a.logits, t, a.stride, a.bf16), e, a.bf16);
 }
 
-// A token's logits: lane l holds experts l, l + 64, ... (-infinity beyond the
-// last; those lanes read the last one's address, so that no load waits for a
-// branch).
+// A token's logits as they lie in memory: lane l holds experts l, l + 64, ...
+// (lanes beyond the last expert read the last one, so that no load waits for a
+// branch). Nothing touches the values before logits_of, so that a row can be on
+// its way while the one before it is worked on.
 template <int NJ>
-__device__ __forceinline__ void load_row(const RouterArgs &a, int64_t t, uint32_t lane, float x[NJ]) {
+__device__ __forceinline__ void load_row(const RouterArgs &a, int64_t t, uint32_t lane, uint32_t raw[NJ]) {
   const uint64_t row = row_of(a.logits, t, a.stride, a.bf16);
   const uint32_t end = (uint32_t)a.n_experts - 1;
   if (a.bf16) {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) x[j] = load_at(row, min(lane + 64 * j, end), true);
+    for (int j = 0; j < NJ; ++j) raw[j] = ld_global<uint16_t>(row + 2u * min(lane + 64 * j, end));
   } else {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) x[j] = load_at(row, min(lane + 64 * j, end), false);
+    for (int j = 0; j < NJ; ++j) raw[j] = ld_global<uint32_t>(row + 4u * min(lane + 64 * j, end));
   }
+}
+
+// The logits of a loaded row, -infinity beyond the last expert.
+template <int NJ>
+__device__ __forceinline__ void logits_of(const RouterArgs &a, uint32_t lane, const uint32_t raw[NJ], float x[NJ]) {
+  const uint32_t shift = a.bf16 ? 16 : 0;
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) x[j] = lane + 64 * j <= end ? x[j] : -INFINITY;
+  for (int j = 0; j < NJ; ++j)
+    x[j] = lane + 64 * j < (uint32_t)a.n_experts ? __uint_as_float(raw[j] << shift) : -INFINITY;
 }
 
 // What turns a logit into its score (softmax: exp(x - top) inv) and a score
@@ -232,7 +240,7 @@ __device__ __forceinline__ float near_tie(float key, float score) {
 struct Candidates {
   uint32_t key[64];
   float score[64];
-  uint16_t expert[64];
+  uint16_t expert[64], lane[64];
 };
 
 // fp32 to an unsigned number of the same order; both zeros alike.
@@ -271,12 +279,11 @@ __device__ __forceinline__ int collect(const uint32_t k[NJ], const float s[NJ], 
 // score. False where it could not be decided.
 //
 // A threshold is sought that at least top_k + 1 of the 64 lanes' greatest keys
-// reach, and few more (bisection on the ordered keys, a compare and a count
-// of a lane mask per step). The experts whose keys reach it, at most 64, are
-// packed to one per lane in the order of their numbers, and each counts the
-// ones before it (greater key, or the same key and a lower lane): its rank.
-// About 115 vector instructions a token of 384 experts, where taking the
-// greatest key top_k times takes 35 each time.
+// reach, and few more: twelve halvings of the two octaves below the greatest
+// (a compare and a count of a lane mask each). The experts whose keys reach
+// it, at most 64, are packed to one per lane in the order of their numbers,
+// and each counts the greater keys: its rank (equal keys, seen when two lanes
+// claim a rank, are counted apart by lane).
 //
 // With a bias the keys carry roundings. Where two neighbours of the first
 // top_k + 1 (or of a run of equals across that border and the next behind it)
@@ -290,7 +297,9 @@ __device__ __forceinline__ bool select_topk(const RouterArgs &a, int64_t t, cons
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
     const float key = Bias ? s[j] + b[j] : x[j];
-    k[j] = selectable(x[j]) && selectable(key) ? ordered(key) : 0u;
+    const bool fit = Bias ? (int)selectable(x[j]) & (int)selectable(key) : (int)selectable(x[j]);
+    const uint32_t u = ordered(key);
+    k[j] = fit ? u : 0u;
     h = max(h, k[j]);
   }
   const uint32_t top = wave_max_u32(h);
@@ -299,53 +308,33 @@ __device__ __forceinline__ bool select_topk(const RouterArgs &a, int64_t t, cons
   if (top == 0) return true;
   const int need = a.top_k + 1;
   // keys down to a quarter of the greatest, or all there are
-  uint32_t lo = top > 0x01000000u ? top - 0x01000000u : 1u, hi = top;
-  int n = __popcll(__ballot(h >= lo));
-  if (n < need) {
-    hi = lo;
+  constexpr uint32_t kSpan = 0x01000000u;
+  uint32_t lo = top > kSpan ? top - kSpan : 1u, step = kSpan / 2;
+  if (__popcll(__ballot(h >= lo)) < need) {
     lo = 1u;
-    n = __popcll(__ballot(h >= lo));
+    step = 0x80000000u;
   }
-  // a lane may hold several keys above lo, so stopping at a few more than needed is enough
-  while (n > need + 2 && hi - lo > 1) {
-    const uint32_t mid = lo + (hi - lo) / 2;
-    const int m = __popcll(__ballot(h >= mid));
-    if (m >= need) lo = mid, n = m;
-    else hi = mid;
+  const int steps = step == kSpan / 2 ? 12 : 20;
+  for (int i = 0; i < steps; ++i) {  // lo + step stays below 2^32
+    lo += __popcll(__ballot(h >= lo + step)) >= need ? step : 0u;
+    step >>= 1;
   }
   int count = collect<NJ>(k, s, lo, lane, c);
-  uint32_t key = lane < count ? c.key[lane] : 0u;
-  int rank = lane < count ? 0 : lane;  // lanes without a candidate stay behind them
-  for (int i = 0; i < min(count, 64); ++i) {
-    const uint32_t other = __builtin_amdgcn_readlane(key, i);
-    rank += lane < count && other > key - (lane > i ? 1u : 0u) ? 1 : 0;
-  }
   if (count > 64 && !Exact) return false;
-  if (Bias && !Exact) {
-    // neighbours by rank
-    const float sc = c.score[lane];
-    const int ex = c.expert[lane];
-    wave_lds_fence();
-    c.key[rank] = key;
-    wave_lds_fence();
-    const bool pair = lane + 1 < count;
-    const float k0 = from_ordered(c.key[lane]), k1 = from_ordered(c.key[(lane + 1) & 63]);
-    wave_lds_fence();
-    // the greatest score of a candidate bounds the pair's
-    const float most = Softmax ? wave_max(lane < count ? sc : 0.0f) : 0.0f;
-    const uint64_t close = __ballot(pair && k0 - k1 <= near_tie<Softmax>(k0, most));
-    if (close & ((2ull << (a.top_k - 1)) - 1)) {
-      int from = 0;  // the lane that holds rank `lane`
+  const bool mine = lane < count;  // this lane holds a candidate
+  uint32_t key = mine ? c.key[lane] : 0u;
+  float sc = c.score[lane];
+  int ex = c.expert[lane];
+  int rank = 0;
+  for (int i = 0; i < min(count, 64); ++i) rank += (uint32_t)__builtin_amdgcn_readlane(key, i) > key ? 1 : 0;
+  rank = mine ? rank : lane;  // lanes without a candidate stay behind them
+  wave_lds_fence();
+  c.lane[rank] = (uint16_t)lane;
+  wave_lds_fence();
+  if (__ballot(c.lane[rank] != lane)) {  // equal keys
 #pragma unroll 1
-      for (int i = 0; i < count; ++i)
-        if (__builtin_amdgcn_readlane(rank, i) == lane) from = i;
-      const float xe = lane < count ? load_logit(a, t, ex) : 0.0f, be = lane < count ? a.bias[ex] : 0.0f;
-      const float x0 = __shfl(xe, from), b0 = __shfl(be, from);
-      const uint64_t same = __ballot(pair && x0 == __shfl_down(x0, 1) && b0 == __shfl_down(b0, 1));
-      const int border = a.top_k - 1 + __builtin_ctzll(~(same >> (a.top_k - 1)));  // first unlike pair from there on
-      const bool open = border + 1 < count ? (close >> border) & 1 : count > a.top_k && lo > 1;
-      if (open || (close & ~same & ((1ull << (a.top_k - 1)) - 1))) return false;
-    }
+    for (int i = 0; i < min(count, 64); ++i)
+      rank += mine && lane > i && (uint32_t)__builtin_amdgcn_readlane(key, i) == key ? 1 : 0;
   }
   if (Exact) {
     double top64 = 0.0, z64 = 1.0;
@@ -361,23 +350,43 @@ __device__ __forceinline__ bool select_topk(const RouterArgs &a, int64_t t, cons
       if (*index >= 0) *score = -1.0f;  // to be taken from the logit
       return true;
     }
-    const double mine = lane < count ? exact_key(a, t, c.expert[lane], top64, z64) : 0.0;
+    sc = c.score[lane];
+    ex = c.expert[lane];
+    const double exact = lane < count ? exact_key(a, t, ex, top64, z64) : 0.0;
     rank = lane < count ? 0 : lane;
 #pragma unroll 1
     for (int i = 0; i < count; ++i) {
-      const double other = __shfl(mine, i);
-      rank += lane < count && (other > mine || (other == mine && i < lane)) ? 1 : 0;
+      const double other = __shfl(exact, i);
+      rank += lane < count && (other > exact || (other == exact && i < lane)) ? 1 : 0;
     }
   }
-  const float sc = c.score[lane];
-  const uint16_t ex = c.expert[lane];
   wave_lds_fence();
+  c.key[rank] = key;
   c.score[rank] = sc;
-  c.expert[rank] = ex;
+  c.expert[rank] = (uint16_t)ex;
   wave_lds_fence();
+  sc = c.score[lane];
+  ex = c.expert[lane];
+  if (Bias && !Exact) {
+    // lane r against r + 1; the greatest score of a candidate bounds the pair's
+    const bool pair = lane + 1 < count;
+    const float k0 = from_ordered(c.key[lane]), k1 = from_ordered(c.key[(lane + 1) & 63]);
+    const float most = Softmax ? wave_max(mine ? sc : 0.0f) : 0.0f;
+    const uint64_t close = __ballot(pair && k0 - k1 <= near_tie<Softmax>(k0, most));
+    if (close & ((2ull << (a.top_k - 1)) - 1)) {
+      const float xe = mine ? load_logit(a, t, ex) : 0.0f, be = mine ? a.bias[ex] : 0.0f;
+      const uint64_t same = __ballot(pair && xe == __shfl_down(xe, 1) && be == __shfl_down(be, 1));
+      const int border = a.top_k - 1 + __builtin_ctzll(~(same >> (a.top_k - 1)));  // first unlike pair from there on
+      const bool open = border + 1 < count ? (close >> border) & 1 : count > a.top_k && lo > 1;
+      if (open || (close & ~same & ((1ull << (a.top_k - 1)) - 1))) {
+        wave_lds_fence();
+        return false;
+      }
+    }
+  }
   if (lane < a.top_k && lane < count) {
-    *index = c.expert[lane];
-    *score = c.score[lane];
+    *index = ex;
+    *score = sc;
   }
   wave_lds_fence();
   return true;
@@ -417,7 +426,8 @@ __global__ void __launch_bounds__(64 * kWavesOf<NJ>) router_forward_kernel(Route
   const int32_t first = blockIdx.x * a.tile;
   const int32_t last = a.n_tokens - first < a.tile ? a.n_tokens : first + a.tile;
   int32_t t = first + wave;  // this wave's next token
-  float ahead[NJ], b[NJ];
+  uint32_t ahead[NJ];
+  float b[NJ];
   if (t < last) load_row<NJ>(a, t, lane, ahead);
 #pragma unroll
   for (int j = 0; j < NJ; ++j) b[j] = Bias ? a.bias[min(lane + 64 * j, a.n_experts - 1)] : 0.0f;
@@ -442,8 +452,7 @@ __global__ void __launch_bounds__(64 * kWavesOf<NJ>) router_forward_kernel(Route
     for (; t < hi; t += W) {
       float x[NJ], s[NJ], w;
       int index;
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) x[j] = ahead[j];
+      logits_of<NJ>(a, lane, ahead, x);
       if (t + W < last) load_row<NJ>(a, t + W, lane, ahead);
       const Norm n = scores<NJ, Softmax>(x, s);
 #pragma unroll
@@ -460,7 +469,9 @@ __global__ void __launch_bounds__(64 * kWavesOf<NJ>) router_forward_kernel(Route
       undecided &= undecided - 1;
       float x[NJ], s[NJ], w;
       int index;
-      load_row<NJ>(a, again, lane, x);
+      uint32_t raw[NJ];
+      load_row<NJ>(a, again, lane, raw);
+      logits_of<NJ>(a, lane, raw, x);
       const Norm n = scores<NJ, Softmax>(x, s);
       select_topk<NJ, Softmax, Bias, true>(a, again, x, s, b, lane, cand[wave], &index, &w);
       if (w < 0.0f) w = score_of<Softmax>(n, load_logit(a, again, index));
@@ -644,7 +655,8 @@ __global__ void __launch_bounds__(64 * kBackWaves) router_backward_kernel(Router
   int32_t t = first + wave;
   if (t >= last) return;
   const bool chosen = o.dweight && lane < a.top_k;  // this lane carries a selected expert
-  float ahead[NJ], dw = 0.0f;
+  uint32_t ahead[NJ];
+  float dw = 0.0f;
   int at = -1;
   load_row<NJ>(a, t, lane, ahead);
   if (chosen) {
@@ -677,8 +689,7 @@ __global__ void __launch_bounds__(64 * kBackWaves) router_backward_kernel(Router
       }
     }
     float x[NJ], s[NJ], g[NJ];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) x[j] = ahead[j];
+    logits_of<NJ>(a, lane, ahead, x);
     const int sel = at >= 0 && at < a.n_experts ? at : -1;
     float d = sel >= 0 ? dw * a.scale : 0.0f;
     if (t + W < last) {

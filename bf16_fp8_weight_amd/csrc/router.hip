@@ -169,6 +169,23 @@ __device__ __forceinline__ Norm scores(const float x[NJ], float s[NJ]) {
 
 __device__ __forceinline__ bool selectable(float x) { return x > -INFINITY; }  // false for NaN
 
+// exp in 64 bits with few registers: x = n ln 2 + r, the series of r by
+// Horner's rule from a table of 1 / k in scalar memory (|r| < 0.35: fourteen
+// terms leave 1e-19), in a loop because it runs for few tokens and must not
+// cost the others' registers.
+__constant__ const double kInverse[15] = {0.0,       1.0,       1.0 / 2,  1.0 / 3,  1.0 / 4,  1.0 / 5,  1.0 / 6, 1.0 / 7,
+                                          1.0 / 8,   1.0 / 9,   1.0 / 10, 1.0 / 11, 1.0 / 12, 1.0 / 13, 1.0 / 14};
+__device__ __forceinline__ double exp64(double x) {
+  if (!(x > -745.0)) return x <= -745.0 ? 0.0 : x;  // NaN stays
+  if (x > 709.0) return INFINITY;
+  const double n = rint(x * 0x1.71547652b82fep+0);
+  const double r = fma(n, -0x1.abc9e3b39803fp-56, fma(n, -0x1.62e42fefa39efp-1, x));
+  double p = 1.0;
+#pragma unroll 1
+  for (int k = 14; k > 0; --k) p = fma(p, r * kInverse[k], 1.0);
+  return ldexp(p, (int)n);
+}
+
 // Top and sum of a softmax in 64 bits.
 __device__ __forceinline__ void softmax64(const RouterArgs &a, int64_t t, int lane, double *top, double *z) {
   double m = -INFINITY, sum = 0.0;
@@ -180,7 +197,7 @@ __device__ __forceinline__ void softmax64(const RouterArgs &a, int64_t t, int la
 #pragma unroll 1
   for (int d = 32; d; d >>= 1) m = fmax(m, __shfl_xor(m, d));
 #pragma unroll 1
-  for (int e = lane; e < a.n_experts; e += 64) sum += exp((double)load_logit(a, t, e) - m);
+  for (int e = lane; e < a.n_experts; e += 64) sum += exp64((double)load_logit(a, t, e) - m);
 #pragma unroll 1
   for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
   *top = m;
@@ -188,41 +205,15 @@ __device__ __forceinline__ void softmax64(const RouterArgs &a, int64_t t, int la
 }
 
 // An expert's key in 64 bits (-infinity: not selectable).
+template <bool Softmax, bool Bias>
 __device__ __forceinline__ double exact_key(const RouterArgs &a, int64_t t, int e, double top, double z) {
   const double x = (double)load_logit(a, t, e);
   double key = x;
-  if (a.bias) key = (a.softmax ? exp(x - top) / z : 1.0 / (1.0 + exp(-x))) + (double)a.bias[e];
-  return x > -INFINITY && key > -INFINITY ? key : -INFINITY;
-}
-
-// Selection one expert after the other, keys in 64 bits and from memory each
-// time: for tokens with more equal keys than there are lanes.
-__device__ __forceinline__ int select_rounds(const RouterArgs &a, int64_t t, int lane, double top, double z) {
-  int index = -1;
-  double last = INFINITY;
-  int last_e = -1;
-#pragma unroll 1
-  for (int r = 0; r < a.top_k; ++r) {
-    // the greatest key behind the last one taken, and of equals the lowest expert
-    double best = -INFINITY;
-    int at = kMaxExperts;
-#pragma unroll 1
-    for (int e = lane; e < a.n_experts; e += 64) {
-      const double k = exact_key(a, t, e, top, z);
-      if ((k < last || (k == last && e > last_e)) && k > best) best = k, at = e;
-    }
-#pragma unroll 1
-    for (int d = 32; d; d >>= 1) {
-      const double ob = __shfl_xor(best, d);
-      const int oa = __shfl_xor(at, d);
-      if (ob > best || (ob == best && oa < at)) best = ob, at = oa;
-    }
-    if (at >= kMaxExperts) break;
-    if (lane == r) index = at;
-    last = best;
-    last_e = at;
+  if (Bias) {
+    const double y = exp64(Softmax ? x - top : -x);
+    key = (Softmax ? y : 1.0) / (Softmax ? z : 1.0 + y) + (double)a.bias[e];
   }
-  return index;
+  return x > -INFINITY && key > -INFINITY ? key : -INFINITY;
 }
 
 // Two keys closer than this may stand in the wrong order, in units of 2^-24
@@ -238,158 +229,219 @@ __device__ __forceinline__ float near_tie(float key, float score) {
 
 // A wave's candidates of a selection.
 struct Candidates {
-  uint32_t key[64];
+  float key[64];
   float score[64];
-  uint16_t expert[64], lane[64];
+  uint32_t expert[64];
 };
 
-// fp32 to an unsigned number of the same order; both zeros alike.
+// fp32 to an unsigned number of the same order, and back.
 __device__ __forceinline__ uint32_t ordered(float x) {
-  const uint32_t b = __float_as_uint(x + 0.0f);
+  const uint32_t b = __float_as_uint(x);
   return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float from_ordered(uint32_t u) {
   return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
 }
 
-// Packs the experts whose keys reach lo to one per lane, in the order of their
-// numbers; returns how many there are (those beyond 64 are left out).
-template <int NJ>
-__device__ __forceinline__ int collect(const uint32_t k[NJ], const float s[NJ], uint32_t lo, int lane, Candidates &c) {
+// A place for each lane of the mask: how many lower lanes there are, plus base.
+__device__ __forceinline__ int place(uint64_t who, int base) {
+  return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who, (uint32_t)base));
+}
+
+// The selection of a token that select_topk cannot decide, by keys in 64 bits:
+// all experts whose fp32 keys reach `reach` are ranked, or, if those are more
+// than 64, the experts are taken one after the other. The candidates are left
+// in the order of their ranks. Returns their number.
+template <bool Softmax, bool Bias>
+__device__ __forceinline__ int select_exact(const RouterArgs &a, int64_t t, const Norm &n, int lane, float reach,
+                                            Candidates &c) {
+  double top = 0.0, z = 1.0;
+  if (Softmax && Bias) softmax64(a, t, lane, &top, &z);
   int count = 0;
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    const bool in = k[j] >= lo;
-    const uint64_t who = __ballot(in);
-    if (who) {
-      const int at = count + __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
-      if (in && at < 64) {
-        c.key[at] = k[j];
-        c.score[at] = s[j];
-        c.expert[at] = (uint16_t)(lane + 64 * j);
-      }
-      count += __popcll(who);
+#pragma unroll 1
+  for (int base = 0; base < a.n_experts; base += 64) {
+    const int e = base + lane;
+    float x = -INFINITY;
+    if (e < a.n_experts) x = load_logit(a, t, e);
+    const float s = score_of<Softmax>(n, x), k = Bias && e < a.n_experts ? s + a.bias[e] : x;
+    const uint64_t who = __ballot(selectable(x) && k >= reach);
+    const int at = place(who, count);
+    if ((who >> lane & 1) && at < 64) {
+      c.score[at] = s;
+      c.expert[at] = e;
     }
+    count += __popcll(who);
+  }
+  wave_lds_fence();
+  if (count <= 64) {
+    const float s = c.score[lane];
+    const uint32_t e = c.expert[lane];
+    const double key = lane < count ? exact_key<Softmax, Bias>(a, t, e, top, z) : 0.0;
+    int rank = lane < count ? 0 : lane;
+#pragma unroll 1
+    for (int i = 0; i < count; ++i) {
+      const double other = __shfl(key, i);
+      rank += lane < count && (other > key || (other == key && i < lane)) ? 1 : 0;
+    }
+    wave_lds_fence();
+    c.score[rank] = s;
+    c.expert[rank] = e;
+    wave_lds_fence();
+    return count;
+  }
+  double last = INFINITY;
+  int last_e = -1;
+  for (count = 0; count < a.top_k; ++count) {
+    // the greatest key behind the last one taken, and of equals the lowest expert
+    double best = -INFINITY;
+    int at = kMaxExperts;
+#pragma unroll 1
+    for (int e = lane; e < a.n_experts; e += 64) {
+      const double k = exact_key<Softmax, Bias>(a, t, e, top, z);
+      if ((k < last || (k == last && e > last_e)) && k > best) best = k, at = e;
+    }
+#pragma unroll 1
+    for (int d = 32; d; d >>= 1) {
+      const double ob = __shfl_xor(best, d);
+      const int oa = __shfl_xor(at, d);
+      if (ob > best || (ob == best && oa < at)) best = ob, at = oa;
+    }
+    if (at >= kMaxExperts) break;
+    if (lane == 0) {
+      c.expert[count] = at;
+      c.score[count] = score_of<Softmax>(n, load_logit(a, t, at));
+    }
+    last = best;
+    last_e = at;
   }
   wave_lds_fence();
   return count;
 }
 
 // Selection: lane r < top_k receives the r-th expert (-1: none left) and its
-// score. False where it could not be decided.
+// score.
 //
 // A threshold is sought that at least top_k + 1 of the 64 lanes' greatest keys
-// reach, and few more: twelve halvings of the two octaves below the greatest
+// reach, and few more: nine halvings of the two octaves below the greatest
 // (a compare and a count of a lane mask each). The experts whose keys reach
 // it, at most 64, are packed to one per lane in the order of their numbers,
 // and each counts the greater keys: its rank (equal keys, seen when two lanes
-// claim a rank, are counted apart by lane).
+// claim a rank, are counted apart by lane). Some 210 vector instructions a
+// token of 384 experts with their scores; taking the greatest key top_k times
+// needs 35 each time.
 //
 // With a bias the keys carry roundings. Where two neighbours of the first
 // top_k + 1 (or of a run of equals across that border and the next behind it)
-// are too close and not of the same logit and bias, the token is not decided;
-// neither is one with more than 64 candidates. Exact takes such a token again:
-// all experts that may belong to the first top_k ranked by keys in 64 bits.
-template <int NJ, bool Softmax, bool Bias, bool Exact>
-__device__ __forceinline__ bool select_topk(const RouterArgs &a, int64_t t, const float x[NJ], const float s[NJ],
-                                            const float b[NJ], int lane, Candidates &c, int *index, float *score) {
-  uint32_t k[NJ], h = 0;
+// are too close and not of the same logit and bias, select_exact decides; as
+// it does where there are more than 64 candidates.
+template <int NJ, bool Softmax, bool Bias>
+__device__ __forceinline__ void select_topk(const RouterArgs &a, int64_t t, const Norm &norm, const float x[NJ],
+                                            const float s[NJ], const float b[NJ], int lane, Candidates &c, int *index,
+                                            float *score) {
+  float k[NJ], h = -INFINITY;  // a key that is NaN reaches no threshold
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
-    const float key = Bias ? s[j] + b[j] : x[j];
-    const bool fit = Bias ? (int)selectable(x[j]) & (int)selectable(key) : (int)selectable(x[j]);
-    const uint32_t u = ordered(key);
-    k[j] = fit ? u : 0u;
-    h = max(h, k[j]);
+    k[j] = Bias ? (x[j] == -INFINITY ? -INFINITY : s[j] + b[j]) : x[j];
+    h = fmaxf(h, k[j]);
   }
-  const uint32_t top = wave_max_u32(h);
+  const uint32_t u = h > -INFINITY ? ordered(h) : 0u, top = wave_max_u32(u);
   *index = -1;
   *score = 0.0f;
-  if (top == 0) return true;
+  if (top == 0) return;
   const int need = a.top_k + 1;
   // keys down to a quarter of the greatest, or all there are
   constexpr uint32_t kSpan = 0x01000000u;
   uint32_t lo = top > kSpan ? top - kSpan : 1u, step = kSpan / 2;
-  if (__popcll(__ballot(h >= lo)) < need) {
+  int steps = 9;
+  if (__popcll(__ballot(u >= lo)) < need) {
     lo = 1u;
     step = 0x80000000u;
+    steps = 20;
   }
-  const int steps = step == kSpan / 2 ? 12 : 20;
   for (int i = 0; i < steps; ++i) {  // lo + step stays below 2^32
-    lo += __popcll(__ballot(h >= lo + step)) >= need ? step : 0u;
+    lo += __popcll(__ballot(u >= lo + step)) >= need ? step : 0u;
     step >>= 1;
   }
-  int count = collect<NJ>(k, s, lo, lane, c);
-  if (count > 64 && !Exact) return false;
-  const bool mine = lane < count;  // this lane holds a candidate
-  uint32_t key = mine ? c.key[lane] : 0u;
-  float sc = c.score[lane];
-  int ex = c.expert[lane];
-  int rank = 0;
-  for (int i = 0; i < min(count, 64); ++i) rank += (uint32_t)__builtin_amdgcn_readlane(key, i) > key ? 1 : 0;
-  rank = mine ? rank : lane;  // lanes without a candidate stay behind them
-  wave_lds_fence();
-  c.lane[rank] = (uint16_t)lane;
-  wave_lds_fence();
-  if (__ballot(c.lane[rank] != lane)) {  // equal keys
-#pragma unroll 1
-    for (int i = 0; i < min(count, 64); ++i)
-      rank += mine && lane > i && (uint32_t)__builtin_amdgcn_readlane(key, i) == key ? 1 : 0;
+  const bool all = lo == 1u;  // every selectable expert is a candidate
+  const float least = all ? -0x1.fffffep+127f : from_ordered(lo);
+  uint64_t who[NJ];
+  int count = 0;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    who[j] = __ballot(k[j] >= least);
+    count += __popcll(who[j]);
   }
-  if (Exact) {
-    double top64 = 0.0, z64 = 1.0;
-    if (Softmax && Bias) softmax64(a, t, lane, &top64, &z64);
-    if (count <= 64 && count > a.top_k) {  // everything within reach of the last place
-      const float last = from_ordered(__builtin_amdgcn_readlane(key, __builtin_ctzll(__ballot(rank == a.top_k - 1))));
-      const float reach = last - near_tie<Softmax>(last, Softmax ? 1.0f : 0.0f);
-      wave_lds_fence();
-      count = collect<NJ>(k, s, min(lo, ordered(reach)), lane, c);
+  float reach = least;
+  bool decided = count <= 64;
+  if (decided) {
+    int base = 0;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      if (who[j]) {
+        const int at = place(who[j], base);
+        if (k[j] >= least) {
+          c.key[at] = k[j];
+          c.score[at] = s[j];
+          c.expert[at] = lane + 64 * j;
+        }
+        base += __popcll(who[j]);
+      }
+    wave_lds_fence();
+    const bool mine = lane < count;  // this lane holds a candidate
+    const float key = mine ? c.key[lane] : -INFINITY;
+    float sc = c.score[lane];
+    uint32_t ex = c.expert[lane];
+    int rank = 0;
+    for (int i = 0; i < count; i += 4) {  // lanes from count on hold -infinity
+      rank += lane_value(key, i) > key ? 1 : 0;
+      rank += lane_value(key, i + 1) > key ? 1 : 0;
+      rank += lane_value(key, i + 2) > key ? 1 : 0;
+      rank += lane_value(key, i + 3) > key ? 1 : 0;
     }
-    if (count > 64) {
-      *index = select_rounds(a, t, lane, top64, z64);
-      if (*index >= 0) *score = -1.0f;  // to be taken from the logit
-      return true;
+    rank = mine ? rank : lane;  // lanes without a candidate stay behind them
+    wave_lds_fence();
+    c.expert[rank] = lane;
+    wave_lds_fence();
+    if (__ballot(c.expert[rank] != (uint32_t)lane)) {  // equal keys: by lane
+      for (int i = 0; i < count; i += 4) {
+        rank += lane_value(key, i) == key && lane > i && mine ? 1 : 0;
+        rank += lane_value(key, i + 1) == key && lane > i + 1 && mine ? 1 : 0;
+        rank += lane_value(key, i + 2) == key && lane > i + 2 && mine ? 1 : 0;
+        rank += lane_value(key, i + 3) == key && lane > i + 3 && mine ? 1 : 0;
+      }
     }
-    sc = c.score[lane];
-    ex = c.expert[lane];
-    const double exact = lane < count ? exact_key(a, t, ex, top64, z64) : 0.0;
-    rank = lane < count ? 0 : lane;
-#pragma unroll 1
-    for (int i = 0; i < count; ++i) {
-      const double other = __shfl(exact, i);
-      rank += lane < count && (other > exact || (other == exact && i < lane)) ? 1 : 0;
-    }
-  }
-  wave_lds_fence();
-  c.key[rank] = key;
-  c.score[rank] = sc;
-  c.expert[rank] = (uint16_t)ex;
-  wave_lds_fence();
-  sc = c.score[lane];
-  ex = c.expert[lane];
-  if (Bias && !Exact) {
-    // lane r against r + 1; the greatest score of a candidate bounds the pair's
-    const bool pair = lane + 1 < count;
-    const float k0 = from_ordered(c.key[lane]), k1 = from_ordered(c.key[(lane + 1) & 63]);
-    const float most = Softmax ? wave_max(mine ? sc : 0.0f) : 0.0f;
-    const uint64_t close = __ballot(pair && k0 - k1 <= near_tie<Softmax>(k0, most));
-    if (close & ((2ull << (a.top_k - 1)) - 1)) {
-      const float xe = mine ? load_logit(a, t, ex) : 0.0f, be = mine ? a.bias[ex] : 0.0f;
-      const uint64_t same = __ballot(pair && xe == __shfl_down(xe, 1) && be == __shfl_down(be, 1));
-      const int border = a.top_k - 1 + __builtin_ctzll(~(same >> (a.top_k - 1)));  // first unlike pair from there on
-      const bool open = border + 1 < count ? (close >> border) & 1 : count > a.top_k && lo > 1;
-      if (open || (close & ~same & ((1ull << (a.top_k - 1)) - 1))) {
-        wave_lds_fence();
-        return false;
+    wave_lds_fence();
+    c.key[rank] = key;
+    c.score[rank] = sc;
+    c.expert[rank] = ex;
+    wave_lds_fence();
+    if (Bias) {
+      // lane r against r + 1; the greatest score of a candidate bounds the pair's
+      const bool pair = lane + 1 < count;
+      const float k0 = c.key[lane], k1 = c.key[(lane + 1) & 63];
+      const float most = Softmax ? wave_max(mine ? sc : 0.0f) : 0.0f;
+      const uint64_t close = __ballot(pair && k0 - k1 <= near_tie<Softmax>(k0, most));
+      if (close & ((2ull << (a.top_k - 1)) - 1)) {
+        const uint32_t er = c.expert[lane];
+        const float xe = mine ? load_logit(a, t, er) : 0.0f, be = mine ? a.bias[er] : 0.0f;
+        const uint64_t same = __ballot(pair && xe == __shfl_down(xe, 1) && be == __shfl_down(be, 1));
+        const int border = a.top_k - 1 + __builtin_ctzll(~(same >> (a.top_k - 1)));  // first unlike pair from there on
+        const bool open = border + 1 < count ? (close >> border) & 1 : count > a.top_k && !all;
+        decided = !open && !(close & ~same & ((1ull << (a.top_k - 1)) - 1));
+        // everything within reach of the last place
+        if (count > a.top_k) {
+          const float last = lane_value(k0, a.top_k - 1);
+          reach = fminf(least, last - near_tie<Softmax>(last, Softmax ? 1.0f : 0.0f));
+        }
       }
     }
   }
+  if (!decided) count = select_exact<Softmax, Bias>(a, t, norm, lane, reach, c);
   if (lane < a.top_k && lane < count) {
-    *index = ex;
-    *score = sc;
+    *index = (int)c.expert[lane];
+    *score = c.score[lane];
   }
   wave_lds_fence();
-  return true;
 }
 
 struct ForwardOut {
@@ -448,7 +500,6 @@ __global__ void __launch_bounds__(64 * kWavesOf<NJ>) router_forward_kernel(Route
     float acc[NJ];
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[j] = 0.0f;
-    uint32_t undecided = 0;  // bit i: the i-th of this wave's tokens in the tile (8 at most)
     for (; t < hi; t += W) {
       float x[NJ], s[NJ], w;
       int index;
@@ -457,26 +508,11 @@ __global__ void __launch_bounds__(64 * kWavesOf<NJ>) router_forward_kernel(Route
       const Norm n = scores<NJ, Softmax>(x, s);
 #pragma unroll
       for (int j = 0; j < NJ; ++j) acc[j] += Softmax ? s[j] : s[j] * n.inv;
-      if (select_topk<NJ, Softmax, Bias, false>(a, t, x, s, b, lane, cand[wave], &index, &w))
-        put_token(a, o, t, lane, index, w, cnt);
-      else
-        undecided |= 1u << ((t - first) / W);
+      select_topk<NJ, Softmax, Bias>(a, t, n, x, s, b, lane, cand[wave], &index, &w);
+      put_token(a, o, t, lane, index, w, cnt);
     }
 #pragma unroll
     for (int j = 0; j < NJ; ++j) sum[wave][lane + 64 * j] = acc[j];
-    while (undecided) {
-      const int32_t again = first + wave + W * __builtin_ctz(undecided);
-      undecided &= undecided - 1;
-      float x[NJ], s[NJ], w;
-      int index;
-      uint32_t raw[NJ];
-      load_row<NJ>(a, again, lane, raw);
-      logits_of<NJ>(a, lane, raw, x);
-      const Norm n = scores<NJ, Softmax>(x, s);
-      select_topk<NJ, Softmax, Bias, true>(a, again, x, s, b, lane, cand[wave], &index, &w);
-      if (w < 0.0f) w = score_of<Softmax>(n, load_logit(a, again, index));
-      put_token(a, o, again, lane, index, w, cnt);
-    }
     __syncthreads();
     const int64_t row = ((int64_t)blockIdx.x + q) * a.n_experts;
     for (int e = threadIdx.x; e < a.n_experts; e += Threads) {

@@ -31,6 +31,11 @@ __device__ __forceinline__ float lane63(float x) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 63));
 }
 
+// Lane i's value (i uniform).
+__device__ __forceinline__ float lane_value(float x, int i) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), i));
+}
+
 // A NaN takes no part in the maximum (of a number and a NaN the number wins).
 __device__ __forceinline__ float wave_max(float m) {
   m = fmaxf(m, dpp_f32<0x0B1, 0xF>(m, m));  // quad_perm [1,0,3,2]

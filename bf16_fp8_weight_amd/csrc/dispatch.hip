@@ -15,6 +15,7 @@
 
 #include "hip_util.h"
 #include "plan.h"
+#include "wave.h"
 #include "wt.h"
 
 namespace wt {
@@ -31,6 +32,7 @@ constexpr int kMaxTiles = 64;
 constexpr int64_t kRowsTile = ROWS_TILE;       // copies of one workgroup, more where there would be over 64 tiles
 constexpr int64_t kRowsSingle = ROWS_SINGLE;
 constexpr int64_t kRowsSingleFill = 65536;     // rows that one workgroup may have to fill
+constexpr int kHeld = 8;                       // times 64 copies that a wave keeps in registers
 
 struct RowsArgs {
   const int32_t *index;
@@ -78,7 +80,8 @@ __device__ __forceinline__ uint64_t same_expert(int e) {
 template <bool Single>
 __global__ void __launch_bounds__(1024) rows_place_kernel(RowsArgs a) {
   extern __shared__ int lds[];
-  const int E = a.n_experts, waves = blockDim.x >> 6, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int E = a.n_experts, waves = blockDim.x >> 6, lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int *next = lds;               // [wave][expert]: counts, then next rows
   int *before = next + waves * E;  // [expert]: copies in the tiles before
   int *total = before + E;       // [expert]: copies in all tiles
@@ -87,9 +90,20 @@ __global__ void __launch_bounds__(1024) rows_place_kernel(RowsArgs a) {
   const int64_t part = a.tile / waves, from = lo + wave * part, to = from + part < hi ? from + part : hi;
   for (int e = threadIdx.x; e < (waves + 2) * E; e += blockDim.x) lds[e] = 0;
   __syncthreads();
-  for (int64_t i = from + lane; i < to; i += 64) {
-    const int e = expert_at(a, i, to);
-    if (e >= 0) atomicAdd(&next[wave * E + e], 1);
+  // a wave's copies, 64 at a time, stay in registers where they fit
+  int held[kHeld];
+  const bool holds = part <= 64 * kHeld;
+  if (holds) {
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) held[k] = from + 64 * k < to ? expert_at(a, from + 64 * k + lane, to) : -1;
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+      if (held[k] >= 0) atomicAdd(&next[wave * E + held[k]], 1);
+  } else {
+    for (int64_t i = from + lane; i < to; i += 64) {
+      const int e = expert_at(a, i, to);
+      if (e >= 0) atomicAdd(&next[wave * E + e], 1);
+    }
   }
   if (!Single) {
     // thread = (expert, every parts-th tile)
@@ -119,7 +133,10 @@ __global__ void __launch_bounds__(1024) rows_place_kernel(RowsArgs a) {
   if (wave == 0) {  // scan of the padded counts, a run of experts to each lane
     const int per = (E + 63) / 64, e0 = lane * per, e1 = min(E, e0 + per);
     int sum = 0;
-    for (int e = e0; e < e1; ++e) sum += (total[e] + a.align - 1) / a.align * a.align;
+    for (int e = e0; e < e1; ++e) {
+      start[e] = (int)(((uint32_t)total[e] + a.align - 1) / (uint32_t)a.align) * a.align;
+      sum += start[e];
+    }
     int scan = sum;
     for (int d = 1; d < 64; d *= 2) {
       const int up = __shfl_up(scan, d);
@@ -127,8 +144,9 @@ __global__ void __launch_bounds__(1024) rows_place_kernel(RowsArgs a) {
     }
     int at = scan - sum;
     for (int e = e0; e < e1; ++e) {
+      const int size = start[e];
       start[e] = at;
-      at += (total[e] + a.align - 1) / a.align * a.align;
+      at += size;
     }
     if (lane == 63) start[E] = scan;
   }
@@ -147,21 +165,27 @@ __global__ void __launch_bounds__(1024) rows_place_kernel(RowsArgs a) {
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[E] = start[E];
   __syncthreads();
-  for (int64_t base = from; base < to; base += 64) {
+  const auto place = [&](int64_t base, int e) {
     const int64_t i = base + lane;
-    const int e = expert_at(a, i, to);
     const uint64_t same = same_expert(e);
     int row = -1;
     if (e >= 0) {
       const int rank = __popcll(same & (((uint64_t)1 << lane) - 1));
       row = next[wave * E + e] + rank;
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      wave_lds_fence();
       if (rank == 0) next[wave * E + e] = row + __popcll(same);
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      wave_lds_fence();
       if (row >= a.n_rows) row = -1;
       else if (a.row_token) a.row_token[row] = (int32_t)((uint32_t)i / (uint32_t)a.top_k);
     }
     if (i < to && a.pair_row) a.pair_row[i] = row;
+  };
+  if (holds) {
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+      if (from + 64 * k < to) place(from + 64 * k, held[k]);
+  } else {
+    for (int64_t base = from; base < to; base += 64) place(base, expert_at(a, base + lane, to));
   }
   if (!a.row_token) return;
   // rows that hold no copy: behind each expert's copies (a wave per expert), and behind the last expert

@@ -17,10 +17,7 @@ namespace {
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 32;
 
-// Waves of a workgroup of the two passes over tokens: 16, 8 where a row of
-// sums per wave would take too much shared memory.
-template <int NJ>
-constexpr int kWavesOf = NJ <= 6 ? 16 : 8;
+constexpr int kWaves = 8;  // of a workgroup of the forward pass
 
 struct RouterArgs {
   uint64_t logits;
@@ -98,20 +95,24 @@ __device__ __forceinline__ float load_logit(const RouterArgs &a, int64_t t, uint
   return load_at(row_of(a.logits, t, a.stride, a.bf16), e, a.bf16);
 }
 
+// A row as a buffer: accesses beyond its last expert read 0 and write nothing,
+// so that no lane needs a branch or an address of its own.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(uint64_t row, int n, bool bf16) {
+  return __builtin_amdgcn_make_buffer_rsrc((void *)(uintptr_t)row, 0, n * (bf16 ? 2 : 4), 0x00020000);
+}
+
 // A token's logits as they lie in memory: lane l holds experts l, l + 64, ...
-// (lanes beyond the last expert read the last one, so that no load waits for a
-// branch). Nothing touches the values before logits_of, so that a row can be on
-// its way while the one before it is worked on.
+// Nothing touches the values before logits_of, so that a row can be on its way
+// while the one before it is worked on.
 template <int NJ>
 __device__ __forceinline__ void load_row(const RouterArgs &a, int64_t t, uint32_t lane, uint32_t raw[NJ]) {
-  const uint64_t row = row_of(a.logits, t, a.stride, a.bf16);
-  const uint32_t end = (uint32_t)a.n_experts - 1;
+  const auto row = row_buffer(row_of(a.logits, t, a.stride, a.bf16), a.n_experts, a.bf16);
   if (a.bf16) {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) raw[j] = ld_global<uint16_t>(row + 2u * min(lane + 64 * j, end));
+    for (int j = 0; j < NJ; ++j) raw[j] = __builtin_amdgcn_raw_buffer_load_b16(row, 2 * lane + 128 * j, 0, 0);
   } else {
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) raw[j] = ld_global<uint32_t>(row + 4u * min(lane + 64 * j, end));
+    for (int j = 0; j < NJ; ++j) raw[j] = __builtin_amdgcn_raw_buffer_load_b32(row, 4 * lane + 256 * j, 0, 0);
   }
 }
 
@@ -469,8 +470,8 @@ __device__ __forceinline__ void put_token(const RouterArgs &a, const ForwardOut 
 // along the tokens each step to the next pair raises i or q, so no two pairs
 // share a row, no sum needs an atomic, and the order of every sum is fixed.
 template <int NJ, bool Softmax, bool Bias>
-__global__ void __launch_bounds__(64 * kWavesOf<NJ>) router_forward_kernel(RouterArgs a, ForwardOut o) {
-  constexpr int W = kWavesOf<NJ>, Threads = 64 * W;
+__global__ void __launch_bounds__(64 * kWaves) router_forward_kernel(RouterArgs a, ForwardOut o) {
+  constexpr int W = kWaves, Threads = 64 * W;
   __shared__ float sum[W][64 * NJ];
   __shared__ int cnt[64 * NJ];
   __shared__ Candidates cand[W];
@@ -662,15 +663,17 @@ struct BackwardIo {
 };
 
 template <int NJ>
-__device__ __forceinline__ void store_row(uint64_t row, int n, bool bf16, int lane, const float x[NJ]) {
-  if (bf16) {
+__device__ __forceinline__ void store_row(const RouterArgs &a, const BackwardIo &o, int64_t t, uint32_t lane,
+                                          const float x[NJ]) {
+  const auto row = row_buffer(row_of(o.dlogits, t, o.dstride, a.bf16), a.n_experts, a.bf16);
+  if (a.bf16) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
-      if (lane + 64 * j < n) st_global<uint16_t>(row + 2u * (uint32_t)(lane + 64 * j), __builtin_bit_cast(uint16_t, (__bf16)x[j]));
+      __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (__bf16)x[j]), row, 2 * lane + 128 * j, 0, 0);
   } else {
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
-      if (lane + 64 * j < n) st_global<float>(row + 4u * (uint32_t)(lane + 64 * j), x[j]);
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[j]), row, 4 * lane + 256 * j, 0, 0);
   }
 }
 
@@ -735,9 +738,8 @@ __global__ void __launch_bounds__(64 * kBackWaves) router_backward_kernel(Router
         dw = o.dweight[(int64_t)(t + W) * a.top_k + lane];
       }
     }
-    const uint64_t drow = row_of(o.dlogits, t, o.dstride, a.bf16);
     if (padding) {
-      store_row<NJ>(drow, a.n_experts, a.bf16, lane, b);  // zeros
+      store_row<NJ>(a, o, t, lane, b);  // zeros
       continue;
     }
     const Norm n = scores<NJ, Softmax>(x, s);
@@ -770,31 +772,21 @@ __global__ void __launch_bounds__(64 * kBackWaves) router_backward_kernel(Router
     for (int j = 0; j < NJ; ++j)
       g[j] = Softmax ? s[j] * (b[j] + g[j] - dot)
                        : ((b[j] - dot * n.inv) * n.inv + g[j]) * s[j] * (1.0f - s[j]);
-    store_row<NJ>(drow, a.n_experts, a.bf16, lane, g);
+    store_row<NJ>(a, o, t, lane, g);
   }
 }
 
-// Tokens of one workgroup.
-#ifndef ROUTER_TILE
-#define ROUTER_TILE 0
-#endif
-int32_t tile_of(int64_t n_tokens) {
-  if (ROUTER_TILE) return ROUTER_TILE;
-  return n_tokens <= 8192 ? 16 : n_tokens <= 16384 ? 32 : 64;
-}
-#ifndef BACK_TILE
-#define BACK_TILE 0
-#endif
-int32_t back_tile_of(int64_t n_tokens) {
-  if (BACK_TILE) return BACK_TILE;
-  return n_tokens <= 8192 ? 4 : n_tokens <= 16384 ? 8 : 16;
-}
+// Tokens of one workgroup. More of them leave fewer partial sums, fewer fill
+// the card with fewer tokens. Measured on MI355X, forward with 4, 8 and 16
+// waves to a workgroup and 1, 2, 4 tokens to a wave: 16384 x 384 31.3 / 26.6 /
+// 24.4, 30.7 / 25.9 / 23.3 and - / 26.6 / 24.2 us, 5003 x 160 17.5 / 15.5 /
+// 16.5, 14.8 / 14.3 / 20.5 and 15.6 / - / 21.2 us; backward (4 waves) of the
+// first 14.6 / 12.5 / 11.8 us, of the second 7.6 / 7.6 / 7.6 us.
+int32_t tile_of(int64_t n_tokens) { return n_tokens <= 8192 ? 16 : n_tokens <= 32768 ? 32 : 64; }
+int32_t back_tile_of(int64_t n_tokens) { return n_tokens <= 8192 ? 4 : 16; }
 
 // Partial sums up to which one workgroup reduces them.
-#ifndef ROUTER_SMALL
-#define ROUTER_SMALL 32768
-#endif
-constexpr int64_t kSmallSums = ROUTER_SMALL;
+constexpr int64_t kSmallSums = 32768;
 constexpr int32_t kSmallSeqs = 8;
 
 int chunks_of(int n_experts) { return (n_experts + kChunk - 1) / kChunk; }
@@ -925,7 +917,7 @@ wt_status wt_router_forward(const wt_router_desc *desc, int32_t *index, float *w
         constexpr int N = decltype(nj)::value;
         const auto kernel = a.softmax ? (a.bias ? router_forward_kernel<N, true, true> : router_forward_kernel<N, true, false>)
                                       : (a.bias ? router_forward_kernel<N, false, true> : router_forward_kernel<N, false, false>);
-        hipLaunchKernelGGL(kernel, dim3(tiles), dim3(64 * kWavesOf<N>), 0, s, a,
+        hipLaunchKernelGGL(kernel, dim3(tiles), dim3(64 * kWaves), 0, s, a,
                            ForwardOut{index, weight, part_p, part_c});
       });
     if (a.n_seqs <= kSmallSeqs && w.rows * a.n_experts <= kSmallSums) {

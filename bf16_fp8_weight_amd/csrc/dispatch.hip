@@ -32,7 +32,6 @@ constexpr int kMaxTiles = 64;
 constexpr int64_t kRowsTile = ROWS_TILE;       // copies of one workgroup, more where there would be over 64 tiles
 constexpr int64_t kRowsSingle = ROWS_SINGLE;
 constexpr int64_t kRowsSingleFill = 65536;     // rows that one workgroup may have to fill
-constexpr int kHeld = 8;                       // times 64 copies that a wave keeps in registers
 
 struct RowsArgs {
   const int32_t *index;
@@ -45,8 +44,9 @@ struct RowsArgs {
   int32_t n_tiles;
 };
 
-// Waves of a workgroup: their histograms take 4 bytes per expert each.
-int waves_for(int n_experts) { return n_experts <= 512 ? 16 : 8; }
+// Waves of a workgroup: 16, or 8 beyond 512 experts (each wave has a histogram
+// of 4 bytes per expert); a thread then looks after one or two experts.
+constexpr int kManyExperts = 512;
 
 __device__ __forceinline__ int expert_at(const RowsArgs &a, int64_t i, int64_t end) {
   const int e = i < end ? a.index[i] : -1;
@@ -77,38 +77,29 @@ __device__ __forceinline__ uint64_t same_expert(int e) {
   return m;
 }
 
-template <bool Single>
-__global__ void __launch_bounds__(1024) rows_place_kernel(RowsArgs a) {
+template <bool Single, int Waves>
+__global__ void __launch_bounds__(64 * Waves) rows_place_kernel(RowsArgs a) {
   extern __shared__ int lds[];
-  const int E = a.n_experts, waves = blockDim.x >> 6, lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int *next = lds;               // [wave][expert]: counts, then next rows
-  int *before = next + waves * E;  // [expert]: copies in the tiles before
-  int *total = before + E;       // [expert]: copies in all tiles
-  int *start = total + E;        // [expert + 1]: first rows
+  constexpr int Threads = 64 * Waves, Per = Waves == 16 ? 1 : 2;  // experts of a thread
+  __shared__ int scan[Waves];
+  const int E = a.n_experts, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int *next = lds;                 // [wave][expert]: counts, then next rows
+  int *before = next + Waves * E;  // [expert]: copies in the tiles before
+  int *total = before + E;         // [expert]: copies in all tiles
+  int *start = total + E;          // [expert + 1]: first rows
   const int64_t lo = blockIdx.x * a.tile, hi = lo + a.tile < a.n_pairs ? lo + a.tile : a.n_pairs;
-  const int64_t part = a.tile / waves, from = lo + wave * part, to = from + part < hi ? from + part : hi;
-  for (int e = threadIdx.x; e < (waves + 2) * E; e += blockDim.x) lds[e] = 0;
+  const int64_t part = a.tile / Waves, from = lo + wave * part, to = from + part < hi ? from + part : hi;
+  for (int e = threadIdx.x; e < (Waves + 2) * E; e += Threads) lds[e] = 0;
   __syncthreads();
-  // a wave's copies, 64 at a time, stay in registers where they fit
-  int held[kHeld];
-  const bool holds = part <= 64 * kHeld;
-  if (holds) {
-#pragma unroll
-    for (int k = 0; k < kHeld; ++k) held[k] = from + 64 * k < to ? expert_at(a, from + 64 * k + lane, to) : -1;
-#pragma unroll
-    for (int k = 0; k < kHeld; ++k)
-      if (held[k] >= 0) atomicAdd(&next[wave * E + held[k]], 1);
-  } else {
-    for (int64_t i = from + lane; i < to; i += 64) {
-      const int e = expert_at(a, i, to);
-      if (e >= 0) atomicAdd(&next[wave * E + e], 1);
-    }
+#pragma unroll 1
+  for (int64_t i = from + lane; i < to; i += 64) {
+    const int e = expert_at(a, i, to);
+    if (e >= 0) atomicAdd(&next[wave * E + e], 1);
   }
   if (!Single) {
     // thread = (expert, every parts-th tile)
-    const int parts = max(1, (int)blockDim.x / E);
-    for (int at = threadIdx.x; at < parts * E; at += blockDim.x) {
+    const int parts = max(1, Threads / E);
+    for (int at = threadIdx.x; at < parts * E; at += Threads) {
       const int e = at % E;
       int b = 0, t = 0;
 #pragma unroll 16
@@ -122,51 +113,59 @@ __global__ void __launch_bounds__(1024) rows_place_kernel(RowsArgs a) {
     }
   }
   __syncthreads();
-  if (Single) {
-    for (int e = threadIdx.x; e < E; e += blockDim.x) {
-      int t = 0;
-      for (int w = 0; w < waves; ++w) t += next[w * E + e];
-      total[e] = t;
-    }
-    __syncthreads();
+  // first rows: a scan of the padded counts over the experts, a run of Per of them to each thread
+  int used[Per][Waves], all[Per], size[Per], sum = 0;
+#pragma unroll
+  for (int p = 0; p < Per; ++p) {
+    const int e = threadIdx.x * Per + p;
+    int own = 0;
+#pragma unroll
+    for (int w = 0; w < Waves; ++w) used[p][w] = e < E ? next[w * E + e] : 0;
+#pragma unroll
+    for (int w = 0; w < Waves; ++w) own += used[p][w];
+    all[p] = Single ? own : e < E ? total[e] : 0;
+    size[p] = (int)(((uint32_t)all[p] + a.align - 1) / (uint32_t)a.align) * a.align;
+    sum += size[p];
   }
-  if (wave == 0) {  // scan of the padded counts, a run of experts to each lane
-    const int per = (E + 63) / 64, e0 = lane * per, e1 = min(E, e0 + per);
-    int sum = 0;
-    for (int e = e0; e < e1; ++e) {
-      start[e] = (int)(((uint32_t)total[e] + a.align - 1) / (uint32_t)a.align) * a.align;
-      sum += start[e];
-    }
-    int scan = sum;
-    for (int d = 1; d < 64; d *= 2) {
-      const int up = __shfl_up(scan, d);
-      if (lane >= d) scan += up;
-    }
-    int at = scan - sum;
-    for (int e = e0; e < e1; ++e) {
-      const int size = start[e];
+  int upto = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int up = __shfl_up(upto, d);
+    if (lane >= d) upto += up;
+  }
+  if (lane == 63) scan[wave] = upto;
+  __syncthreads();
+  int at = upto - sum;
+#pragma unroll
+  for (int w = 0; w < Waves; ++w) at += w < wave ? scan[w] : 0;
+#pragma unroll
+  for (int p = 0; p < Per; ++p) {
+    const int e = threadIdx.x * Per + p;
+    if (e < E) {
+      int row = at + before[e];
+#pragma unroll
+      for (int w = 0; w < Waves; ++w) {
+        next[w * E + e] = row;
+        row += used[p][w];
+      }
       start[e] = at;
-      at += size;
-    }
-    if (lane == 63) start[E] = scan;
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < E; e += blockDim.x) {
-    int at = start[e] + before[e];
-    for (int w = 0; w < waves; ++w) {
-      const int c = next[w * E + e];
-      next[w * E + e] = at;
-      at += c;
-    }
-    if (blockIdx.x == 0) {
-      a.offsets[e] = start[e];
-      if (a.counts) a.counts[e] = total[e];
+      total[e] = all[p];
+      if (blockIdx.x == 0) {
+        a.offsets[e] = at;
+        if (a.counts) a.counts[e] = all[p];
+      }
+      at += size[p];
+      if (e == E - 1) {
+        start[E] = at;
+        if (blockIdx.x == 0) a.offsets[E] = at;
+      }
     }
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[E] = start[E];
   __syncthreads();
-  const auto place = [&](int64_t base, int e) {
+#pragma unroll 1
+  for (int64_t base = from; base < to; base += 64) {
     const int64_t i = base + lane;
+    const int e = expert_at(a, i, to);
     const uint64_t same = same_expert(e);
     int row = -1;
     if (e >= 0) {
@@ -179,22 +178,15 @@ __global__ void __launch_bounds__(1024) rows_place_kernel(RowsArgs a) {
       else if (a.row_token) a.row_token[row] = (int32_t)((uint32_t)i / (uint32_t)a.top_k);
     }
     if (i < to && a.pair_row) a.pair_row[i] = row;
-  };
-  if (holds) {
-#pragma unroll
-    for (int k = 0; k < kHeld; ++k)
-      if (from + 64 * k < to) place(from + 64 * k, held[k]);
-  } else {
-    for (int64_t base = from; base < to; base += 64) place(base, expert_at(a, base + lane, to));
   }
   if (!a.row_token) return;
   // rows that hold no copy: behind each expert's copies (a wave per expert), and behind the last expert
-  for (int e = blockIdx.x * waves + wave; e < E; e += gridDim.x * waves) {
+  for (int e = blockIdx.x * Waves + wave; e < E; e += gridDim.x * Waves) {
     const int64_t end = start[e + 1] < a.n_rows ? start[e + 1] : a.n_rows;
     for (int64_t r = (int64_t)start[e] + total[e] + lane; r < end; r += 64) a.row_token[r] = -1;
   }
-  for (int64_t r = (int64_t)start[E] + blockIdx.x * blockDim.x + threadIdx.x; r < a.n_rows;
-       r += (int64_t)gridDim.x * blockDim.x)
+  for (int64_t r = (int64_t)start[E] + blockIdx.x * Threads + threadIdx.x; r < a.n_rows;
+       r += (int64_t)gridDim.x * Threads)
     a.row_token[r] = -1;
 }
 
@@ -246,7 +238,7 @@ wt_status wt_dispatch_rows(const int32_t *index, int64_t n_tokens, int32_t top_k
       return fail(what, "misaligned pointer", WT_E_ALIGN);
     if (workspace_bytes < need) return fail(what, "workspace too small", WT_E_RANGE);
     const bool single = pairs <= kRowsSingle && (!row_token || n_rows <= kRowsSingleFill);
-    const int waves = waves_for(n_experts), unit = 64 * waves;
+    const int waves = n_experts <= kManyExperts ? 16 : 8, unit = 64 * waves;
     RowsArgs a{};
     a.index = index;
     a.n_pairs = pairs;
@@ -266,13 +258,11 @@ wt_status wt_dispatch_rows(const int32_t *index, int64_t n_tokens, int32_t top_k
     const hipStream_t s = (hipStream_t)stream;
     const uint32_t grid = a.n_tiles > 0 ? (uint32_t)a.n_tiles : 1u, threads = 64u * waves;
     const uint32_t lds = 4u * ((waves + 3) * n_experts + 1);
-    if (single) {
-      hipLaunchKernelGGL((rows_place_kernel<true>), dim3(grid), dim3(threads), lds, s, a);
-    } else {
-      if (a.n_tiles > 0)
-        hipLaunchKernelGGL(rows_count_kernel, dim3(grid), dim3(threads), 4u * n_experts, s, a);
-      hipLaunchKernelGGL((rows_place_kernel<false>), dim3(grid), dim3(threads), lds, s, a);
-    }
+    if (!single && a.n_tiles > 0)
+      hipLaunchKernelGGL(rows_count_kernel, dim3(grid), dim3(threads), 4u * n_experts, s, a);
+    const auto kernel = single ? (waves == 16 ? rows_place_kernel<true, 16> : rows_place_kernel<true, 8>)
+                               : (waves == 16 ? rows_place_kernel<false, 16> : rows_place_kernel<false, 8>);
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(threads), lds, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return fail(what, hip_msg("launch", e), WT_E_HIP);
     return WT_OK;

@@ -190,12 +190,10 @@ __device__ __forceinline__ uint32_t bf16_nearest(float x) {
 }
 
 // fp32 -> BF16, the magnitude rounded up where the 16 dropped bits plus the
-// random ones reach a whole step; infinities and NaN keep their top bits (a
-// NaN whose payload sits in the dropped bits stays a NaN).
+// random ones reach a whole step. An infinity has no bits to carry; a NaN gives
+// up its payload, which could.
 __device__ __forceinline__ uint32_t bf16_random(float x, uint32_t r16) {
-  const uint32_t b = __float_as_uint(x);
-  if ((b & 0x7F800000u) == 0x7F800000u) return bf16_nearest(x);
-  return (b + r16) >> 16;
+  return ((x == x ? __float_as_uint(x) : 0x7FC00000u) + r16) >> 16;
 }
 
 constexpr uint32_t kFiniteEnd = 0x7F800000u;  // magnitude bits from here up: infinity, NaN
@@ -333,7 +331,7 @@ __device__ __forceinline__ void update_item(const AdamTensor &t, uint32_t chunk,
     root[e] = Bits == 8 ? fast_sqrt(v[e]) : sqrtf(v[e]);
     if (Bits == 8) {
       am = max(am, __float_as_uint(m[e]) & 0x7FFFFFFFu);
-      av = max(av, __float_as_uint(root[e]) & 0x7FFFFFFFu);
+      av = max(av, __float_as_uint(root[e]));  // no sign, unless it is a NaN's
     }
   }
   // some lane of the wave has a zero or subnormal v, a huge value, an infinity or NaN
@@ -360,15 +358,21 @@ __device__ __forceinline__ void update_item(const AdamTensor &t, uint32_t chunk,
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     const int64_t i = i0 + 64 * c, left = t.n - i;
-    uint32_t h[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int k = 4 * c + e;
+    for (int k = 4 * c; k < 4 * c + 4; ++k) {
       const float u = m[k] * __builtin_amdgcn_rcpf(fmaf(root[k], s.inv_bias2, s.eps));
       p[k] = fmaf(-rate, u, p[k] * decay);
-      h[e] = has_master ? bf16_nearest(p[k]) : bf16_random(p[k], (random_word(key, 4 * l + 64 * c + e) * 0x9E3779B9u) >> 16);
     }
-    if (has_master) store_f32<Full>(t.master, i, left, vec, p + 4 * c);
+    uint32_t h[4];
+    if (has_master) {
+      store_f32<Full>(t.master, i, left, vec, p + 4 * c);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) h[e] = bf16_nearest(p[4 * c + e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        h[e] = bf16_random(p[4 * c + e], (random_word(key, 4 * l + 64 * c + e) * 0x9E3779B9u) >> 16);
+    }
     if (has_param) store_bf16<Full>(t.param, i, left, vec, h);
   }
   if (Bits == 8) {

@@ -356,24 +356,24 @@ __device__ __forceinline__ void update_item(const AdamTensor &t, uint32_t chunk,
   // parameters; 1 / d by v_rcp_f32 (one bit): d lies in the normal range, and what the update is off by is far
   // below a rounding of p
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const int64_t i = i0 + 64 * c, left = t.n - i;
+  for (int e = 0; e < 8; ++e) {
+    const float u = m[e] * __builtin_amdgcn_rcpf(fmaf(root[e], s.inv_bias2, s.eps));
+    p[e] = fmaf(-rate, u, p[e] * decay);
+  }
+  uint32_t h[8];
+  if (has_master) {
 #pragma unroll
-    for (int k = 4 * c; k < 4 * c + 4; ++k) {
-      const float u = m[k] * __builtin_amdgcn_rcpf(fmaf(root[k], s.inv_bias2, s.eps));
-      p[k] = fmaf(-rate, u, p[k] * decay);
-    }
-    uint32_t h[4];
-    if (has_master) {
-      store_f32<Full>(t.master, i, left, vec, p + 4 * c);
+    for (int c = 0; c < 2; ++c) store_f32<Full>(t.master, i0 + 64 * c, t.n - i0 - 64 * c, vec, p + 4 * c);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) h[e] = bf16_nearest(p[4 * c + e]);
-    } else {
+    for (int e = 0; e < 8; ++e) h[e] = bf16_nearest(p[e]);
+  } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        h[e] = bf16_random(p[4 * c + e], (random_word(key, 4 * l + 64 * c + e) * 0x9E3779B9u) >> 16);
-    }
-    if (has_param) store_bf16<Full>(t.param, i, left, vec, h);
+    for (int e = 0; e < 8; ++e)
+      h[e] = bf16_random(p[e], (random_word(key, 4 * l + 64 * (e >> 2) + (e & 3)) * 0x9E3779B9u) >> 16);
+  }
+  if (has_param) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) store_bf16<Full>(t.param, i0 + 64 * c, t.n - i0 - 64 * c, vec, h + 4 * c);
   }
   if (Bits == 8) {
     float im, iv;

@@ -21,6 +21,7 @@ struct Range {
 };
 
 constexpr int64_t kMaxElements = (int64_t)1 << 46;
+constexpr double kMaxFactor = 1e6;  // of learning rates and decays: their products stay far from infinity
 
 uint64_t align256(uint64_t x) { return (x + 255) / 256 * 256; }
 
@@ -70,9 +71,8 @@ wt_status build_adamw(const wt_adamw_tensor *t, size_t n, const wt_adamw_options
     };
     if (a.n < 0 || a.n > kMaxElements) return bad("element count out of range");
     if (a.grad_dtype != WT_DT_F32 && a.grad_dtype != WT_DT_BF16) return bad("unknown gradient type");
-    if (!(a.lr_mul >= 0) || !std::isfinite(a.lr_mul)) return bad("lr_mul must be finite and not negative");
-    if (!(a.weight_decay >= 0) || !std::isfinite(a.weight_decay))
-      return bad("weight_decay must be finite and not negative");
+    if (!(a.lr_mul >= 0 && a.lr_mul <= kMaxFactor)) return bad("lr_mul must lie in [0, 1e6]");
+    if (!(a.weight_decay >= 0 && a.weight_decay <= kMaxFactor)) return bad("weight_decay must lie in [0, 1e6]");
     if (a.n == 0) continue;
     if (!a.param && !a.master) return bad("neither param nor master");
     if (!a.grad || !a.m || !a.v) return bad("NULL grad, m or v");
@@ -165,7 +165,7 @@ wt_status check_adamw_hyper(const wt_adamw_hyper *h, std::string *err) {
     return st;
   };
   if (!h) return bad("NULL hyper");
-  if (!(h->lr >= 0) || !std::isfinite(h->lr)) return bad("lr must be finite and not negative");
+  if (!(h->lr >= 0 && h->lr <= kMaxFactor)) return bad("lr must lie in [0, 1e6]");
   if (!(h->beta1 >= 0 && h->beta1 < 1) || !(h->beta2 >= 0 && h->beta2 < 1)) return bad("betas must lie in [0, 1)");
   if (!(h->eps >= 1e-30) || !(h->eps <= 1e30)) return bad("eps must lie in [1e-30, 1e30]");
   if (!std::isfinite(h->grad_scale) || std::fabs(h->grad_scale) > 1e30) return bad("grad_scale out of range");

@@ -558,7 +558,10 @@ wt_status create_impl(const wt_adamw_tensor *tensors, size_t n, const wt_adamw_o
   if (st != WT_OK) return fail(err, st);
   a->at = adamw_offsets(a->L);
   e = hipMalloc((void **)&a->mem, a->at.bytes);
-  if (e == hipErrorOutOfMemory) return fail("device allocation failed", WT_E_NOMEM);
+  if (e == hipErrorOutOfMemory) {
+    (void)hipGetLastError();
+    return fail("device allocation failed", WT_E_NOMEM);
+  }
   if (e == hipSuccess) e = hipMemset(a->mem, 0, a->at.bytes);
   if (e == hipSuccess && !a->L.tensors.empty())
     e = hipMemcpy(a->mem + a->at.tensors, a->L.tensors.data(), a->L.tensors.size() * sizeof(AdamTensor),

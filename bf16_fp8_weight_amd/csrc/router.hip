@@ -353,14 +353,18 @@ __device__ __forceinline__ void select_topk(const RouterArgs &a, int64_t t, cons
   // keys down to a quarter of the greatest, or all there are
   constexpr uint32_t kSpan = 0x01000000u;
   uint32_t lo = top > kSpan ? top - kSpan : 1u, step = kSpan / 2;
-  int steps = 9;
-  if (__popcll(__ballot(u >= lo)) < need) {
+  int n = __popcll(__ballot(u >= lo)), steps = 9;
+  if (n < need) {
     lo = 1u;
     step = 0x80000000u;
     steps = 20;
+    n = __popcll(__ballot(u >= lo));
   }
-  for (int i = 0; i < steps; ++i) {  // lo + step stays below 2^32
-    lo += __popcll(__ballot(u >= lo + step)) >= need ? step : 0u;
+  // lo + step stays below 2^32; keys that lie close together take more steps
+  for (int i = 0; i < steps || (n > need + 8 && step); ++i) {
+    const int m = __popcll(__ballot(u >= lo + step));
+    lo += m >= need ? step : 0u;
+    n = m >= need ? m : n;
     step >>= 1;
   }
   const bool all = lo == 1u;  // every selectable expert is a candidate
@@ -826,9 +830,13 @@ wt_status check_desc(const char *what, const wt_router_desc *d) {
   return WT_OK;
 }
 
+// Row strides whose last row still has a 64-bit byte offset.
+int64_t max_stride(int64_t n_tokens) { return ((int64_t)1 << 60) / (n_tokens > 1 ? n_tokens : 1); }
+
 wt_status check_memory_args(const char *what, const wt_router_desc *d) {
   const int64_t size = d->logits_dtype == WT_DT_BF16 ? 2 : 4;
-  if (d->logits_stride < d->n_experts || d->logits_stride > ((int64_t)1 << 40)) return fail(what, "logits_stride out of range");
+  if (d->logits_stride < d->n_experts || d->logits_stride > max_stride(d->n_tokens))
+    return fail(what, "logits_stride out of range");
   if (d->n_tokens > 0 && !d->logits) return fail(what, "NULL logits");
   if ((uintptr_t)d->logits % size) return fail(what, "logits misaligned", WT_E_ALIGN);
   if ((uintptr_t)d->bias % 4 || (uintptr_t)d->seq_offsets % 4) return fail(what, "bias or seq_offsets misaligned", WT_E_ALIGN);
@@ -946,7 +954,7 @@ wt_status wt_router_backward(const wt_router_desc *desc, const int32_t *index, c
     wt_status st = check_desc(what, desc);
     if (st == WT_OK) st = check_memory_args(what, desc);
     if (st != WT_OK) return st;
-    if (dlogits_stride < desc->n_experts || dlogits_stride > ((int64_t)1 << 40))
+    if (dlogits_stride < desc->n_experts || dlogits_stride > max_stride(desc->n_tokens))
       return fail(what, "dlogits_stride out of range");
     if (desc->n_tokens == 0) return WT_OK;
     if (!dlogits) return fail(what, "NULL dlogits");

@@ -594,6 +594,8 @@ class AdamW:
         (`keep` holds them: dicts of tensors by field name)."""
         import torch
 
+        if wl.shard_mem != "device":
+            raise ValueError("the step updates shards in device memory")
         shards = [s for o in wl.outputs for p in o.parts for s, r in zip(p.shards, p.shard_rows) if r]
         if len(grads) != len(shards):
             raise ValueError(f"{len(grads)} gradients for {len(shards)} non-empty shards")

@@ -563,8 +563,8 @@ typedef struct wt_adamw_tensor {
   float *v_scale;
   int64_t n;
   int32_t grad_dtype;
-  float lr_mul;       /* >= 0; multiplies the step's learning rate */
-  float weight_decay; /* >= 0 */
+  float lr_mul;       /* 0 .. 1e6; multiplies the step's learning rate */
+  float weight_decay; /* 0 .. 1e6 */
   int32_t reserved;
 } wt_adamw_tensor;
 
@@ -576,7 +576,7 @@ typedef struct wt_adamw_options {
 
 /* What one step takes. wt_adamw_hyper_init() fills the defaults. */
 typedef struct wt_adamw_hyper {
-  double lr;         /* 1e-3 */
+  double lr;         /* 1e-3; 0 .. 1e6 */
   double beta1;      /* 0.9; 0 <= beta < 1 */
   double beta2;      /* 0.999 */
   double eps;        /* 1e-8; at least 1e-30 */
@@ -614,7 +614,8 @@ wt_status wt_adamw_check(const wt_adamw_tensor *tensors, size_t n_tensors, const
                          wt_adamw_info *info);
 
 /* Builds the step's device tables. The table is copied; the tensors stay the
- * caller's and must outlive the handle at the same addresses. On failure *out
+ * caller's and must outlive the handle at the same addresses. Allocates and
+ * copies, so not for use under stream capture. On failure *out
  * is NULL and wt_plan_last_error(NULL) says why (likewise for the calls
  * below). */
 wt_status wt_adamw_create(const wt_adamw_tensor *tensors, size_t n_tensors, const wt_adamw_options *opts,

@@ -59,7 +59,7 @@ def test_refusals(wt, bits):
     assert _status(wt, [_t(wt, n=1 << 47)], bits) == E.WT_E_INVAL
     assert _status(wt, [_t(wt, grad_dtype=2)], bits) == E.WT_E_INVAL
     for k in ("lr_mul", "weight_decay"):
-        for x in (-1.0, math.nan, math.inf):
+        for x in (-1.0, math.nan, math.inf, 2e6):
             assert _status(wt, [_t(wt, **{k: x})], bits) == E.WT_E_INVAL
     assert _status(wt, [_t(wt, param=0x100001)], bits) == E.WT_E_ALIGN
     assert _status(wt, [_t(wt, master=0x200002)], bits) == E.WT_E_ALIGN

@@ -476,6 +476,28 @@ def test_handle_refuses_memory_it_cannot_use(wt):
     assert e.value.status == wt.WT_E_INVAL
 
 
+def test_hyper_values_refused(wt):
+    t = Tensor(256, 8, "fp32", True, True)
+    before = t.snapshot()
+    with wt.AdamW([t.entry(wt)], 8) as a:
+        for k, x in (("lr", -1.0), ("lr", math.nan), ("lr", 2e6), ("beta1", 1.0), ("beta1", -0.1), ("beta2", 1.0),
+                     ("beta2", math.nan), ("eps", 0.0), ("eps", math.inf), ("grad_scale", math.inf),
+                     ("grad_scale", math.nan), ("max_norm", -1.0), ("max_norm", math.inf), ("step", 0)):
+            with pytest.raises(wt.WtError) as e:
+                a.step(hyper(wt, **{k: x}), 0)
+            assert e.value.status == wt.WT_E_INVAL and k.split("_")[0].rstrip("12") in str(e.value), str(e.value)
+        for k in ("step_dev", "lr_dev", "norm_out"):
+            with pytest.raises(wt.WtError) as e:
+                a.step(hyper(wt, **{k: 0x1002}), 0)
+            assert e.value.status == wt.WT_E_ALIGN
+        with pytest.raises(wt.WtError) as e:
+            wt.wt_adamw_step(0, hyper(wt), 0)
+        assert e.value.status == wt.WT_E_INVAL
+    torch.cuda.synchronize()
+    after = t.snapshot()
+    assert all(np.array_equal(before[k].view(np.uint8), after[k].view(np.uint8)) for k in before)
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_step_then_prepare_of_the_same_shards(wt, bits):
     # what a training step and the transfer behind it do: update the shards in place, prepare them on the same

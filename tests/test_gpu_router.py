@@ -238,6 +238,27 @@ def test_near_ties_are_decided_in_64_bits(wt):
 
 
 @pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("centre", [0.0, 100.0, -60.0])
+@pytest.mark.parametrize("spread", [1e-2, 1e-4, 1e-6, 0.0])
+def test_logits_close_together(wt, kind, centre, spread):
+    # a router at its start: all keys nearly alike, so that thresholds far below the greatest separate nothing
+    E, T = 384, 40
+    x = centre + spread * torch.randn(T, E, generator=torch.Generator().manual_seed(3))
+    for b in (None, torch.zeros(E), 0.01 * bias(E)):
+        Case(wt, x, 8, kind, bias=b).check_forward()
+    Case(wt, x.to(torch.bfloat16), 8, kind).check_forward()
+
+
+def test_as_many_places_as_experts(wt):
+    for E, K in ((32, 32), (64, 32), (33, 32), (2, 2), (5, 5)):
+        for b in (None, bias(E)):
+            c = Case(wt, logits(50, E, seed=E), K, "sigmoid", bias=b)
+            c.check_forward()
+            c.check_backward()
+            Case(wt, logits(50, E, torch.bfloat16, seed=E), K, "softmax", bias=b).check_forward()
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
 @pytest.mark.parametrize("with_bias", [False, True])
 def test_experts_switched_off(wt, kind, with_bias):
     # -infinity: some experts, all but two (fewer than top_k), all

@@ -64,6 +64,7 @@ def test_forward_refusals(wt):
     f(wt.WT_E_RANGE, workspace_bytes=n - 1)
     f(wt.WT_E_INVAL, _desc(wt, logits=None))
     f(wt.WT_E_INVAL, _desc(wt, logits_stride=47))
+    f(wt.WT_E_INVAL, _desc(wt, logits_stride=2 ** 60 // 100 + 1))
     f(wt.WT_E_ALIGN, _desc(wt, logits=A + 2))
     f(wt.WT_E_ALIGN, _desc(wt, logits=A + 1, logits_dtype=wt.WT_DT_BF16))
     f(wt.WT_E_ALIGN, _desc(wt, bias=A + 1))
@@ -80,6 +81,7 @@ def test_backward_refusals(wt):
     f(wt.WT_E_INVAL, index=0)
     f(wt.WT_E_INVAL, seq_counts=0)
     f(wt.WT_E_INVAL, stride=47)
+    f(wt.WT_E_INVAL, stride=2 ** 62)
     f(wt.WT_E_ALIGN, dlogits=A + 2)
     for k in ("index", "seq_counts", "dweight", "dloss"):
         f(wt.WT_E_ALIGN, **{k: A + 2})

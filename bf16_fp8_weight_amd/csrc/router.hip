@@ -352,19 +352,17 @@ __device__ __forceinline__ void select_topk(const RouterArgs &a, int64_t t, cons
   const int need = a.top_k + 1;
   // keys down to a quarter of the greatest, or all there are
   constexpr uint32_t kSpan = 0x01000000u;
-  uint32_t lo = top > kSpan ? top - kSpan : 1u, step = kSpan / 2;
-  int n = __popcll(__ballot(u >= lo)), steps = 9;
-  if (n < need) {
+  uint32_t lo = top > kSpan ? top - kSpan : 1u, step;  // lo + step stays below 2^32
+  if (__popcll(__ballot(u >= lo)) >= need) {
+#pragma unroll
+    for (step = kSpan / 2; step > kSpan >> 10; step >>= 1) lo += __popcll(__ballot(u >= lo + step)) >= need ? step : 0u;
+  } else {
     lo = 1u;
-    step = 0x80000000u;
-    steps = 20;
-    n = __popcll(__ballot(u >= lo));
+    for (step = 0x80000000u; step > kSpan >> 10; step >>= 1) lo += __popcll(__ballot(u >= lo + step)) >= need ? step : 0u;
   }
-  // lo + step stays below 2^32; keys that lie close together take more steps
-  for (int i = 0; i < steps || (n > need + 8 && step); ++i) {
-    const int m = __popcll(__ballot(u >= lo + step));
-    lo += m >= need ? step : 0u;
-    n = m >= need ? m : n;
+  // keys that lie close together take more steps
+  while (__popcll(__ballot(u >= lo)) > need + 8 && step) {
+    lo += __popcll(__ballot(u >= lo + step)) >= need ? step : 0u;
     step >>= 1;
   }
   const bool all = lo == 1u;  // every selectable expert is a candidate

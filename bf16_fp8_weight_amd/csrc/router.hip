@@ -249,50 +249,55 @@ __device__ __forceinline__ int place(uint64_t who, int base) {
   return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who, (uint32_t)base));
 }
 
-// The selection of a token that select_topk cannot decide, by keys in 64 bits:
-// all experts whose fp32 keys reach `reach` are ranked, or, if those are more
-// than 64, the experts are taken one after the other. The candidates are left
-// in the order of their ranks. Returns their number.
+// Packs the experts of the lane masks to one per lane, in the order of their
+// numbers.
+template <int NJ>
+__device__ __forceinline__ void collect(const uint64_t who[NJ], const float k[NJ], const float s[NJ], int lane,
+                                        Candidates &c) {
+  int base = 0;
+#pragma unroll
+  for (int j = 0; j < NJ; ++j)
+    if (who[j]) {
+      const int at = place(who[j], base);
+      if (who[j] >> lane & 1) {
+        c.key[at] = k[j];
+        c.score[at] = s[j];
+        c.expert[at] = lane + 64 * j;
+      }
+      base += __popcll(who[j]);
+    }
+  wave_lds_fence();
+}
+
+// Ranks the wave's `count` <= 64 candidates by keys in 64 bits and leaves them
+// in that order.
 template <bool Softmax, bool Bias>
-__device__ __forceinline__ int select_exact(const RouterArgs &a, int64_t t, const Norm &n, int lane, float reach,
-                                            Candidates &c) {
+__device__ __forceinline__ void rank_exact(const RouterArgs &a, int64_t t, int lane, int count, Candidates &c) {
   double top = 0.0, z = 1.0;
   if (Softmax && Bias) softmax64(a, t, lane, &top, &z);
-  int count = 0;
+  const float s = c.score[lane];
+  const uint32_t e = c.expert[lane];
+  const double key = lane < count ? exact_key<Softmax, Bias>(a, t, e, top, z) : 0.0;
+  int rank = lane < count ? 0 : lane;
 #pragma unroll 1
-  for (int base = 0; base < a.n_experts; base += 64) {
-    const int e = base + lane;
-    float x = -INFINITY;
-    if (e < a.n_experts) x = load_logit(a, t, e);
-    const float s = score_of<Softmax>(n, x), k = Bias && e < a.n_experts ? s + a.bias[e] : x;
-    const uint64_t who = __ballot(selectable(x) && k >= reach);
-    const int at = place(who, count);
-    if ((who >> lane & 1) && at < 64) {
-      c.score[at] = s;
-      c.expert[at] = e;
-    }
-    count += __popcll(who);
+  for (int i = 0; i < count; ++i) {
+    const double other = __shfl(key, i);
+    rank += lane < count && (other > key || (other == key && i < lane)) ? 1 : 0;
   }
   wave_lds_fence();
-  if (count <= 64) {
-    const float s = c.score[lane];
-    const uint32_t e = c.expert[lane];
-    const double key = lane < count ? exact_key<Softmax, Bias>(a, t, e, top, z) : 0.0;
-    int rank = lane < count ? 0 : lane;
-#pragma unroll 1
-    for (int i = 0; i < count; ++i) {
-      const double other = __shfl(key, i);
-      rank += lane < count && (other > key || (other == key && i < lane)) ? 1 : 0;
-    }
-    wave_lds_fence();
-    c.score[rank] = s;
-    c.expert[rank] = e;
-    wave_lds_fence();
-    return count;
-  }
-  double last = INFINITY;
-  int last_e = -1;
-  for (count = 0; count < a.top_k; ++count) {
+  c.score[rank] = s;
+  c.expert[rank] = e;
+  wave_lds_fence();
+}
+
+// Selection one expert after the other by keys in 64 bits, for a token with
+// more candidates than lanes (many equal keys). Returns how many were found.
+template <bool Softmax, bool Bias>
+__device__ __forceinline__ int select_rounds(const RouterArgs &a, int64_t t, const Norm &n, int lane, Candidates &c) {
+  double top = 0.0, z = 1.0, last = INFINITY;
+  if (Softmax && Bias) softmax64(a, t, lane, &top, &z);
+  int count = 0, last_e = -1;
+  for (; count < a.top_k; ++count) {
     // the greatest key behind the last one taken, and of equals the lowest expert
     double best = -INFINITY;
     int at = kMaxExperts;
@@ -333,8 +338,9 @@ __device__ __forceinline__ int select_exact(const RouterArgs &a, int64_t t, cons
 //
 // With a bias the keys carry roundings. Where two neighbours of the first
 // top_k + 1 (or of a run of equals across that border and the next behind it)
-// are too close and not of the same logit and bias, select_exact decides; as
-// it does where there are more than 64 candidates.
+// are too close and not of the same logit and bias, all experts within reach
+// of the last place are ranked by keys in 64 bits. More than 64 candidates
+// (many equal keys) are selected one after the other.
 template <int NJ, bool Softmax, bool Bias>
 __device__ __forceinline__ void select_topk(const RouterArgs &a, int64_t t, const Norm &norm, const float x[NJ],
                                             const float s[NJ], const float b[NJ], int lane, Candidates &c, int *index,
@@ -377,19 +383,7 @@ __device__ __forceinline__ void select_topk(const RouterArgs &a, int64_t t, cons
   float reach = least;
   bool decided = count <= 64;
   if (decided) {
-    int base = 0;
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-      if (who[j]) {
-        const int at = place(who[j], base);
-        if (k[j] >= least) {
-          c.key[at] = k[j];
-          c.score[at] = s[j];
-          c.expert[at] = lane + 64 * j;
-        }
-        base += __popcll(who[j]);
-      }
-    wave_lds_fence();
+    collect<NJ>(who, k, s, lane, c);
     const bool mine = lane < count;  // this lane holds a candidate
     const float key = mine ? c.key[lane] : -INFINITY;
     float sc = c.score[lane];
@@ -439,7 +433,21 @@ __device__ __forceinline__ void select_topk(const RouterArgs &a, int64_t t, cons
       }
     }
   }
-  if (!decided) count = select_exact<Softmax, Bias>(a, t, norm, lane, reach, c);
+  if (!decided) {
+    count = 0;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      who[j] = __ballot(k[j] >= reach);
+      count += __popcll(who[j]);
+    }
+    wave_lds_fence();
+    if (count <= 64) {
+      collect<NJ>(who, k, s, lane, c);
+      rank_exact<Softmax, Bias>(a, t, lane, count, c);
+    } else {
+      count = select_rounds<Softmax, Bias>(a, t, norm, lane, c);
+    }
+  }
   if (lane < a.top_k && lane < count) {
     *index = (int)c.expert[lane];
     *score = c.score[lane];
@@ -787,8 +795,11 @@ __global__ void __launch_bounds__(64 * kBackWaves) router_backward_kernel(Router
 int32_t tile_of(int64_t n_tokens) { return n_tokens <= 8192 ? 16 : n_tokens <= 32768 ? 32 : 64; }
 int32_t back_tile_of(int64_t n_tokens) { return n_tokens <= 8192 ? 4 : 16; }
 
-// Partial sums up to which one workgroup reduces them.
-constexpr int64_t kSmallSums = 32768;
+// Partial sums up to which one workgroup reduces them. Measured on MI355X, the
+// whole forward pass of 384 experts with one workgroup / with two launches:
+// 128 tokens (3,456 sums) 10.3 / 10.8 us, 512 tokens (12,672) 11.9 / 11.3 us,
+// 1024 tokens 16.1 / 14.2 us.
+constexpr int64_t kSmallSums = 8192;
 constexpr int32_t kSmallSeqs = 8;
 
 int chunks_of(int n_experts) { return (n_experts + kChunk - 1) / kChunk; }

@@ -1,5 +1,14 @@
 // router.hip -- expert selection, per-expert counts and the balance loss of
 // a routed layer, forward and backward, for gfx950. The definition is in wt.h.
+//
+// Forward: one pass over the logits leaves selections, weights and, per tile
+// of tokens and sequence, sums of probabilities and counts; one or two small
+// launches reduce those. Bound by instructions: 16384 tokens x 384 experts are
+// 25 MB, 4 us at the card's copy rate, and take 18 us (250 vector and 200
+// scalar instructions a token, four waves to a SIMD half of the time waiting
+// for one another's results), 22.6 us with the reductions. Backward: one pass
+// that reads the logits again and writes their gradient, 51 MB in 11.3 us
+// (4.5 TB/s).
 #include <hip/hip_runtime.h>
 
 #include <cmath>

@@ -520,8 +520,10 @@ wt_status wt_dispatch_rows(const int32_t *index, int64_t n_tokens, int32_t top_k
  *   p' = p - lr lr_mul (weight_decay p + u)
  * all in fp32. p is the fp32 master copy if the tensor has one (the BF16 shard
  * then receives p' rounded to nearest even), else the BF16 shard itself.
- * clip = min(1, max_norm / (norm + 1e-6)), norm = grad_scale * sqrt(the sum of
- * grad^2 over every tensor); 1 when max_norm is 0.
+ * clip = min(1, max_norm / (norm + 1e-6)), norm = |grad_scale| sqrt(the sum of
+ * grad^2 over every tensor); 1 when max_norm is 0. The squares are taken in
+ * fp32 (added in 64 bits): a gradient beyond 1.8e19 makes the norm infinite,
+ * one below 1e-23 counts as 0.
  *
  * Rounded states. Where fewer than 32 bits carry a value from step to step
  * (8-bit states, a BF16 shard without a master), rounding to nearest would

@@ -197,6 +197,60 @@ def test_long_batch_with_larger_tiles(wt):
     c.check_backward()
 
 
+def test_thousands_of_sequences(wt):
+    # more sequences than one probe of the search covers, many of them empty, padding at both ends
+    T, E, K, S = 3000, 16, 2, 5000
+    g = torch.Generator().manual_seed(1)
+    offsets = torch.sort(torch.randint(5, T - 7, (S + 1,), generator=g)).values
+    c = Case(wt, logits(T, E, seed=21), K, "sigmoid", bias=bias(E), offsets=offsets.tolist())
+    c.forward()
+    torch.cuda.synchronize()
+    x = c.x.double()
+    s = torch.sigmoid(x)
+    p = s / s.sum(1, keepdim=True)
+    top = torch.sort(s + c.bias.cpu().double(), dim=1, descending=True, stable=True).indices[:, :K]
+    t = torch.arange(T)
+    live = (t >= offsets[0]) & (t < offsets[-1])
+    assert torch.equal(c.index[:T].cpu().long(), torch.where(live[:, None], top, -1))
+    seq = torch.searchsorted(offsets, t[live], right=True) - 1
+    n = torch.bincount(seq, minlength=S).double()
+    counts = torch.zeros(S, E, dtype=torch.float64).index_add_(0, seq, torch.zeros(int(live.sum()), E, dtype=torch.float64).scatter_(1, top[live], 1.0))
+    assert torch.equal(c.seq_counts.cpu().double(), counts) and torch.equal(c.counts.cpu().double(), counts.sum(0))
+    psum = torch.zeros(S, E, dtype=torch.float64).index_add_(0, seq, p[live])
+    loss = c.coef / S * float((E / K * counts * psum).sum(1).div(n.clamp(min=1) ** 2).sum())
+    assert abs(float(c.loss[0]) - loss) <= 80 * EPS32 * loss
+    c.check_backward()
+
+
+def test_two_calls_at_once(wt):
+    # two streams, each with buffers of its own, many calls in flight on both
+    cs = [Case(wt, logits(2500, 200, seed=k), 6, "sigmoid", bias=bias(200), offsets=[0, 900, 2490]) for k in (1, 2)]
+    want = []
+    for c in cs:
+        c.forward()
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in (c.index, c.weight, c.counts, c.seq_counts, c.loss)])
+    n_rows = 2500 * 6
+    rows = []
+    for c in cs:
+        size = wt.wt_dispatch_workspace_bytes(2500, 6, 200)
+        i32 = dict(dtype=torch.int32, device="cuda")
+        rows.append((torch.empty(n_rows, **i32), torch.empty(2500, 6, **i32), torch.empty(201, **i32),
+                     torch.empty(size, dtype=torch.uint8, device="cuda")))
+    streams = [torch.cuda.Stream() for _ in cs]
+    for _ in range(20):
+        for c, r, s in zip(cs, rows, streams):
+            c.forward(s.cuda_stream)
+            wt.wt_dispatch_rows(c.index.data_ptr(), 2500, 6, 200, 1, n_rows, r[0].data_ptr(), r[1].data_ptr(),
+                                r[2].data_ptr(), 0, r[3].data_ptr(), r[3].numel(), s.cuda_stream)
+    torch.cuda.synchronize()
+    for c, w, r in zip(cs, want, rows):
+        for t, x in zip((c.index, c.weight, c.counts, c.seq_counts, c.loss), w):
+            assert torch.equal(t, x)
+        ref = R.rows(c.index[:2500].cpu().numpy(), 200, 1, n_rows)
+        assert np.array_equal(r[0].cpu().numpy(), ref[0]) and np.array_equal(r[1].cpu().numpy(), ref[1])
+
+
 def test_no_tokens(wt):
     c = Case(wt, torch.zeros(0, 24), 3, offsets=[0, 0, 0])
     c.forward()

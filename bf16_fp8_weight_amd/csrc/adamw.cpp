@@ -123,7 +123,7 @@ wt_status build_adamw(const wt_adamw_tensor *t, size_t n, const wt_adamw_options
     if (vec) d.flags |= kAdamVector, L->info.n_vector_tensors++;
     blocks += nb;
     items += (e + item - 1) / item;
-    if (blocks >> 32 || items >> 31) {
+    if (blocks >> 32 || (items * (item / 8)) >> 32) {  // numbers of blocks; threads of the launch, eight elements each
       *err = at + "the table holds too many elements";
       return WT_E_INVAL;
     }

@@ -25,6 +25,7 @@ namespace {
 
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 32;
+constexpr int64_t kMaxTokens = (int64_t)1 << 27;  // sixteen threads each (backward) stay below a launch's 2^32
 
 constexpr int kWaves = 8;  // of a workgroup of the forward pass
 
@@ -838,7 +839,8 @@ wt_status check_desc(const char *what, const wt_router_desc *d) {
   if (!d) return fail(what, "NULL description");
   if (d->n_experts < 1 || d->n_experts > kMaxExperts) return fail(what, "n_experts out of range");
   if (d->top_k < 1 || d->top_k > kMaxTopK || d->top_k > d->n_experts) return fail(what, "top_k out of range");
-  if (d->n_tokens < 0 || d->n_tokens > (((int64_t)1 << 31) - 1) / d->top_k) return fail(what, "n_tokens out of range");
+  if (d->n_tokens < 0 || d->n_tokens > kMaxTokens || d->n_tokens * d->top_k >= (int64_t)1 << 31)
+    return fail(what, "n_tokens out of range");
   if (d->logits_dtype != WT_DT_F32 && d->logits_dtype != WT_DT_BF16) return fail(what, "unknown logits type");
   if (d->score != WT_SCORE_SIGMOID && d->score != WT_SCORE_SOFTMAX) return fail(what, "unknown score");
   if (d->normalize != 0 && d->normalize != 1) return fail(what, "normalize must be 0 or 1");

@@ -421,8 +421,8 @@ enum { WT_DT_F32 = 0, WT_DT_BF16 = 1 };
  *   weight_k = scale s_k, with `normalize` scale s_k / (sum over the selected
  *     s + 1e-20). The bias takes part in the selection alone.
  *   probability p_e = s_e (softmax), s_e / (sum_j s_j + 1e-20) (sigmoid)
- * An expert whose logit is -infinity or NaN is never selected (a way to switch
- * experts off); where fewer than top_k are left, the remaining places hold
+ * An expert whose logit (or bias) is -infinity or NaN is never selected (a way
+ * to switch experts off); where fewer than top_k are left, the remaining places hold
  * index -1 and weight 0. A token with no expert left has probabilities 0. A
  * NaN logit still reaches the loss as NaN, and with softmax the weights (with
  * softmax and a bias no key of such a token is a number, and none is selected).
@@ -440,7 +440,7 @@ enum { WT_DT_F32 = 0, WT_DT_BF16 = 1 };
 enum { WT_SCORE_SIGMOID = 0, WT_SCORE_SOFTMAX = 1 };
 
 typedef struct wt_router_desc {
-  int64_t n_tokens;       /* 0 <= n_tokens < 2^31 / top_k */
+  int64_t n_tokens;       /* 0 .. 2^27, with n_tokens top_k < 2^31 */
   int32_t n_experts;      /* 1 .. 1024 */
   int32_t top_k;          /* 1 .. min(n_experts, 32) */
   const void *logits;     /* n_tokens rows, device */

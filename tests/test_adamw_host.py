@@ -71,6 +71,17 @@ def test_refusals(wt, bits):
     assert _status(wt, [_t(wt)], 16) == E.WT_E_INVAL
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_more_elements_than_a_launch_holds(wt, bits):
+    # a thread updates eight elements, and a launch holds fewer than 2^32 threads
+    big = dict(param=1 << 44, master=0, grad=2 << 44, m=3 << 44, v=4 << 44, m_scale=5 << 44, v_scale=6 << 44)
+    assert _status(wt, [_t(wt, n=2 ** 35, **big)], bits) == wt.WT_E_INVAL
+    with pytest.raises(wt.WtError, match="too many elements"):
+        o = wt.wt_adamw_options_init()
+        o.state_bits = bits
+        wt.wt_adamw_check(wt.AdamWTable([_t(wt, n=2 ** 35, **big)]), o)
+
+
 def test_overlaps(wt):
     E = wt
     base = 0x100000

@@ -361,6 +361,27 @@ def test_infinities_and_nan(wt, kind, with_bias):
     assert bool(torch.isfinite(out).all())
 
 
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_masks_of_the_lowest_value_and_endless_biases(wt, kind, dtype, with_bias):
+    x = logits(30, 70, dtype, seed=6)
+    x[:, 3:9] = torch.finfo(dtype).min
+    x[4] = torch.finfo(dtype).min
+    x[5, 8:] = torch.finfo(dtype).min
+    x[6] = -math.inf
+    b = None
+    if with_bias:
+        b = bias(70)
+        b[10], b[11], b[12], b[13] = math.inf, -math.inf, math.nan, math.inf
+    c = Case(wt, x, 6, kind, True, bias=b)
+    index, _ = c.check_forward()
+    if with_bias:
+        live = index[[t for t in range(30) if t != 6]]
+        assert (live[:, 0] == 10).all() and (live[:, 1] == 13).all() and not np.isin(index, [11, 12]).any()
+    c.check_backward(dweight=False)
+
+
 def test_offsets_that_make_no_sense_stay_inside_the_arrays(wt):
     # falling, negative and too large offsets: the results mean nothing, the guards stay whole
     for offsets in ([50, 10, 90, 0], [-5, 1 << 30], [100, 0], [7, -7, 7, -7, 7], [2 ** 31 - 1, -(2 ** 31)]):

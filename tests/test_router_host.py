@@ -47,6 +47,14 @@ def test_descriptions_refused(wt, field, value):
     _refused(wt, wt.WT_E_INVAL, wt.wt_router_backward, d, A, A, A, A, A, 48)
 
 
+def test_more_tokens_than_a_launch_holds(wt):
+    # one place per token: index and weight would still have 32-bit sizes, the grid and the token numbers not
+    assert wt.wt_router_workspace_bytes(_desc(wt, n_tokens=2 ** 27, top_k=1)) > 2 ** 27
+    for n in (2 ** 27 + 1, 2 ** 31 - 1):
+        _refused(wt, wt.WT_E_INVAL, wt.wt_router_workspace_bytes, _desc(wt, n_tokens=n, top_k=1))
+        _refused(wt, wt.WT_E_INVAL, wt.wt_router_backward, _desc(wt, n_tokens=n, top_k=1), A, A, A, A, A, 48)
+
+
 def test_forward_refusals(wt):
     n = wt.wt_router_workspace_bytes(_desc(wt))
     assert 0 < n < 1 << 20

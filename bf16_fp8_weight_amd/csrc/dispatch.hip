@@ -4,14 +4,19 @@
 // A copy's row = its expert's first row + the copies of that expert in the
 // tiles before its own, in the waves before its own, and in the lanes before
 // its own. Counts come from integer histograms and lane masks, never from the
-// order of atomics. Up to kRowsSingle copies one workgroup does everything (one
+// order of atomics. Up to kRowsSingle copies one workgroup places them all (one
 // launch); beyond, a first launch counts each tile and the second one's
 // workgroups each add up what they need of the (at most 64) tiles' counts (side
-// by side, where a scan kernel between the two took 12 us alone). Nothing here
-// is bound by bytes: 16384 tokens move 1.8 MB in 14.4 us, which go to the
-// launches, five barriers, and reads and scattered writes that wait for L2.
+// by side, where a scan kernel between the two took 12 us alone). Workgroups
+// behind the last tile take part in filling the rows that hold no copy; with one
+// tile each of them counts the copies for itself. Nothing here is bound by
+// bytes: 16384 tokens move 1.8 MB in 14 us, which go to two launches, five
+// barriers, and reads and scattered writes that wait for L2. Tiles of 1024,
+// 2048 and 4096 copies (at most 128, 64 and 64 of them): 1024 tokens 8.9 / 9.3
+// / 11.4 us, 8192 tokens 13.1 / 11.4 / 13.3, 16384 tokens 18.0 / 13.9 / 14.0.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <string>
 
 #include "hip_util.h"
@@ -26,10 +31,14 @@ constexpr int kMaxExperts = 1024;
 constexpr int kMaxTiles = 64;
 constexpr int64_t kRowsTile = 2048;    // copies of one workgroup, more where there would be over 64 tiles
 // Copies up to which one workgroup takes them all. Measured on MI355X, 8 copies
-// of each token over 384 experts, one workgroup / two launches: 128 tokens 7.3 /
-// 9.2 us, 256 tokens 8.5 / 10.7, 512 tokens 10.8 / 10.0, 1024 tokens 15.4 / 10.0.
-constexpr int64_t kRowsSingle = 2048;
-constexpr int64_t kRowsSingleFill = 65536;     // rows that one workgroup may have to fill
+// of each token over 384 experts, one workgroup / two launches: 256 tokens 5.9 /
+// 8.1 us, 512 tokens 8.3 / 8.8, 1024 tokens 12.7 / 9.3.
+constexpr int64_t kRowsSingle = 4096;
+// Rows for which there is one workgroup to fill them. 128 tokens over 384 experts
+// in tiles of 128 rows, with one workgroup per 1024 / 4096 / 16384 rows 5.2 / 5.3
+// / 6.5 us (in tiles of 16 rows 5.6 / 8.5 / 8.5), 9.6 us when one fills them all.
+constexpr int64_t kRowsFill = 1024;
+constexpr int64_t kMaxFill = 256;
 
 struct RowsArgs {
   const int32_t *index;
@@ -85,7 +94,7 @@ __global__ void __launch_bounds__(64 * Waves) rows_place_kernel(RowsArgs a) {
   int *before = next + Waves * E;  // [expert]: copies in the tiles before
   int *total = before + E;         // [expert]: copies in all tiles
   int *start = total + E;          // [expert + 1]: first rows
-  const int64_t lo = blockIdx.x * a.tile, hi = lo + a.tile < a.n_pairs ? lo + a.tile : a.n_pairs;
+  const int64_t lo = Single ? 0 : blockIdx.x * a.tile, hi = lo + a.tile < a.n_pairs ? lo + a.tile : a.n_pairs;
   const int64_t part = a.tile / Waves, from = lo + wave * part, to = from + part < hi ? from + part : hi;
   for (int e = threadIdx.x; e < (Waves + 2) * E; e += Threads) lds[e] = 0;
   __syncthreads();
@@ -161,7 +170,7 @@ __global__ void __launch_bounds__(64 * Waves) rows_place_kernel(RowsArgs a) {
   }
   __syncthreads();
 #pragma unroll 1
-  for (int64_t base = from; base < to; base += 64) {
+  for (int64_t base = !Single || blockIdx.x == 0 ? from : to; base < to; base += 64) {
     const int64_t i = base + lane;
     const int e = expert_at(a, i, to);
     const uint64_t same = same_expert(e);
@@ -179,7 +188,7 @@ __global__ void __launch_bounds__(64 * Waves) rows_place_kernel(RowsArgs a) {
   }
   if (!a.row_token) return;
   // rows that hold no copy: behind each expert's copies (a wave per expert), and behind the last expert
-  for (int e = blockIdx.x * Waves + wave; e < E; e += gridDim.x * Waves) {
+  for (int e = a.align > 1 ? blockIdx.x * Waves + wave : E; e < E; e += gridDim.x * Waves) {
     const int64_t end = start[e + 1] < a.n_rows ? start[e + 1] : a.n_rows;
     for (int64_t r = (int64_t)start[e] + total[e] + lane; r < end; r += 64) a.row_token[r] = -1;
   }
@@ -235,7 +244,7 @@ wt_status wt_dispatch_rows(const int32_t *index, int64_t n_tokens, int32_t top_k
          (uintptr_t)workspace) % 4)
       return fail(what, "misaligned pointer", WT_E_ALIGN);
     if (workspace_bytes < need) return fail(what, "workspace too small", WT_E_RANGE);
-    const bool single = pairs <= kRowsSingle && (!row_token || n_rows <= kRowsSingleFill);
+    const bool single = pairs <= kRowsSingle;
     const int waves = n_experts <= kManyExperts ? 16 : 8, unit = 64 * waves;
     RowsArgs a{};
     a.index = index;
@@ -254,10 +263,12 @@ wt_status wt_dispatch_rows(const int32_t *index, int64_t n_tokens, int32_t top_k
     if (a.tile == 0) a.tile = unit;
     a.n_tiles = (int32_t)((pairs + a.tile - 1) / a.tile);
     const hipStream_t s = (hipStream_t)stream;
-    const uint32_t grid = a.n_tiles > 0 ? (uint32_t)a.n_tiles : 1u, threads = 64u * waves;
+    // workgroups behind the last tile only fill rows
+    const int64_t fill = row_token ? std::min<int64_t>(n_rows / kRowsFill, kMaxFill) : 0;
+    const uint32_t grid = (uint32_t)std::max<int64_t>({1, a.n_tiles, fill}), threads = 64u * waves;
     const uint32_t lds = 4u * ((waves + 3) * n_experts + 1);
     if (!single && a.n_tiles > 0)
-      hipLaunchKernelGGL(rows_count_kernel, dim3(grid), dim3(threads), 4u * n_experts, s, a);
+      hipLaunchKernelGGL(rows_count_kernel, dim3((uint32_t)a.n_tiles), dim3(threads), 4u * n_experts, s, a);
     const auto kernel = single ? (waves == 16 ? rows_place_kernel<true, 16> : rows_place_kernel<true, 8>)
                                : (waves == 16 ? rows_place_kernel<false, 16> : rows_place_kernel<false, 8>);
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(threads), lds, s, a);

@@ -47,8 +47,11 @@ def value(x, index, seq_counts, dweight, dloss, *, kind, top_k, normalize, scale
     E = x.shape[1]
     S = len(offsets) - 1
     total = x.new_zeros(())
-    s = torch.sigmoid(x) if kind == "sigmoid" else torch.softmax(x, dim=1)
-    p = s / s.sum(1, keepdim=True) if kind == "sigmoid" else s
+    # a token whose experts are all switched off has no scores
+    none = (x == -float("inf")).all(1, keepdim=True)
+    y = torch.where(none, torch.zeros_like(x), x)
+    s = (torch.sigmoid(y) if kind == "sigmoid" else torch.softmax(y, dim=1)) * ~none
+    p = s / (s.sum(1, keepdim=True) + 1e-20) if kind == "sigmoid" else s
     for q in range(S):
         a, b = offsets[q], offsets[q + 1]
         if a == b:

@@ -538,6 +538,15 @@ def test_rows(wt, T, K, E, align):
     run_rows(wt, e, E, align, 0)
 
 
+@pytest.mark.parametrize("T", [0, 3, 300])
+def test_many_more_rows_than_copies(wt, T):
+    # whole row tiles of many unused experts' neighbours, and a long array behind the last expert
+    g = torch.Generator().manual_seed(T)
+    e = torch.randint(0, 900, (T, 8), generator=g, dtype=torch.int32)
+    run_rows(wt, e, 900, 4096, 8 * T + min(900, 8 * T) * 4095)
+    run_rows(wt, e, 900, 1, 400001)
+
+
 def test_all_copies_to_one_expert(wt):
     run_rows(wt, torch.full((3000, 4), 17, dtype=torch.int32), 40, 128, 13000)
     run_rows(wt, torch.full((300, 4), -1, dtype=torch.int32), 40, 128, 100)

@@ -774,8 +774,11 @@ __global__ void __launch_bounds__(64 * kBackWaves) router_backward_kernel(Router
 #pragma unroll
       for (int j = 0; j < NJ; ++j) row[lane + 64 * j] = 0.0f;
       if (a.normalize) {
-        const float r = __builtin_amdgcn_rcpf(wave_sum(ss) + 1e-20f), ds = wave_sum(d * ss);
-        if (sel >= 0) d = (d - ds * r) * r;
+        // with z = sum + 1e-20, d_j - sum(d s) / z = c_j - sum(c s) / z + d_0 1e-20 / z for c = d - d_0: what all
+        // of a token's gradients share cancels before it is rounded (entirely, if one expert is selected)
+        const float r = __builtin_amdgcn_rcpf(wave_sum(ss) + 1e-20f), d0 = lane_value(d, 0), c = d - d0;
+        const float cs = wave_sum(c * ss);
+        if (sel >= 0) d = (c - cs * r + d0 * (1e-20f * r)) * r;
       }
       wave_lds_fence();
       if (sel >= 0) atomicAdd(&row[sel], d);

@@ -416,6 +416,36 @@ def test_gradient_in_place_and_foreign_indices(wt):
 
 
 @pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+def test_a_gradient_that_cancels(wt, kind):
+    # one selected expert with a normalized weight: the weight is 1 whatever the logits are, up to the 1e-20
+    c = Case(wt, logits(300, 70, seed=8), 1, kind, True)
+    c.check_forward()
+    dw = torch.randn(300, 1, device="cuda")
+    out = torch.full((300, 70), 5.0, device="cuda")
+    wt.wt_router_backward(c.d, c.index.data_ptr(), c.seq_counts.data_ptr(), dw.data_ptr(), 0, out.data_ptr(), 70)
+    torch.cuda.synchronize()
+    # |dweight| scale 1e-20 / score <= 5 * 2.5 * 1e-20 / (1 / 70), with room for the roundings
+    assert float(out.abs().max()) <= 1e-17
+    # gradients that are alike: the true one is what is left of their difference
+    c = Case(wt, logits(300, 70, seed=9), 6, kind, True)
+    c.check_forward()
+    dw = 1000.0 + torch.rand(300, 6, generator=torch.Generator().manual_seed(1))
+    out2 = torch.full((300, 70), 5.0, device="cuda")
+    dwd = dw.cuda()
+    wt.wt_router_backward(c.d, c.index.data_ptr(), c.seq_counts.data_ptr(), dwd.data_ptr(), 0, out2.data_ptr(), 70)
+    torch.cuda.synchronize()
+    x = c.x.double().requires_grad_()
+    v = R.value(x, c.index[:300].cpu().long(), c.seq_counts.cpu(), dw.double(), None, kind=kind, top_k=6,
+                normalize=True, scale=c.scale, offsets=c.offsets, coef=c.coef)
+    want = torch.autograd.grad(v, x)[0]
+    # d - d_0 is exact up to the rounding of d scale (1 in 2^24 of 2502); a difference of at most 2.5 over the mass m of
+    # the selected, with 64 roundings of the sums, scores and quotients; each times a score's slope, at most 1 / 4
+    m = c._least_mass(c.index[:300])
+    tol = (2 * EPS32 * 2502.5 + 64 * EPS32 * 2.5) / m / 4
+    assert float((out2.cpu().double() - want).abs().max()) <= tol
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
 def test_gradient_against_differences(wt, kind):
     # the formula's own gradient (float64 differences of the forward definition with the selection held)
     T, E, K = 6, 20, 3

@@ -6,14 +6,13 @@
 // its own. Counts come from integer histograms and lane masks, never from the
 // order of atomics. Up to kRowsSingle copies one workgroup places them all (one
 // launch); beyond, a first launch counts each tile and the second one's
-// workgroups each add up what they need of the (at most 64) tiles' counts (side
-// by side, where a scan kernel between the two took 12 us alone). Workgroups
-// behind the last tile take part in filling the rows that hold no copy; with one
-// tile each of them counts the copies for itself. Nothing here is bound by
-// bytes: 16384 tokens move 1.8 MB in 14 us, which go to two launches, five
-// barriers, and reads and scattered writes that wait for L2. Tiles of 1024,
-// 2048 and 4096 copies (at most 128, 64 and 64 of them): 1024 tokens 8.9 / 9.3
-// / 11.4 us, 8192 tokens 13.1 / 11.4 / 13.3, 16384 tokens 18.0 / 13.9 / 14.0.
+// workgroups each add up what they need of all tiles' counts (side by side, where
+// a scan kernel between the two took 12 us alone; four experts to a load, where
+// one to a load took 2.7 us more with 64 tiles). Workgroups behind the last tile
+// take part in filling the rows that hold no copy; with one tile each of them
+// counts the copies for itself. Nothing here is bound by bytes: 16384 tokens
+// move 1.8 MB in 10.4 us, which go to two launches (3 + 8 us), five barriers,
+// and reads and scattered writes that wait for L2.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -28,11 +27,16 @@ namespace wt {
 namespace {
 
 constexpr int kMaxExperts = 1024;
-constexpr int kMaxTiles = 64;
-constexpr int64_t kRowsTile = 2048;    // copies of one workgroup, more where there would be over 64 tiles
-// Copies up to which one workgroup takes them all. Measured on MI355X, 8 copies
-// of each token over 384 experts, one workgroup / two launches: 256 tokens 5.9 /
-// 8.1 us, 512 tokens 8.3 / 8.8, 1024 tokens 12.7 / 9.3.
+// Copies of a workgroup's tile: kRowsTile, half of it up to kRowsFew, more beyond
+// kMaxTiles tiles. Measured on MI355X, 8 copies of each token over 384 experts,
+// tiles of 1024 / 2048 / 4096 copies: 1024 tokens 8.3 / 8.9 / 11.1 us, 4096
+// tokens 9.2 / 9.3 / 11.5, 8192 tokens 10.3 / 9.9 / 11.7, 16384 tokens 11.7 /
+// 11.1 / 12.2; at most 64 / 128 / 256 tiles: 65536 tokens 17.9 / 14.1 / 15.1 us.
+constexpr int64_t kRowsTile = 2048;
+constexpr int64_t kRowsFew = 32768;
+constexpr int kMaxTiles = 128;
+// Copies up to which one workgroup takes them all; one workgroup / two launches:
+// 512 tokens 7.6 / 8.0 us, 1024 tokens 11.6 / 8.3.
 constexpr int64_t kRowsSingle = 4096;
 // Rows for which there is one workgroup to fill them. 128 tokens over 384 experts
 // in tiles of 128 rows, with one workgroup per 1024 / 4096 / 16384 rows 5.2 / 5.3
@@ -46,7 +50,7 @@ struct RowsArgs {
   int32_t top_k, n_experts, align;
   int64_t n_rows;
   int32_t *row_token, *pair_row, *offsets, *counts;
-  int32_t *tile_counts;  // [tile][expert]
+  int32_t *tile_counts;  // [tile][expert], 16-byte aligned rows
   int64_t tile;          // copies of a tile, a multiple of 64 times the workgroup's waves
   int32_t n_tiles;
 };
@@ -54,6 +58,12 @@ struct RowsArgs {
 // Waves of a workgroup: 16, or 8 beyond 512 experts (each wave has a histogram
 // of 4 bytes per expert); a thread then looks after one or two experts.
 constexpr int kManyExperts = 512;
+
+// Copies that a lane loads at once. 1 / 2 / 4 of them: 512 tokens 8.3 / 7.6 / 7.5
+// us, 128 tokens 4.8 / 4.8 / 5.0.
+constexpr int kAhead = 2;
+
+__host__ __device__ constexpr int counts_row(int n_experts) { return (n_experts + 3) / 4 * 4; }
 
 __device__ __forceinline__ int expert_at(const RowsArgs &a, int64_t i, int64_t end) {
   const int e = i < end ? a.index[i] : -1;
@@ -70,7 +80,7 @@ __global__ void __launch_bounds__(1024) rows_count_kernel(RowsArgs a) {
     if (e >= 0) atomicAdd(&lds[e], 1);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < a.n_experts; e += blockDim.x) a.tile_counts[blockIdx.x * a.n_experts + e] = lds[e];
+  for (int e = threadIdx.x; e < a.n_experts; e += blockDim.x) a.tile_counts[blockIdx.x * counts_row(a.n_experts) + e] = lds[e];
 }
 
 // Lanes of the wave with the same expert as this one.
@@ -99,24 +109,35 @@ __global__ void __launch_bounds__(64 * Waves) rows_place_kernel(RowsArgs a) {
   for (int e = threadIdx.x; e < (Waves + 2) * E; e += Threads) lds[e] = 0;
   __syncthreads();
 #pragma unroll 1
-  for (int64_t i = from + lane; i < to; i += 64) {
-    const int e = expert_at(a, i, to);
-    if (e >= 0) atomicAdd(&next[wave * E + e], 1);
+  for (int64_t base = from; base < to; base += 64 * kAhead) {
+    int e[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) e[j] = expert_at(a, base + 64 * j + lane, to);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (e[j] >= 0) atomicAdd(&next[wave * E + e[j]], 1);
   }
   if (!Single) {
-    // thread = (expert, every parts-th tile)
-    const int parts = max(1, Threads / E);
-    for (int at = threadIdx.x; at < parts * E; at += Threads) {
-      const int e = at % E;
-      int b = 0, t = 0;
-#pragma unroll 16
-      for (int k = at / E; k < a.n_tiles; k += parts) {
-        const int c = a.tile_counts[k * E + e];
-        b += k < (int)blockIdx.x ? c : 0;
-        t += c;
+    // thread = (four experts, every parts-th tile)
+    const int quads = counts_row(E) / 4, parts = Threads / quads, quad = threadIdx.x % quads;
+    if ((int)threadIdx.x < parts * quads) {
+      int b[4] = {0, 0, 0, 0}, t[4] = {0, 0, 0, 0};
+#pragma unroll 4
+      for (int k = threadIdx.x / quads; k < a.n_tiles; k += parts) {
+        const int4 c = *(const int4 *)(a.tile_counts + (int64_t)k * counts_row(E) + 4 * quad);
+        const int v[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          b[i] += k < (int)blockIdx.x ? v[i] : 0;
+          t[i] += v[i];
+        }
       }
-      atomicAdd(&before[e], b);
-      atomicAdd(&total[e], t);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (4 * quad + i < E) {
+          atomicAdd(&before[4 * quad + i], b[i]);
+          atomicAdd(&total[4 * quad + i], t[i]);
+        }
     }
   }
   __syncthreads();
@@ -170,21 +191,28 @@ __global__ void __launch_bounds__(64 * Waves) rows_place_kernel(RowsArgs a) {
   }
   __syncthreads();
 #pragma unroll 1
-  for (int64_t base = !Single || blockIdx.x == 0 ? from : to; base < to; base += 64) {
-    const int64_t i = base + lane;
-    const int e = expert_at(a, i, to);
-    const uint64_t same = same_expert(e);
-    int row = -1;
-    if (e >= 0) {
-      const int rank = __popcll(same & (((uint64_t)1 << lane) - 1));
-      row = next[wave * E + e] + rank;
-      wave_lds_fence();
-      if (rank == 0) next[wave * E + e] = row + __popcll(same);
-      wave_lds_fence();
-      if (row >= a.n_rows) row = -1;
-      else if (a.row_token) a.row_token[row] = (int32_t)((uint32_t)i / (uint32_t)a.top_k);
+  for (int64_t base = !Single || blockIdx.x == 0 ? from : to; base < to; base += 64 * kAhead) {
+    int expert[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) expert[j] = expert_at(a, base + 64 * j + lane, to);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (base + 64 * j >= to) break;
+      const int64_t i = base + 64 * j + lane;
+      const int e = expert[j];
+      const uint64_t same = same_expert(e);
+      int row = -1;
+      if (e >= 0) {
+        const int rank = __popcll(same & (((uint64_t)1 << lane) - 1));
+        row = next[wave * E + e] + rank;
+        wave_lds_fence();
+        if (rank == 0) next[wave * E + e] = row + __popcll(same);
+        wave_lds_fence();
+        if (row >= a.n_rows) row = -1;
+        else if (a.row_token) a.row_token[row] = (int32_t)((uint32_t)i / (uint32_t)a.top_k);
+      }
+      if (i < to && a.pair_row) a.pair_row[i] = row;
     }
-    if (i < to && a.pair_row) a.pair_row[i] = row;
   }
   if (!a.row_token) return;
   // rows that hold no copy: behind each expert's copies (a wave per expert), and behind the last expert
@@ -195,6 +223,12 @@ __global__ void __launch_bounds__(64 * Waves) rows_place_kernel(RowsArgs a) {
   for (int64_t r = (int64_t)start[E] + blockIdx.x * Threads + threadIdx.x; r < a.n_rows;
        r += (int64_t)gridDim.x * Threads)
     a.row_token[r] = -1;
+}
+
+// Copies of a tile.
+int64_t tile_of(int64_t pairs) {
+  if (pairs <= kRowsFew) return kRowsTile / 2;
+  return std::max(kRowsTile, (pairs + kMaxTiles - 1) / kMaxTiles);
 }
 
 wt_status fail(const char *what, const std::string &m, wt_status st = WT_E_INVAL) {
@@ -221,8 +255,8 @@ wt_status wt_dispatch_workspace_bytes(int64_t n_tokens, int32_t top_k, int32_t n
   const wt_status st = check_sizes(what, n_tokens, top_k, n_experts);
   if (st != WT_OK) return st;
   if (!bytes) return fail(what, "NULL result");
-  const int64_t tiles = (n_tokens * top_k + kRowsTile - 1) / kRowsTile;
-  *bytes = (size_t)(4 * n_experts * (tiles < 1 ? 1 : tiles > kMaxTiles ? kMaxTiles : tiles));
+  const int64_t pairs = n_tokens * top_k, tile = tile_of(pairs);
+  *bytes = (size_t)(4 * counts_row(n_experts) * ((pairs + tile - 1) / tile) + 16);
   return WT_OK;
 }
 
@@ -257,8 +291,8 @@ wt_status wt_dispatch_rows(const int32_t *index, int64_t n_tokens, int32_t top_k
     a.pair_row = pair_row;
     a.offsets = offsets;
     a.counts = counts;
-    a.tile_counts = (int32_t *)workspace;
-    a.tile = single ? pairs : pairs <= kRowsTile * kMaxTiles ? kRowsTile : (pairs + kMaxTiles - 1) / kMaxTiles;
+    a.tile_counts = (int32_t *)(((uintptr_t)workspace + 15) / 16 * 16);
+    a.tile = single ? pairs : tile_of(pairs);
     a.tile = (a.tile + unit - 1) / unit * unit;
     if (a.tile == 0) a.tile = unit;
     a.n_tiles = (int32_t)((pairs + a.tile - 1) / a.tile);

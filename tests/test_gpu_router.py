@@ -577,6 +577,25 @@ def test_many_more_rows_than_copies(wt, T):
     run_rows(wt, e, 900, 1, 400001)
 
 
+@pytest.mark.parametrize("T,E", [(3000, 381), (40000, 6)])
+def test_rows_with_a_workspace_at_any_word(wt, T, E):
+    g = torch.Generator().manual_seed(T)
+    idx = torch.randint(0, E, (T, 4), generator=g, dtype=torch.int32)
+    want = R.rows(idx.numpy(), E, 32, 4 * T + 31 * E)
+    dev = idx.cuda()
+    size = wt.wt_dispatch_workspace_bytes(T, 4, E)
+    for word in range(4):
+        ws = torch.full((size + 64,), 0xA5, dtype=torch.uint8, device="cuda")
+        tok, pair, off, cnt = (torch.full(s, -77, dtype=torch.int32, device="cuda")
+                               for s in ((4 * T + 31 * E,), (T, 4), (E + 1,), (E,)))
+        wt.wt_dispatch_rows(dev.data_ptr(), T, 4, E, 32, tok.numel(), tok.data_ptr(), pair.data_ptr(), off.data_ptr(),
+                            cnt.data_ptr(), ws.data_ptr() + 4 * word, size)
+        torch.cuda.synchronize()
+        assert bool((ws[4 * word + size:] == 0xA5).all()) and bool((ws[:4 * word] == 0xA5).all())
+        for got, w in zip((tok, pair, off, cnt), want):
+            assert np.array_equal(got.cpu().numpy(), w)
+
+
 def test_all_copies_to_one_expert(wt):
     run_rows(wt, torch.full((3000, 4), 17, dtype=torch.int32), 40, 128, 13000)
     run_rows(wt, torch.full((300, 4), -1, dtype=torch.int32), 40, 128, 100)

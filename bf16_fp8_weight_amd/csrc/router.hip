@@ -629,8 +629,8 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Both reductions in one workgroup, for few partial sums (a second launch
-// would cost more than the reads one after the other).
+// Both reductions of one sequence in one workgroup, for few partial sums (a
+// second launch would cost more than the reads one after the other).
 constexpr int kSmallThreads = 1024;
 __global__ void __launch_bounds__(kSmallThreads)
     router_small_kernel(RouterArgs a, const float *part_p, const int32_t *part_c, int32_t *seq_counts,
@@ -638,37 +638,32 @@ __global__ void __launch_bounds__(kSmallThreads)
   __shared__ double sp[kSmallThreads];
   __shared__ int sc[kSmallThreads];
   const int E = a.n_experts, rows = kSmallThreads / E, e = threadIdx.x % E, row = threadIdx.x / E;
-  double total = 0.0;
-  int all = 0;
-  for (int32_t q = 0; q < a.n_seqs; ++q) {
-    const int32_t lo = seq_start(a, q), hi = seq_start(a, q + 1);
-    double p = 0.0;
-    int c = 0;
-    if (hi > lo && row < rows) {
-      const int32_t last = (hi - 1) / a.tile;
+  const int32_t lo = seq_start(a, 0), hi = seq_start(a, 1);
+  double p = 0.0, total = 0.0;
+  int c = 0;
+  if (hi > lo && row < rows) {
+    const int32_t last = (hi - 1) / a.tile;
 #pragma unroll 4
-      for (int32_t i = lo / a.tile + row; i <= last; i += rows) {
-        const int64_t at = ((int64_t)i + q) * E + e;
-        p += (double)part_p[at];
-        c += part_c[at];
-      }
+    for (int32_t i = lo / a.tile + row; i <= last; i += rows) {
+      const int64_t at = (int64_t)i * E + e;
+      p += (double)part_p[at];
+      c += part_c[at];
     }
-    sp[threadIdx.x] = p;
-    sc[threadIdx.x] = c;
-    __syncthreads();
-    if (row == 0) {
-      for (int i = 1; i < rows; ++i) {
-        p += sp[i * E + e];
-        c += sc[i * E + e];
-      }
-      seq_counts[(int64_t)q * E + e] = c;
-      all += c;
-      const double n = hi > lo ? (double)(hi - lo) : 1.0;
-      total += (double)c * p / (n * n);
-    }
-    __syncthreads();
   }
-  if (row == 0 && counts) counts[e] = all;
+  sp[threadIdx.x] = p;
+  sc[threadIdx.x] = c;
+  __syncthreads();
+  if (row == 0) {
+    for (int i = 1; i < rows; ++i) {
+      p += sp[i * E + e];
+      c += sc[i * E + e];
+    }
+    seq_counts[e] = c;
+    if (counts) counts[e] = c;
+    const double n = hi > lo ? (double)(hi - lo) : 1.0;
+    total = (double)c * p / (n * n);
+  }
+  __syncthreads();
   for (int d = 32; d; d >>= 1) total += __shfl_xor(total, d);
   if ((threadIdx.x & 63) == 0) sp[threadIdx.x >> 6] = total;
   __syncthreads();
@@ -808,17 +803,22 @@ __global__ void __launch_bounds__(64 * kBackWaves) router_backward_kernel(Router
 // the card with fewer tokens. Measured on MI355X, forward with 4, 8 and 16
 // waves to a workgroup and 1, 2, 4 tokens to a wave: 16384 x 384 31.3 / 26.6 /
 // 24.4, 30.7 / 25.9 / 23.3 and - / 26.6 / 24.2 us, 5003 x 160 17.5 / 15.5 /
-// 16.5, 14.8 / 14.3 / 20.5 and 15.6 / - / 21.2 us; backward (4 waves) of the
+// 16.5, 14.8 / 14.3 / 20.5 and 15.6 / - / 21.2 us; few tokens with 1 and 2 to
+// each of 8 waves: 64 x 384 8.8 / 10.4 us, 128 x 384 9.3 / 10.6, 512 x 384 9.5 /
+// 11.5, 2048 x 160 11.6 / 12.9, 4096 x 384 15.4 / 14.8, 8192 x 384 21.8 / 17.8; backward (4 waves) of the
 // first 14.6 / 12.5 / 11.8 us, of the second 7.6 / 7.6 / 7.6 us.
-int32_t tile_of(int64_t n_tokens) { return n_tokens <= 8192 ? 16 : n_tokens <= 32768 ? 32 : 64; }
+int32_t tile_of(int64_t n_tokens) {
+  return n_tokens <= 2048 ? 8 : n_tokens <= 8192 ? 16 : n_tokens <= 32768 ? 32 : 64;
+}
 int32_t back_tile_of(int64_t n_tokens) { return n_tokens <= 8192 ? 4 : 16; }
 
-// Partial sums up to which one workgroup reduces them. Measured on MI355X, the
-// whole forward pass of 384 experts with one workgroup / with two launches:
-// 128 tokens (3,456 sums) 10.3 / 10.8 us, 512 tokens (12,672) 11.9 / 11.3 us,
-// 1024 tokens 16.1 / 14.2 us.
+// Partial sums of one sequence up to which one workgroup reduces them. Measured
+// on MI355X, the whole forward pass of 384 experts with one workgroup / with two
+// launches: 1 token 7.5 / 8.9 us, 64 tokens (3,456 sums) 8.7 / 9.4, 192 tokens
+// (9,600) 9.7 / 9.8, 256 tokens (12,672) 10.1 / 9.7. With several sequences, one
+// after the other in that workgroup: 128 tokens in 2 of them 10.1 / 9.4 us, in 8
+// (160 experts) 15.1 / 8.5.
 constexpr int64_t kSmallSums = 8192;
-constexpr int32_t kSmallSeqs = 8;
 
 int chunks_of(int n_experts) { return (n_experts + kChunk - 1) / kChunk; }
 
@@ -956,7 +956,7 @@ wt_status wt_router_forward(const wt_router_desc *desc, int32_t *index, float *w
         hipLaunchKernelGGL(kernel, dim3(tiles), dim3(64 * kWaves), 0, s, a,
                            ForwardOut{index, weight, part_p, part_c});
       });
-    if (a.n_seqs <= kSmallSeqs && w.rows * a.n_experts <= kSmallSums) {
+    if (a.n_seqs == 1 && w.rows * a.n_experts <= kSmallSums) {
       hipLaunchKernelGGL(router_small_kernel, dim3(1), dim3(kSmallThreads), 0, s, a, part_p, part_c, seq_counts, counts,
                          loss);
     } else {

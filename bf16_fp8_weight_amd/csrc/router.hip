@@ -180,6 +180,8 @@ __device__ __forceinline__ Norm scores(const float x[NJ], float s[NJ]) {
 
 __device__ __forceinline__ bool selectable(float x) { return x > -INFINITY; }  // false for NaN
 
+constexpr float kLowest = -0x1.fffffep+127f;  // no selectable key is below it
+
 // exp in 64 bits with few registers: x = n ln 2 + r, the series of r by
 // Horner's rule from a table of 1 / k in scalar memory (|r| < 0.35: fourteen
 // terms leave 1e-19), in a loop because it runs for few tokens and must not
@@ -382,7 +384,7 @@ __device__ __forceinline__ void select_topk(const RouterArgs &a, int64_t t, cons
     step >>= 1;
   }
   const bool all = lo == 1u;  // every selectable expert is a candidate
-  const float least = all ? -0x1.fffffep+127f : from_ordered(lo);
+  const float least = all ? kLowest : from_ordered(lo);
   uint64_t who[NJ];
   int count = 0;
 #pragma unroll
@@ -435,10 +437,11 @@ __device__ __forceinline__ void select_topk(const RouterArgs &a, int64_t t, cons
         const int border = a.top_k - 1 + __builtin_ctzll(~(same >> (a.top_k - 1)));  // first unlike pair from there on
         const bool open = border + 1 < count ? (close >> border) & 1 : count > a.top_k && !all;
         decided = !open && !(close & ~same & ((1ull << (a.top_k - 1)) - 1));
-        // everything within reach of the last place
+        // everything within reach of the last place. The difference may pass the lowest fp32 value: experts that are
+        // switched off, and columns behind the last expert, have the key -infinity and must not come within reach.
         if (count > a.top_k) {
           const float last = lane_value(k0, a.top_k - 1);
-          reach = fminf(least, last - near_tie<Softmax>(last, Softmax ? 1.0f : 0.0f));
+          reach = fmaxf(fminf(least, last - near_tie<Softmax>(last, Softmax ? 1.0f : 0.0f)), kLowest);
         }
       }
     }

@@ -382,6 +382,25 @@ def test_masks_of_the_lowest_value_and_endless_biases(wt, kind, dtype, with_bias
     c.check_backward(dweight=False)
 
 
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,K", [(20, 4), (40, 8), (63, 8), (63, 32), (64, 8), (200, 8)])
+@pytest.mark.parametrize("live", [0, 2, 3])
+def test_biases_of_the_lowest_value(wt, kind, dtype, E, K, live):
+    # a step below the lowest fp32 value is -infinity, the key of experts that are switched off and of the columns
+    # behind the last one: none of them is selected, whatever lies behind the rows and behind the bias
+    x = logits(9, E, dtype, seed=E)
+    x[3, 5] = -math.inf
+    b = torch.full((E,), torch.finfo(torch.float32).min)
+    b[torch.randperm(E, generator=torch.Generator().manual_seed(E))[:live]] = 0.0
+    c = Case(wt, x, K, kind, True, bias=b, pad=64)  # sevens behind each row
+    wide = torch.full((E + 64,), 100.0, device="cuda")
+    wide[:E] = c.bias
+    c.d.bias = wide.data_ptr()
+    c.check_forward()
+    c.check_backward()
+
+
 def test_offsets_that_make_no_sense_stay_inside_the_arrays(wt):
     # falling, negative and too large offsets: the results mean nothing, the guards stay whole
     for offsets in ([50, 10, 90, 0], [-5, 1 << 30], [100, 0], [7, -7, 7, -7, 7], [2 ** 31 - 1, -(2 ** 31)]):

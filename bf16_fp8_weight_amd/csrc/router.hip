@@ -383,7 +383,9 @@ __device__ __forceinline__ void select_topk(const RouterArgs &a, int64_t t, cons
     lo += __popcll(__ballot(u >= lo + step)) >= need ? step : 0u;
     step >>= 1;
   }
-  const bool all = lo == 1u;  // every selectable expert is a candidate
+  // numbers up to that of the lowest fp32 value are none of a key (below it lie -infinity and NaNs, which no comparison
+  // reaches): every selectable expert is a candidate
+  const bool all = lo <= 0x00800000u;
   const float least = all ? kLowest : from_ordered(lo);
   uint64_t who[NJ];
   int count = 0;

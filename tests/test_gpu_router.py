@@ -401,6 +401,30 @@ def test_biases_of_the_lowest_value(wt, kind, dtype, E, K, live):
     c.check_backward()
 
 
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,K", [(2, 1), (3, 2), (8, 2), (8, 7), (16, 8), (17, 8), (33, 32), (70, 6)])
+@pytest.mark.parametrize("where", ["logits", "bias", "both"])
+def test_few_experts_masked_by_the_lowest_value(wt, kind, E, K, where):
+    # the lowest finite value is a key like any other: the ordinary experts first, then the masked ones by their index
+    T, low = 40, torch.finfo(torch.float32).min
+    g = torch.Generator().manual_seed(E)
+    x = logits(T, E, seed=E)
+    b = None if where == "logits" else bias(E)
+    for t in range(T):  # none to K experts left, or all of them
+        off = torch.randperm(E, generator=g)[(t % (K + 1)):]
+        if where != "bias" and t % (K + 2) <= K:
+            x[t, off] = low
+    if where != "logits":
+        b[torch.randperm(E, generator=g)[K // 2:]] = low
+    c = Case(wt, x, K, kind, True, bias=b)
+    index, _ = c.check_forward()
+    assert (index >= 0).all()
+    # one step above it, and half of it
+    for other in (float(np.nextafter(np.float32(low), np.float32(0))), low / 2):
+        y = torch.where(x == low, other, x)
+        Case(wt, y, K, kind, False, bias=None if b is None else torch.where(b == low, other, b)).check_forward()
+
+
 def test_offsets_that_make_no_sense_stay_inside_the_arrays(wt):
     # falling, negative and too large offsets: the results mean nothing, the guards stay whole
     for offsets in ([50, 10, 90, 0], [-5, 1 << 30], [100, 0], [7, -7, 7, -7, 7], [2 ** 31 - 1, -(2 ** 31)]):

@@ -768,6 +768,12 @@ __global__ void __launch_bounds__(64 * kBackWaves) router_backward_kernel(Router
       continue;
     }
     const Norm n = scores<NJ, Softmax>(x, s);
+    if (!Softmax) {
+      // x becomes the sigmoid's slope s (1 - s). 1 - s is exp(-x) s: a difference would have no digits left for a
+      // confident expert, whose 1 - s is small. An exponential that is infinite meets a score of 0.
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) x[j] = s[j] * (s[j] * fminf(fast_exp(-x[j]), 0x1.fffffep+127f));
+    }
 #pragma unroll
     for (int j = 0; j < NJ; ++j) g[j] = 0.0f;
     if (o.dweight) {
@@ -799,7 +805,7 @@ __global__ void __launch_bounds__(64 * kBackWaves) router_backward_kernel(Router
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
       g[j] = Softmax ? s[j] * (b[j] + g[j] - dot)
-                       : ((b[j] - dot * n.inv) * n.inv + g[j]) * s[j] * (1.0f - s[j]);
+                       : ((b[j] - dot * n.inv) * n.inv + g[j]) * x[j];
     store_row<NJ>(a, o, t, lane, g);
   }
 }

@@ -488,6 +488,41 @@ def test_a_gradient_that_cancels(wt, kind):
     assert float((out2.cpu().double() - want).abs().max()) <= tol
 
 
+@pytest.mark.parametrize("E", [20, 100])
+def test_slope_of_confident_scores(wt, E):
+    # sigmoid scores next to 1 and next to 0: s (1 - s) has all its digits, whichever of the two is small
+    T, K = 50, 6
+    g = torch.Generator().manual_seed(E)
+    x = (torch.rand(T, E, generator=g) * 40.0 - 20.0)
+    x[:5] = 8.0 + 12.0 * torch.rand(5, E, generator=g)
+    c = Case(wt, x, K, "sigmoid", False, bias=bias(E), offsets=[0, 20, T], coef=2.0)
+    index, _ = c.check_forward()
+    dw = torch.rand(T, K, generator=g) + 0.5
+    dl, out = torch.tensor([0.7], device="cuda"), torch.full((T, E), 9.0, device="cuda")
+    dwd = dw.cuda()
+    idx = torch.from_numpy(index).long()
+    y = x.double()
+    s, slope = torch.sigmoid(y), torch.sigmoid(y) * torch.sigmoid(-y)
+    # y = exp(-x): the argument's product and factor are rounded (|x| 2 EPS32 of y together), then the exponential (2);
+    # y / (1 + y)^2 moves by at most as much as y; sum, reciprocal (2), twice, and three products: 2 |x| + 16 with dw's
+    rel = (2.0 * y.abs() + 16.0) * EPS32
+    wt.wt_router_backward(c.d, c.index.data_ptr(), c.seq_counts.data_ptr(), dwd.data_ptr(), 0, out.data_ptr(), E)
+    torch.cuda.synchronize()
+    want = torch.zeros(T, E, dtype=torch.float64).scatter_(1, idx, dw.double() * c.scale) * slope
+    bad = (out.cpu().double() - want).abs() > rel * want
+    assert not bad.any(), (out.cpu()[bad][:4], want[bad][:4], x[bad][:4])
+    # of the loss: b - sum(b s) / z, with errors of the greatest b (7 roundings of its own, and of the quotient of two
+    # sums over experts: 7 of the scores and 8 of the sum each, 3 beside them), times 1 / z (18) and the slope (12)
+    wt.wt_router_backward(c.d, c.index.data_ptr(), c.seq_counts.data_ptr(), 0, dl.data_ptr(), out.data_ptr(), E)
+    torch.cuda.synchronize()
+    z = s.sum(1, keepdim=True)
+    for a, b, q in ((0, 20, 0), (20, T, 1)):
+        d = float(dl) * c.coef / 2 * E / (K * (b - a)) / (b - a) * c.seq_counts[q].cpu().double()
+        want = (d - (d * s[a:b]).sum(1, keepdim=True) / z[a:b]) / z[a:b] * slope[a:b]
+        tol = (72.0 + 2.0 * y[a:b].abs()) * EPS32 * d.max() / z[a:b] * slope[a:b]
+        assert bool(((out[a:b].cpu().double() - want).abs() <= tol).all())
+
+
 @pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
 def test_gradient_against_differences(wt, kind):
     # the formula's own gradient (float64 differences of the forward definition with the selection held)

@@ -488,6 +488,47 @@ def test_a_gradient_that_cancels(wt, kind):
     assert float((out2.cpu().double() - want).abs().max()) <= tol
 
 
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E", [9, 64, 65, 129, 193, 257, 384, 385, 513, 1024])  # every number of columns
+def test_gradient_of_the_balance_loss(wt, kind, dtype, E):
+    # alone, and beside weights' gradients of its own size, with a tolerance relative to what it is made of
+    T, K, offsets = 37, 8, [0, 11, 35]
+    c = Case(wt, logits(T, E, dtype, seed=E), K, kind, False, scale=1.0, offsets=offsets, coef=1.0)
+    index, _ = c.check_forward()
+    x = c.x.double()
+    s = torch.sigmoid(x) if kind == "sigmoid" else torch.softmax(x, 1)
+    z = s.sum(1, keepdim=True)
+    d = torch.zeros(T, E, dtype=torch.float64)  # of the loss by each probability
+    for q, (a, b) in enumerate(zip(offsets, offsets[1:])):
+        d[a:b] = 0.7 / 2 * E / (K * (b - a)) / (b - a) * c.seq_counts[q].cpu().double()
+    idx = torch.from_numpy(index).long()
+    dw = torch.randn(T, K, generator=torch.Generator().manual_seed(E)) * float((d[:35] / z[:35]).mean())
+    dl, out = torch.tensor([0.7], device="cuda"), torch.full((T, E), 9.0, dtype=dtype, device="cuda")
+    dwd = dw.cuda()
+    for both in (False, True):
+        wt.wt_router_backward(c.d, c.index.data_ptr(), c.seq_counts.data_ptr(), dwd.data_ptr() if both else 0,
+                              dl.data_ptr(), out.data_ptr(), E)
+        torch.cuda.synchronize()
+        g = torch.zeros(T, E, dtype=torch.float64)
+        if both:
+            g[:35].scatter_(1, idx[:35], dw[:35].double())
+        if kind == "sigmoid":
+            want = ((d - (d * s).sum(1, keepdim=True) / z) / z + g) * s * torch.sigmoid(-x)
+            # d: 7 roundings; a score 7, a sum over the experts 16 + 6, the quotient of two such sums 61, a difference
+            # 1, the reciprocal of a sum 32, the slope 12 + 2 |x| with |x| below 6: 125
+            part = (d.amax(1, keepdim=True) / z + g.abs()) * s * torch.sigmoid(-x)
+        else:
+            want = s * (d + g - ((d + g) * s).sum(1, keepdim=True))
+            # a score: argument and exponential 18, sum 22, reciprocal and product 3; the mean of d + g by the scores
+            # 7 + 1 + 43 + 1 + 22 of their greatest, differences 2, the score again and products 45: 121
+            part = s * (d + g.abs()).amax(1, keepdim=True)
+        tol = 128 * EPS32 * part + (2.0 ** -8 * want.abs() if dtype == torch.bfloat16 else 0.0)
+        err = (out.cpu().double() - want).abs()
+        assert bool((err <= tol).all()), float((err / tol.clamp(min=1e-30)).max())
+        assert float(want[:35].abs().max()) > 100 * float((128 * EPS32 * part).max()) and not out[35:].any()
+
+
 @pytest.mark.parametrize("E", [20, 100])
 def test_slope_of_confident_scores(wt, E):
     # sigmoid scores next to 1 and next to 0: s (1 - s) has all its digits, whichever of the two is small

@@ -439,9 +439,9 @@ __global__ void __launch_bounds__(adam_item(Bits) / 8) adamw_update_kernel(AdamA
 
 // ------------------------------------------------------------ norm
 template <int Item, bool Full>
-__device__ __forceinline__ float item_squares(const AdamGradItem &t) {
+__device__ __forceinline__ double item_squares(const AdamGradItem &t) {
   const bool vec = t.flags & kAdamVector, gbf = t.flags & kAdamGradBf16;
-  float sum = 0.0f;
+  double sum = 0.0;
 #pragma unroll
   for (int c = 0; c < Item / (4 * kThreads); ++c) {
     const int64_t i = 4 * (c * kThreads + (int)threadIdx.x), left = (int64_t)t.count - i;
@@ -449,7 +449,7 @@ __device__ __forceinline__ float item_squares(const AdamGradItem &t) {
     if (gbf) load_bf16<Full>(t.grad, i, left, vec, g);
     else load_f32<Full>(t.grad, i, left, vec, g);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sum = fmaf(g[e], g[e], sum);
+    for (int e = 0; e < 4; ++e) sum += (double)(g[e] * g[e]);
   }
   return sum;
 }
@@ -463,8 +463,9 @@ __device__ __forceinline__ double block_sum(double x, double *lds) {
   return (lds[0] + lds[1]) + (lds[2] + lds[3]);
 }
 
-// Sum of the squares of every gradient, per workgroup: fp32 over a thread's
-// elements of an item, fp64 beyond.
+// Sum of the squares of every gradient, per workgroup: each square in fp32, all
+// sums in fp64 (fp32 sums of a thread's 8 or 16 squares would be infinite from
+// gradients of 4.6e18 on, where a square is up to 1.8e19).
 template <int Item>
 __global__ void __launch_bounds__(kThreads)
     adamw_norm_kernel(const AdamGradItem *items, uint32_t n_items, double *partials) {
@@ -475,7 +476,7 @@ __global__ void __launch_bounds__(kThreads)
     const AdamGradItem t = next;
     if (k + gridDim.x < n_items) next = ld_table(items, k + gridDim.x);
     const bool full = (t.flags & kAdamVector) && t.count == Item;
-    sum += (double)(full ? item_squares<Item, true>(t) : item_squares<Item, false>(t));
+    sum += full ? item_squares<Item, true>(t) : item_squares<Item, false>(t);
   }
   sum = block_sum(sum, lds);
   if (threadIdx.x == 0) partials[blockIdx.x] = sum;

@@ -238,6 +238,24 @@ def test_norm_alone_and_over_many_items(wt):
         assert float(norm) == 0.0
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("grad", ["fp32", "bf16"])
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("value", [1e-18, 3e18, 4.7e18, 6.6e18, 1.8e19])
+def test_norm_up_to_the_greatest_square(wt, bits, grad, shift, value):
+    # every gradient as large as a square allows: only each square, not a sum of them, has to fit fp32
+    norm = torch.zeros(1, device="cuda")
+    ts = [Tensor(n, bits, grad, True, True, shift, seed=n) for n in (5000, 37)]
+    for t in ts:
+        t.set("grad", torch.where(torch.arange(t.n) % 3 == 1, -value, value).to(t.dtype["grad"]))
+    h = hyper(wt, max_norm=1.0, norm_out=norm.data_ptr(), grad_scale=0.5)
+    before, after = run(wt, ts, h, bits)
+    want = exact_norm(ts, before, 0.5)
+    # a square rounded once, halved by the root, and the norm rounded once
+    assert abs(float(norm) - want) <= 2 * R.EPS32 * want
+    check_all(ts, before, after, h, min(1.0, 1.0 / (want + 1e-6)))
+
+
 @pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
 @pytest.mark.parametrize("bits", [32, 8])
 def test_gradients_that_are_not_finite(wt, bits, value):

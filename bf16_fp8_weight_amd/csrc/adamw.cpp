@@ -213,12 +213,8 @@ wt_status wt_adamw_check(const wt_adamw_tensor *tensors, size_t n_tensors, const
     }
     if (info) *info = L.info;
     return WT_OK;
-  } catch (const std::bad_alloc &) {
-    set_thread_error("host allocation failed");
-    return WT_E_NOMEM;
   } catch (...) {
-    set_thread_error("internal error");
-    return WT_E_INVAL;
+    return caught_status();
   }
 }
 

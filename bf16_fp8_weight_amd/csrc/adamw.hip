@@ -653,12 +653,8 @@ wt_status wt_adamw_create(const wt_adamw_tensor *tensors, size_t n_tensors, cons
   try {
     a = new wt_adamw();
     st = create_impl(tensors, n_tensors, resolve_adamw_opts(opts), a);
-  } catch (const std::bad_alloc &) {
-    set_thread_error("host allocation failed");
-    st = WT_E_NOMEM;
   } catch (...) {
-    set_thread_error("internal error");
-    st = WT_E_INVAL;
+    st = caught_status();
   }
   if (st == WT_OK)
     *out = a;
@@ -678,8 +674,7 @@ wt_status wt_adamw_step(wt_adamw *adamw, const wt_adamw_hyper *hyper, void *stre
   try {
     st = step_impl(adamw, hyper, (hipStream_t)stream);
   } catch (...) {
-    set_thread_error("internal error");
-    st = WT_E_INVAL;
+    st = caught_status();
   }
   adamw->busy.store(false);
   return st;

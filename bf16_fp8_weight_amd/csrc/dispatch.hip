@@ -252,12 +252,16 @@ extern "C" {
 
 wt_status wt_dispatch_workspace_bytes(int64_t n_tokens, int32_t top_k, int32_t n_experts, size_t *bytes) {
   const char *what = "wt_dispatch_workspace_bytes";
-  const wt_status st = check_sizes(what, n_tokens, top_k, n_experts);
-  if (st != WT_OK) return st;
-  if (!bytes) return fail(what, "NULL result");
-  const int64_t pairs = n_tokens * top_k, tile = tile_of(pairs);
-  *bytes = (size_t)(4 * counts_row(n_experts) * ((pairs + tile - 1) / tile) + 16);
-  return WT_OK;
+  try {
+    const wt_status st = check_sizes(what, n_tokens, top_k, n_experts);
+    if (st != WT_OK) return st;
+    if (!bytes) return fail(what, "NULL result");
+    const int64_t pairs = n_tokens * top_k, tile = tile_of(pairs);
+    *bytes = (size_t)(4 * counts_row(n_experts) * ((pairs + tile - 1) / tile) + 16);
+    return WT_OK;
+  } catch (...) {
+    return caught_status();
+  }
 }
 
 wt_status wt_dispatch_rows(const int32_t *index, int64_t n_tokens, int32_t top_k, int32_t n_experts,
@@ -310,8 +314,7 @@ wt_status wt_dispatch_rows(const int32_t *index, int64_t n_tokens, int32_t top_k
     if (e != hipSuccess) return fail(what, hip_msg("launch", e), WT_E_HIP);
     return WT_OK;
   } catch (...) {
-    set_thread_error("internal error");
-    return WT_E_INVAL;
+    return caught_status();
   }
 }
 

@@ -21,6 +21,26 @@ thread_local std::string g_last_error;
 
 void set_thread_error(const std::string &msg) { g_last_error = msg; }
 
+void set_thread_error(const char *msg) noexcept {
+  try {
+    g_last_error = msg;
+  } catch (...) {
+    g_last_error = "out of memory";  // fits a string without an allocation
+  }
+}
+
+wt_status caught_status() noexcept {
+  try {
+    throw;
+  } catch (const std::bad_alloc &) {
+    set_thread_error("host allocation failed");
+    return WT_E_NOMEM;
+  } catch (...) {
+    set_thread_error("internal error");
+    return WT_E_INVAL;
+  }
+}
+
 wt_plan_options resolve_opts(const wt_plan_options *o) {
   wt_plan_options d;
   wt_plan_options_init(&d);

@@ -112,6 +112,11 @@ void schedule_ops(const Layout &L, std::vector<wt_sched_op> *ops);
 wt_plan_options resolve_opts(const wt_plan_options *o);
 // The calling thread's last error text (host_api.cpp).
 void set_thread_error(const std::string &msg);
+void set_thread_error(const char *msg) noexcept;
+
+// In a handler of a C entry: the status of the exception in flight, its text
+// left as the thread's error.
+wt_status caught_status() noexcept;
 // Text of the last error recorded on a plan (runtime.cpp).
 const char *plan_error_text(const wt_plan *plan);
 

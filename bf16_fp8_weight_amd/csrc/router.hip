@@ -931,11 +931,15 @@ void wt_router_desc_init(wt_router_desc *desc) {
 
 wt_status wt_router_workspace_bytes(const wt_router_desc *desc, size_t *bytes) {
   const char *what = "wt_router_workspace_bytes";
-  const wt_status st = check_desc(what, desc);
-  if (st != WT_OK) return st;
-  if (!bytes) return fail(what, "NULL result");
-  *bytes = (size_t)workspace_of(*desc).bytes;
-  return WT_OK;
+  try {
+    const wt_status st = check_desc(what, desc);
+    if (st != WT_OK) return st;
+    if (!bytes) return fail(what, "NULL result");
+    *bytes = (size_t)workspace_of(*desc).bytes;
+    return WT_OK;
+  } catch (...) {
+    return caught_status();
+  }
 }
 
 wt_status wt_router_forward(const wt_router_desc *desc, int32_t *index, float *weight, int32_t *counts,
@@ -980,8 +984,7 @@ wt_status wt_router_forward(const wt_router_desc *desc, int32_t *index, float *w
     if (e != hipSuccess) return fail(what, hip_msg("launch", e), WT_E_HIP);
     return WT_OK;
   } catch (...) {
-    set_thread_error("internal error");
-    return WT_E_INVAL;
+    return caught_status();
   }
 }
 
@@ -1018,8 +1021,7 @@ wt_status wt_router_backward(const wt_router_desc *desc, const int32_t *index, c
     if (e != hipSuccess) return fail(what, hip_msg("launch", e), WT_E_HIP);
     return WT_OK;
   } catch (...) {
-    set_thread_error("internal error");
-    return WT_E_INVAL;
+    return caught_status();
   }
 }
 

@@ -459,6 +459,34 @@ def test_gradient_in_place_and_foreign_indices(wt):
 
 
 @pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+def test_an_expert_in_several_places_adds_up_in_their_order(wt, kind):
+    # sums that depend on their order in fp32: bit for bit those of the places from the first to the last
+    T, E, K = 64, 150, 8
+    g = torch.Generator().manual_seed(5)
+    c = Case(wt, logits(T, E, seed=14), K, kind, False, scale=1.0)
+    index = torch.stack([torch.randperm(E, generator=g)[:K] for _ in range(T)]).to(torch.int32)
+    dw = torch.randn(T, K, generator=g) * torch.exp(6.0 * torch.randn(T, K, generator=g))
+    one, sums = index.clone(), dw.clone()
+    for t in range(T):
+        places = sorted(torch.randperm(K, generator=g)[:2 + t % (K - 1)].tolist())
+        total = np.float32(0)
+        for k in places:
+            total = np.float32(total + np.float32(dw[t, k]))
+            index[t, k] = int(index[t, places[0]])
+            one[t, k] = -1
+        one[t, places[0]] = index[t, places[0]]
+        sums[t, places[0]] = float(total)
+    outs = []
+    for i, w in ((index, dw), (one, sums)):
+        out = torch.full((T, E), 9.0, device="cuda")
+        i, w = i.cuda(), w.cuda()
+        wt.wt_router_backward(c.d, i.data_ptr(), 0, w.data_ptr(), 0, out.data_ptr(), E)
+        torch.cuda.synchronize()
+        outs.append(out)
+    assert torch.equal(outs[0], outs[1])
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
 def test_a_gradient_that_cancels(wt, kind):
     # one selected expert with a normalized weight: the weight is 1 whatever the logits are, up to the 1e-20
     c = Case(wt, logits(300, 70, seed=8), 1, kind, True)

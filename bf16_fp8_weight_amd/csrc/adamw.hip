@@ -428,6 +428,9 @@ __global__ void __launch_bounds__(adam_item(Bits) / 8) adamw_update_kernel(AdamA
     gs *= a.norm->clip;
   }
   AdamScalars s = a.s;
+  // two powers, a root and two quotients in fp64 in every thread, replayed from a graph: 96 vectors of 896 elements 4.6
+  // -> 5.6 us (32-bit states) and 5.5 -> 6.4 us (8-bit), 17 M elements 56.8 -> 57.9 and 34.9 -> 36.1 us; nothing that
+  // shows over 176 M
   if (a.step_dev || a.lr_dev)
     s = step_scalars(a.lr_dev ? (double)*a.lr_dev : a.lr, a.beta1, a.beta2, a.eps, a.step_dev ? *a.step_dev : a.step,
                      a.seed);

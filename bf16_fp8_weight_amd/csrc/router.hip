@@ -3,12 +3,12 @@
 //
 // Forward: one pass over the logits leaves selections, weights and, per tile
 // of tokens and sequence, sums of probabilities and counts; one or two small
-// launches reduce those. Bound by instructions: 16384 tokens x 384 experts are
-// 26 MB, 5.6 us at the card's copy rate, and take 17.5 us (250 vector and 200
-// scalar instructions a token, the waves half of the time waiting for one
-// another's results), 22.6 us with the reductions. Backward: one pass
-// that reads the logits again and writes their gradient, 51 MB in 11.3 us
-// (4.5 TB/s).
+// launches reduce those. 16384 tokens x 384 experts are 26 MB, 5.6 us at the
+// card's copy rate, and take 17.8 us, 22.8 us with the reductions. The pass is
+// bound by latency: its 273 vector and 202 scalar instructions a token need some
+// 7 us to issue, but each token's selection is one chain of dependent steps, and
+// the waves wait for 48 % of their cycles. Backward: one pass that reads the
+// logits again and writes their gradient, 51 MB in 11.5 us (4.5 TB/s).
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -144,6 +144,8 @@ struct Norm {
 // exp(x) as 2^(x log2 e): the rounding of the product makes it off by |x|
 // 2^-24 of the result, so by less than 2^-24 of 1 / e at the most where the
 // result is below 1 (all there is here: 1 / (1 + exp) and exp(x - top)).
+// Relative to a small score the error grows with |x|, to 4e-6 at x = -60; a
+// longer argument would cost further instructions for every logit.
 __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
 
 template <bool Softmax>
@@ -344,9 +346,9 @@ __device__ __forceinline__ int select_rounds(const RouterArgs &a, int64_t t, con
 // (a compare and a count of a lane mask each). The experts whose keys reach
 // it, at most 64, are packed to one per lane in the order of their numbers,
 // and each counts the greater keys: its rank (equal keys, seen when two lanes
-// claim a rank, are counted apart by lane). Some 210 vector instructions a
-// token of 384 experts with their scores; taking the greatest key top_k times
-// needs 35 each time.
+// claim a rank, are counted apart by lane). With the scores that is most of a
+// token's 273 vector instructions (384 experts); taking the greatest key top_k
+// times needs 35 each time.
 //
 // With a bias the keys carry roundings. Where two neighbours of the first
 // top_k + 1 (or of a run of equals across that border and the next behind it)
@@ -494,11 +496,20 @@ __device__ __forceinline__ void put_token(const RouterArgs &a, const ForwardOut 
 // tokens that tile i shares with sequence q leave their sums at row i + q:
 // along the tokens each step to the next pair raises i or q, so no two pairs
 // share a row, no sum needs an atomic, and the order of every sum is fixed.
+// Probabilities are added in fp32 over the at most 8 tokens of a wave and the
+// eight waves, which keeps a sum within 15 roundings; sums of tiles are in fp64.
+//
+// The runs of a tile are worked on one after the other, with three barriers
+// each, so a batch of very short sequences takes longer: 256 tokens x 200 in 1 /
+// 8 / 64 / 256 sequences 8.5 / 11.7 / 16.8 / 29.2 us (replayed from a graph),
+// 2048 x 384 in 1 / 13 / 64 / 1024 of them 11.8 / 14.0 / 16.2 / 62 us, 16384 x
+// 384 in 13 / 64 / 1024 / 4096 of them 22.9 / 25.3 / 70.8 / 202 us.
 //
 // Up to 384 experts six waves fit a SIMD (80 registers) instead of four, which
-// 16384 tokens do not need (21.7 against 21.6 us) and longer batches do: 24000
-// x 384 26.7 against 30.7 us, 65536 x 384 48.5 against 52.2. Softmax scores
-// with a bias would spill registers for it.
+// 16384 tokens do not need (one time with both) and longer batches do, compared
+// in one run: 24000 x 384 26.7 against 30.7 us, 65536 x 384 48.5 against 52.2.
+// Softmax scores with a bias would spill registers for it; beyond 384 experts it
+// has not been tried (16384 x 512 24.6 us, without it).
 template <int NJ, bool Softmax, bool Bias>
 __global__ void __launch_bounds__(64 * kWaves, NJ > 6 || (Softmax && Bias) ? 1 : 6) router_forward_kernel(RouterArgs a, ForwardOut o) {
   constexpr int W = kWaves, Threads = 64 * W;
@@ -706,7 +717,9 @@ __device__ __forceinline__ void store_row(const RouterArgs &a, const BackwardIo 
 // have to be read anyway). Of the loss, d/dp_e is the same for all tokens of a
 // sequence and stays in registers; of the weights, the top_k values meet their
 // experts' lanes in the wave's row of shared memory: first the scores lie
-// there for the selected to be picked up, then the selected's gradients.
+// there for the selected to be picked up, then the selected's gradients. An
+// expert in several places adds up by one atomic instruction of one wave, whose
+// lanes shared memory takes in their order (a test holds it to that).
 constexpr int kBackWaves = 4;
 template <int NJ, bool Softmax>
 __global__ void __launch_bounds__(64 * kBackWaves) router_backward_kernel(RouterArgs a, BackwardIo o) {
@@ -901,7 +914,10 @@ RouterArgs args_of(const wt_router_desc &d) {
   return a;
 }
 
-// Calls f with the number of 64-expert columns as a constant.
+// Calls f with the number of 64-expert columns as a constant, the next one that
+// there is: 257 to 384 experts cost the same, and 513 to 1024. 16384 tokens over
+// 256 / 320 / 384 / 512 / 640 / 1024 experts, forward 21 / 22.8 / 23.0 / 24.6 /
+// 40.4 / 42.4 us, backward 10.6 / 12.0 / 12.3 / 14.6 / 21 / 27.7 us.
 template <class F>
 void with_columns(int n_experts, F f) {
   const int nj = (n_experts + 63) / 64;

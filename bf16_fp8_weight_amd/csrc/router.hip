@@ -487,7 +487,7 @@ __device__ __forceinline__ void put_token(const RouterArgs &a, const ForwardOut 
   if (index >= 0) atomicAdd(&cnt[index], 1);
   if (lane < a.top_k) {
     o.index[(int64_t)t * a.top_k + lane] = index;
-    o.weight[(int64_t)t * a.top_k + lane] = w * a.scale;
+    o.weight[(int64_t)t * a.top_k + lane] = index >= 0 ? w * a.scale : 0.0f;  // a NaN sum reaches experts alone
   }
 }
 

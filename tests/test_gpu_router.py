@@ -425,6 +425,21 @@ def test_few_experts_masked_by_the_lowest_value(wt, kind, E, K, where):
         Case(wt, y, K, kind, False, bias=None if b is None else torch.where(b == low, other, b)).check_forward()
 
 
+@pytest.mark.parametrize("kind", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("normalize", [False, True])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_places_without_an_expert_next_to_nan_scores(wt, kind, normalize, value):
+    # a softmax with a NaN or an infinity is NaN; a place that no expert takes holds weight 0 all the same
+    x = logits(8, 20, seed=17)
+    x[:, 6:] = -math.inf
+    x[::2, 3] = value
+    x[5, 2:] = math.nan
+    c = Case(wt, x, 9, kind, normalize)
+    index, weight = c.check_forward()
+    assert (index[:, 6:] == -1).all() and bool((c.weight[:8, 6:] == 0).all())
+    assert np.isnan(weight[0, :5]).all() == (kind == "softmax")
+
+
 def test_offsets_that_make_no_sense_stay_inside_the_arrays(wt):
     # falling, negative and too large offsets: the results mean nothing, the guards stay whole
     for offsets in ([50, 10, 90, 0], [-5, 1 << 30], [100, 0], [7, -7, 7, -7, 7], [2 ** 31 - 1, -(2 ** 31)]):

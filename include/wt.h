@@ -413,7 +413,8 @@ enum { WT_DT_F32 = 0, WT_DT_BF16 = 1 };
  * token goes to its top-k experts) and, in training, the loss that keeps the
  * experts evenly used, with the gradient of both.
  *
- * For token t with logits x_e (fp32 or BF16, computed in fp32):
+ * For token t with logits x_e (fp32 or BF16, computed in fp32; a score below
+ * 2^-126 counts as 0):
  *   score s_e = 1 / (1 + exp(-x_e))   (WT_SCORE_SIGMOID)
  *             = exp(x_e) / sum_j exp(x_j)   (WT_SCORE_SOFTMAX)
  *   selected: the top_k experts by s_e + bias_e (by x_e without a bias), in

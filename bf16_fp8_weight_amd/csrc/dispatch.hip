@@ -30,8 +30,8 @@ namespace {
 constexpr int kMaxExperts = 1024;
 // Copies of a workgroup's tile: kRowsTile, half of it up to kRowsFew, more beyond
 // kMaxTiles tiles. Measured on MI355X, 8 copies of each token over 384 experts,
-// replayed from a graph (with the rule as it is: 1024 tokens 8.2 us, 4096 9.1,
-// 8192 9.7, 16384 10.3, 65536 14.0), tiles of 1024 / 2048 / 4096 copies: 1024 tokens 8.3 / 8.9 / 11.1 us, 4096
+// replayed from a graph (with the rule as it is, row_align 1: 1024 tokens 8.2 us,
+// 4096 9.1, 8192 9.7, 16384 10.3, 65536 14.0), tiles of 1024 / 2048 / 4096 copies: 1024 tokens 8.3 / 8.9 / 11.1 us, 4096
 // tokens 9.2 / 9.3 / 11.5, 8192 tokens 10.3 / 9.9 / 11.7, 16384 tokens 11.7 /
 // 11.1 / 12.2; at most 64 / 128 / 256 tiles: 65536 tokens 17.9 / 14.1 / 15.1 us.
 constexpr int64_t kRowsTile = 2048;

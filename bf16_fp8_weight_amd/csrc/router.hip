@@ -385,8 +385,8 @@ __device__ __forceinline__ void select_topk(const RouterArgs &a, int64_t t, cons
     lo += __popcll(__ballot(u >= lo + step)) >= need ? step : 0u;
     step >>= 1;
   }
-  // numbers up to that of the lowest fp32 value are none of a key (below it lie -infinity and NaNs, which no comparison
-  // reaches): every selectable expert is a candidate
+  // 0x00800000 is the number of the lowest fp32 value, which every key reaches; the numbers below it are those of
+  // -infinity and of NaNs, which no key would
   const bool all = lo <= 0x00800000u;
   const float least = all ? kLowest : from_ordered(lo);
   uint64_t who[NJ];

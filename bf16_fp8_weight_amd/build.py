@@ -17,7 +17,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libwt.so")
 
 SOURCES = ["plan.cpp", "schedule.cpp", "host_api.cpp", "runtime.cpp", "prep_kernels.hip", "progress.hip", "act_quant.hip",
-           "adamw.cpp", "adamw.hip", "router.hip", "dispatch.hip"]
+           "adamw.cpp", "adamw.hip", "router.hip", "dispatch.hip",
+           "expert.cpp", "expert.hip", "mxfp4.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

@@ -1,0 +1,44 @@
+// expert.h -- what the experts' products share between their host checks
+// (expert.cpp, no GPU call) and their kernels (expert_tile.h, expert.hip,
+// mxfp4.hip).
+#pragma once
+
+#include <cstdint>
+#include <string>
+
+#include "wt.h"
+
+namespace wt {
+
+// What a product's kernel takes. Addresses and strides of a, b and their scales
+// in bytes, those of out and pre in elements.
+struct ProductArgs {
+  const int32_t *offsets, *counts;  // offsets NULL: one expert that owns every row
+  const int32_t *row_index;         // of the gathered operand, or NULL
+  uint64_t a, b, a_scales, b_scales, out, pre;
+  int64_t a_stride, b_stride, b_expert;
+  int64_t a_scale_stride, b_scale_stride, b_scale_expert;
+  int64_t out_stride, out_expert, pre_stride;
+  int64_t n_rows, n_index_rows;
+  int32_t n_experts;
+  int32_t m, n, k;      // n: columns of out (of h in the gated forms)
+  int32_t act, out_f32;
+  int32_t out_wide;     // four columns of out (and pre) can be stored at once
+};
+
+enum class Epilogue { kPlain, kGated, kGatedBack };
+
+// Fills *a from a description that it has checked; `what` names the call in the
+// thread's error text.
+wt_status product_args(const char *what, const wt_product_desc *d, Epilogue epi, const void *pre, int64_t pre_stride,
+                       ProductArgs *a);
+wt_status mxfp4_product_args(const char *what, const wt_mxfp4_product_desc *d, ProductArgs *a);
+
+// The caller's error text, set; returns st.
+wt_status operator_fail(const char *what, const std::string &m, wt_status st = WT_E_INVAL);
+
+constexpr int64_t kProductMaxRows = (int64_t)1 << 27;
+constexpr int64_t kProductMaxSize = (int64_t)1 << 24;
+constexpr int kProductMaxExperts = 1024;
+
+}  // namespace wt

@@ -1,0 +1,80 @@
+// expert.hip -- the experts' BF16 products and the gated feed-forward block.
+#include <hip/hip_runtime.h>
+
+#include <string>
+
+#include "expert_tile.h"
+#include "hip_util.h"
+#include "plan.h"
+#include "wt.h"
+
+namespace wt {
+namespace {
+
+constexpr int64_t kMaxGrid = ((int64_t)1 << 31) - 1;
+
+template <int Form, Epilogue Epi>
+wt_status run(const char *what, const ProductArgs &a, hipStream_t stream) {
+  constexpr int BM = 128, BN = 128;
+  constexpr int columns = Epi == Epilogue::kGated ? BN / 2 : BN;
+  const int64_t n_tiles = (a.n + columns - 1) / columns;
+  const int64_t rows = Form == kTN ? (int64_t)(a.m + BM - 1) / BM * a.n_experts : most_row_tiles(a, BM);
+  // rounded up, since tiles are dealt to XCDs in equal parts
+  const int64_t grid = (rows * n_tiles + kXcds - 1) / kXcds * kXcds;
+  if (grid > kMaxGrid) return operator_fail(what, "too many tiles");
+  if (grid == 0) return WT_OK;
+  hipLaunchKernelGGL((product_any_kernel<Form, Epi, false, BM, BN, 2, 2>), dim3((uint32_t)grid), dim3(256), 0, stream, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return operator_fail(what, hip_msg("launch", e), WT_E_HIP);
+  return WT_OK;
+}
+
+}  // namespace
+}  // namespace wt
+
+using namespace wt;
+
+extern "C" {
+
+wt_status wt_expert_product(const wt_product_desc *desc, void *stream) {
+  const char *what = "wt_expert_product";
+  try {
+    ProductArgs a;
+    const wt_status st = product_args(what, desc, Epilogue::kPlain, nullptr, 0, &a);
+    if (st != WT_OK) return st;
+    const StreamDevice on((hipStream_t)stream);
+    if (desc->form == WT_PRODUCT_NT) return run<kNT, Epilogue::kPlain>(what, a, (hipStream_t)stream);
+    if (desc->form == WT_PRODUCT_NN) return run<kNN, Epilogue::kPlain>(what, a, (hipStream_t)stream);
+    return run<kTN, Epilogue::kPlain>(what, a, (hipStream_t)stream);
+  } catch (...) {
+    return caught_status();
+  }
+}
+
+wt_status wt_gated_forward(const wt_product_desc *desc, void *pre, int64_t pre_stride, void *stream) {
+  const char *what = "wt_gated_forward";
+  try {
+    ProductArgs a;
+    const wt_status st = product_args(what, desc, Epilogue::kGated, pre, pre_stride, &a);
+    if (st != WT_OK) return st;
+    const StreamDevice on((hipStream_t)stream);
+    return run<kNT, Epilogue::kGated>(what, a, (hipStream_t)stream);
+  } catch (...) {
+    return caught_status();
+  }
+}
+
+wt_status wt_gated_backward(const wt_product_desc *desc, const void *pre, int64_t pre_stride, void *stream) {
+  const char *what = "wt_gated_backward";
+  try {
+    ProductArgs a;
+    const wt_status st = product_args(what, desc, Epilogue::kGatedBack, pre, pre_stride, &a);
+    if (st != WT_OK) return st;
+    const StreamDevice on((hipStream_t)stream);
+    return run<kNN, Epilogue::kGatedBack>(what, a, (hipStream_t)stream);
+  } catch (...) {
+    return caught_status();
+  }
+}
+
+}  // extern "C"

@@ -34,6 +34,22 @@ struct DeviceGuard {
   }
 };
 
+// Makes a stream's device current for the scope: a launch on a stream of another
+// device than the current one fails. The null stream is the current device's.
+struct StreamDevice {
+  DeviceGuard guard;
+  explicit StreamDevice(hipStream_t stream) : guard(of(stream)) {}
+  static int of(hipStream_t stream) {
+    hipDevice_t dev = -1;
+    if (!stream) return -1;
+    if (hipStreamGetDevice(stream, &dev) != hipSuccess) {
+      (void)hipGetLastError();
+      return -1;
+    }
+    return dev;
+  }
+};
+
 // Checks that [p, p + bytes) lies in one allocation of the expected kind.
 inline wt_status check_memory(const void *p, uint64_t bytes, int32_t kind, int device, const std::string &what,
                               std::string *err) {

@@ -30,6 +30,9 @@ WT_DT_F32 = 0
 WT_DT_BF16 = 1
 WT_SCORE_SIGMOID = 0
 WT_SCORE_SOFTMAX = 1
+WT_PRODUCT_NT, WT_PRODUCT_NN, WT_PRODUCT_TN = range(3)
+WT_ACT_SILU = 0
+WT_ACT_GELU = 1
 
 EXPORTS = [
     "wt_plan_options_init", "wt_plan_check", "wt_plan_schedule", "wt_plan_create", "wt_prepare",
@@ -42,6 +45,8 @@ EXPORTS = [
     "wt_adamw_get_info", "wt_adamw_destroy",
     "wt_router_desc_init", "wt_router_workspace_bytes", "wt_router_forward", "wt_router_backward",
     "wt_dispatch_workspace_bytes", "wt_dispatch_rows",
+    "wt_product_desc_init", "wt_expert_product", "wt_gated_forward", "wt_gated_backward",
+    "wt_mxfp4_quantize", "wt_mxfp4_dequantize", "wt_mxfp4_product_desc_init", "wt_mxfp4_product",
 ]
 
 
@@ -139,6 +144,57 @@ class wt_router_desc(ctypes.Structure):
     ]
 
 
+class wt_product_desc(ctypes.Structure):
+    _fields_ = [
+        ("n_rows", ctypes.c_int64),
+        ("n_experts", ctypes.c_int32),
+        ("form", ctypes.c_int32),
+        ("offsets", ctypes.c_void_p),
+        ("counts", ctypes.c_void_p),
+        ("row_index", ctypes.c_void_p),
+        ("n_index_rows", ctypes.c_int64),
+        ("m", ctypes.c_int64),
+        ("n", ctypes.c_int64),
+        ("k", ctypes.c_int64),
+        ("a", ctypes.c_void_p),
+        ("a_stride", ctypes.c_int64),
+        ("b", ctypes.c_void_p),
+        ("b_stride", ctypes.c_int64),
+        ("b_expert_stride", ctypes.c_int64),
+        ("out", ctypes.c_void_p),
+        ("out_stride", ctypes.c_int64),
+        ("out_expert_stride", ctypes.c_int64),
+        ("out_dtype", ctypes.c_int32),
+        ("act", ctypes.c_int32),
+    ]
+
+
+class wt_mxfp4_product_desc(ctypes.Structure):
+    _fields_ = [
+        ("n_rows", ctypes.c_int64),
+        ("n_experts", ctypes.c_int32),
+        ("gated", ctypes.c_int32),
+        ("offsets", ctypes.c_void_p),
+        ("counts", ctypes.c_void_p),
+        ("n", ctypes.c_int64),
+        ("k", ctypes.c_int64),
+        ("a", ctypes.c_void_p),
+        ("a_stride", ctypes.c_int64),
+        ("a_scales", ctypes.c_void_p),
+        ("a_scale_stride", ctypes.c_int64),
+        ("b", ctypes.c_void_p),
+        ("b_stride", ctypes.c_int64),
+        ("b_expert_stride", ctypes.c_int64),
+        ("b_scales", ctypes.c_void_p),
+        ("b_scale_stride", ctypes.c_int64),
+        ("b_scale_expert_stride", ctypes.c_int64),
+        ("out", ctypes.c_void_p),
+        ("out_stride", ctypes.c_int64),
+        ("out_dtype", ctypes.c_int32),
+        ("act", ctypes.c_int32),
+    ]
+
+
 class wt_adamw_tensor(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("param", "master", "grad", "m", "v", "m_scale", "v_scale")] + [
         ("n", ctypes.c_int64),
@@ -231,6 +287,22 @@ def _load() -> ctypes.CDLL:
     L.wt_dispatch_workspace_bytes.argtypes = [i64, i32, i32, P(sz)]
     L.wt_dispatch_rows.restype = ctypes.c_int
     L.wt_dispatch_rows.argtypes = [vp, i64, i32, i32, i32, i64, vp, vp, vp, vp, vp, sz, vp]
+    L.wt_product_desc_init.restype = None
+    L.wt_product_desc_init.argtypes = [P(wt_product_desc)]
+    L.wt_expert_product.restype = ctypes.c_int
+    L.wt_expert_product.argtypes = [P(wt_product_desc), vp]
+    L.wt_gated_forward.restype = ctypes.c_int
+    L.wt_gated_forward.argtypes = [P(wt_product_desc), vp, i64, vp]
+    L.wt_gated_backward.restype = ctypes.c_int
+    L.wt_gated_backward.argtypes = [P(wt_product_desc), vp, i64, vp]
+    L.wt_mxfp4_quantize.restype = ctypes.c_int
+    L.wt_mxfp4_quantize.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, i64, vp, i64, vp]
+    L.wt_mxfp4_dequantize.restype = ctypes.c_int
+    L.wt_mxfp4_dequantize.argtypes = [vp, i64, vp, i64, i64, i64, vp, i32, i64, vp]
+    L.wt_mxfp4_product_desc_init.restype = None
+    L.wt_mxfp4_product_desc_init.argtypes = [P(wt_mxfp4_product_desc)]
+    L.wt_mxfp4_product.restype = ctypes.c_int
+    L.wt_mxfp4_product.argtypes = [P(wt_mxfp4_product_desc), vp]
     L.wt_adamw_options_init.restype = None
     L.wt_adamw_options_init.argtypes = [P(wt_adamw_options)]
     L.wt_adamw_hyper_init.restype = None
@@ -519,6 +591,46 @@ def wt_dispatch_rows(index: int, n_tokens: int, top_k: int, n_experts: int, row_
 
 
 # ------------------------------------------------------------- optimizer step
+def wt_product_desc_init() -> wt_product_desc:
+    d = wt_product_desc()
+    lib.wt_product_desc_init(ctypes.byref(d))
+    return d
+
+
+def wt_expert_product(desc: wt_product_desc, stream: int = 0) -> None:
+    _check(lib.wt_expert_product(ctypes.byref(desc), stream or None))
+
+
+def wt_gated_forward(desc: wt_product_desc, pre: int = 0, pre_stride: int = 0, stream: int = 0) -> None:
+    _check(lib.wt_gated_forward(ctypes.byref(desc), pre or None, pre_stride, stream or None))
+
+
+def wt_gated_backward(desc: wt_product_desc, pre: int, pre_stride: int, stream: int = 0) -> None:
+    _check(lib.wt_gated_backward(ctypes.byref(desc), pre or None, pre_stride, stream or None))
+
+
+def wt_mxfp4_quantize(x: int, dtype: int, n_rows: int, cols: int, x_row_stride: int, row_index: int, n_out: int,
+                      codes: int, code_row_stride: int, scales: int, scale_row_stride: int, stream: int = 0) -> None:
+    _check(lib.wt_mxfp4_quantize(x or None, dtype, n_rows, cols, x_row_stride, row_index or None, n_out, codes or None,
+                                 code_row_stride, scales or None, scale_row_stride, stream or None))
+
+
+def wt_mxfp4_dequantize(codes: int, code_row_stride: int, scales: int, scale_row_stride: int, n_rows: int, cols: int,
+                        out: int, dtype: int, out_row_stride: int, stream: int = 0) -> None:
+    _check(lib.wt_mxfp4_dequantize(codes or None, code_row_stride, scales or None, scale_row_stride, n_rows, cols,
+                                   out or None, dtype, out_row_stride, stream or None))
+
+
+def wt_mxfp4_product_desc_init() -> wt_mxfp4_product_desc:
+    d = wt_mxfp4_product_desc()
+    lib.wt_mxfp4_product_desc_init(ctypes.byref(d))
+    return d
+
+
+def wt_mxfp4_product(desc: wt_mxfp4_product_desc, stream: int = 0) -> None:
+    _check(lib.wt_mxfp4_product(ctypes.byref(desc), stream or None))
+
+
 def wt_adamw_options_init() -> wt_adamw_options:
     o = wt_adamw_options()
     lib.wt_adamw_options_init(ctypes.byref(o))

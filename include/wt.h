@@ -507,6 +507,153 @@ wt_status wt_dispatch_rows(const int32_t *index, int64_t n_tokens, int32_t top_k
                            int32_t row_align, int64_t n_rows, int32_t *row_token, int32_t *pair_row,
                            int32_t *offsets, int32_t *counts, void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---- Experts: grouped products and the gated feed-forward block ----
+ * What a token's copies go through between the row map and the way back ("Weight
+ * transfer for RL post-training in under 2 seconds", section "Task pipeline":
+ * gate and up projections are fused to gate_up; "Enabling trillion-parameter
+ * models on AWS EFA": tokens reach their experts as groups of rows), forward and
+ * backward, over the weights that wt_adamw_step updates and wt_prepare ships. A
+ * dense layer is one expert that owns every row.
+ *
+ * Rows. Expert e owns the rows [offsets[e], offsets[e] + counts[e]) of a row
+ * space of n_rows rows, as wt_dispatch_rows leaves them; offsets and counts stay
+ * on the device. Other rows (padding, and what lies behind the last expert) are
+ * neither read nor written. Offsets or counts that leave [0, n_rows] are cut to
+ * it; experts whose rows overlap give meaningless results in those rows, but no
+ * access outside the arrays.
+ *
+ * wt_expert_product, per expert e with rows r (BF16 operands, fp32 sums, rounded
+ * once to out_dtype):
+ *   WT_PRODUCT_NT: out[r, j] = sum_k a[r, k] b_e[j, k]    j < n: a projection, b_e [n x k]
+ *   WT_PRODUCT_NN: out[r, j] = sum_k a[r, k] b_e[k, j]    j < n: its input's gradient, b_e [k x n]
+ *   WT_PRODUCT_TN: out_e[i, j] = sum_r a[r, i] b[r, j]    i < m, j < n: its weights' gradient
+ *     (zeros for an expert without rows; k is ignored)
+ * row_index (may be NULL) makes row r of one operand row row_index[r] of an
+ * array of n_index_rows rows: of a in NT and NN, of b in TN. Row numbers outside
+ * of it stand for a row of zeros; the same row may be taken many times.
+ *
+ * wt_gated_forward (form NT, b_e [2n x k]: n gate rows, then n up rows, the order
+ * of a fused gate_up): g = a[r] . b_e[j], u = a[r] . b_e[n + j],
+ *   out[r, j] = act(g) u, rounded once to BF16; pre (may be NULL): pre[r, j] = g,
+ *   pre[r, n + j] = u in BF16, what the backward pass reads.
+ * wt_gated_backward (form NN, a = the gradient of the block's output, b_e = the
+ * weights back, [k x n]): dh = a[r] . b_e[:, j], g and u from pre,
+ *   out[r, j] = dh u act'(g), out[r, n + j] = dh act(g), in BF16 (out has 2n columns).
+ * The rest of the block's backward pass are products of `out`: NN with the
+ * gate_up weights for the rows' gradient, TN with the rows for the weights'.
+ *   act = WT_ACT_SILU: x / (1 + exp(-x)); WT_ACT_GELU: x / 2 (1 + tanh(sqrt(2 / pi)
+ *   (x + 0.044715 x^3))); at an infinity their limits.
+ *
+ * A NaN or an infinity in an operand reaches exactly the results whose sum it is
+ * part of. Sums run in an order that depends on the sizes alone: a call repeats
+ * bit for bit. Arrays with rows (and TN's out) whose strides are multiples of 8
+ * elements and whose addresses are multiples of 16 bytes, with even sizes (k a
+ * multiple of 8 in NT, and for a in NN), take the fast path; any other shape a
+ * general one, same results to rounding. No workspace; every call may be
+ * captured. Calls on the same arrays must be ordered. */
+enum { WT_PRODUCT_NT = 0, WT_PRODUCT_NN = 1, WT_PRODUCT_TN = 2 };
+enum { WT_ACT_SILU = 0, WT_ACT_GELU = 1 };
+
+typedef struct wt_product_desc {
+  int64_t n_rows;          /* 0 .. 2^27 */
+  int32_t n_experts;       /* 1 .. 1024 */
+  int32_t form;
+  const int32_t *offsets;  /* n_experts + 1, or NULL: one expert that owns every row */
+  const int32_t *counts;   /* n_experts, or NULL: counts[e] = offsets[e + 1] - offsets[e] */
+  const int32_t *row_index; /* n_rows, or NULL */
+  int64_t n_index_rows;    /* 0 .. 2^31 - 1, with row_index */
+  int64_t m, n, k;         /* 1 .. 2^24 where the form has them */
+  const void *a;           /* rows, BF16 */
+  int64_t a_stride;        /* elements from row to row, at least the row's length; likewise below */
+  const void *b;           /* NT, NN: the weights; TN: rows */
+  int64_t b_stride;
+  int64_t b_expert_stride; /* NT, NN: elements from expert to expert (0: all share one) */
+  void *out;               /* NT, NN: rows; TN: n_experts matrices */
+  int64_t out_stride;
+  int64_t out_expert_stride; /* TN: elements from expert to expert */
+  int32_t out_dtype;       /* WT_DT_BF16 or WT_DT_F32 (gated calls: WT_DT_BF16) */
+  int32_t act;             /* gated calls */
+} wt_product_desc;
+
+/* Zeroes, then n_experts = 1 and out_dtype = WT_DT_BF16. */
+void wt_product_desc_init(wt_product_desc *desc);
+
+/* Enqueued on `stream` (of the device that owns the arrays, whichever is
+ * current; NULL: the current device's null stream); returns without waiting.
+ * WT_E_INVAL: NULL pointers, sizes, strides or values out of range (a grid of
+ * 2^31 tiles too); WT_E_ALIGN: an address that is no multiple of its element's
+ * size; WT_E_HIP if a launch fails. n_rows = 0 is a no-op in NT and NN. */
+wt_status wt_expert_product(const wt_product_desc *desc, void *stream);
+wt_status wt_gated_forward(const wt_product_desc *desc, void *pre, int64_t pre_stride, void *stream);
+wt_status wt_gated_backward(const wt_product_desc *desc, const void *pre, int64_t pre_stride, void *stream);
+
+/* ---- MXFP4: 4-bit floating point with a scale to each 32 elements ----
+ * The OCP microscaling format MXFP4, the narrower companion of the block-scaled
+ * FP8 above: elements E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives: code =
+ * sign 8 + index), scales E8M0 (byte c stands for 2^(c - 127), 255 for NaN), one
+ * to each 32 consecutive elements of a row.
+ *
+ * Quantisation of a block with the largest magnitude amax:
+ *   c = 127 + clamp(floor(log2 amax) - 2, -127, 125) (127 for a block of zeros),
+ *   element = the value nearest to x / 2^(c - 127), of two equally near ones the
+ *   even code, magnitudes beyond 6 become 6; the sign is kept, also of a zero.
+ *   A block that holds a NaN or an infinity gets c = 255 and codes 0, so that all
+ *   of it reads as NaN.
+ * Element 2i of a row is the low half of byte i, element 2i + 1 the high half. A
+ * row's codes take 16 ceil(cols / 32) bytes (the last block is filled with
+ * codes 0), its scales ceil(cols / 32). */
+
+/* x: n_rows rows of cols elements of `dtype`, x_row_stride elements apart.
+ * row_index (may be NULL): output row i quantizes row row_index[i], as in
+ * wt_quantize_act_b128; output rows whose index is outside of [0, n_rows) are not
+ * written. codes: 4-byte aligned, code_row_stride bytes from row to row, a
+ * multiple of 4 and >= 16 ceil(cols / 32); scales: scale_row_stride bytes >= ceil(cols /
+ * 32). Bytes between the rows are left alone. For the operands of
+ * wt_mxfp4_product see the alignments there. Weights are rows too: a matrix
+ * [n x k] is quantized along k. Errors as for wt_quantize_act_b128 (with
+ * ceil(cols / 32) for its ceil(cols / 128)). */
+wt_status wt_mxfp4_quantize(const void *x, int32_t dtype, int64_t n_rows, int64_t cols, int64_t x_row_stride,
+                            const int32_t *row_index, int64_t n_out, void *codes, int64_t code_row_stride,
+                            void *scales, int64_t scale_row_stride, void *stream);
+
+/* out (dtype WT_DT_BF16 or WT_DT_F32): the values that n_rows rows of codes stand
+ * for. Every value but those that overflow (c > 252) is exact in both types. */
+wt_status wt_mxfp4_dequantize(const void *codes, int64_t code_row_stride, const void *scales,
+                              int64_t scale_row_stride, int64_t n_rows, int64_t cols, void *out, int32_t dtype,
+                              int64_t out_row_stride, void *stream);
+
+/* out[r, j] = sum_k a[r, k] b_e[j, k] over the values that the codes stand for, in
+ * fp32 sums; gated = 1: out[r, j] = act(a[r] . b_e[j]) (a[r] . b_e[n + j]), b_e
+ * then having 2n rows. Experts and rows as for wt_expert_product. The rows of a
+ * are the expert's own (gather while quantizing). Strides of codes and scales are in bytes.
+ * Codes: 16-byte aligned, strides multiples of 16 and rows >= 16 ceil(k / 32) bytes whose codes
+ * beyond k are 0, as wt_mxfp4_quantize writes them; scales: 4-byte aligned,
+ * strides multiples of 4, rows >= ceil(k / 32) (WT_E_ALIGN otherwise). */
+typedef struct wt_mxfp4_product_desc {
+  int64_t n_rows;          /* 0 .. 2^27 */
+  int32_t n_experts;       /* 1 .. 1024 */
+  int32_t gated;           /* 0 or 1 */
+  const int32_t *offsets;  /* as in wt_product_desc */
+  const int32_t *counts;
+  int64_t n, k;            /* 1 .. 2^24 */
+  const void *a;
+  int64_t a_stride;
+  const void *a_scales;
+  int64_t a_scale_stride;
+  const void *b;
+  int64_t b_stride, b_expert_stride;
+  const void *b_scales;
+  int64_t b_scale_stride, b_scale_expert_stride;
+  void *out;
+  int64_t out_stride;      /* elements */
+  int32_t out_dtype;       /* WT_DT_BF16 or WT_DT_F32 */
+  int32_t act;             /* with gated */
+} wt_mxfp4_product_desc;
+
+/* Zeroes, then n_experts = 1 and out_dtype = WT_DT_BF16. */
+void wt_mxfp4_product_desc_init(wt_mxfp4_product_desc *desc);
+wt_status wt_mxfp4_product(const wt_mxfp4_product_desc *desc, void *stream);
+
 /* ---- AdamW over many parameter shards ----
  * The optimizer step that produces what wt_prepare transfers ("Weight transfer
  * for RL post-training in under 2 seconds", section "High-level workflow":

@@ -11,11 +11,11 @@
 namespace wt {
 namespace {
 
+constexpr int kCus = 256;
 constexpr int64_t kMaxGrid = ((int64_t)1 << 31) - 1;
 
-template <int Form, Epilogue Epi>
-wt_status run(const char *what, const ProductArgs &a, hipStream_t stream) {
-  constexpr int BM = 128, BN = 128;
+template <int Form, Epilogue Epi, int BM, int BN, int WM, int WN, bool Aligned>
+wt_status launch(const char *what, const ProductArgs &a, hipStream_t stream) {
   constexpr int columns = Epi == Epilogue::kGated ? BN / 2 : BN;
   const int64_t n_tiles = (a.n + columns - 1) / columns;
   const int64_t rows = Form == kTN ? (int64_t)(a.m + BM - 1) / BM * a.n_experts : most_row_tiles(a, BM);
@@ -23,10 +23,22 @@ wt_status run(const char *what, const ProductArgs &a, hipStream_t stream) {
   const int64_t grid = (rows * n_tiles + kXcds - 1) / kXcds * kXcds;
   if (grid > kMaxGrid) return operator_fail(what, "too many tiles");
   if (grid == 0) return WT_OK;
-  hipLaunchKernelGGL((product_any_kernel<Form, Epi, false, BM, BN, 2, 2>), dim3((uint32_t)grid), dim3(256), 0, stream, a);
+  if constexpr (Aligned)
+    hipLaunchKernelGGL((product_kernel<Form, Epi, false, BM, BN, WM, WN>), dim3((uint32_t)grid), dim3(64 * WM * WN), 0, stream, a);
+  else
+    hipLaunchKernelGGL((product_any_kernel<Form, Epi, false, BM, BN, WM, WN>), dim3((uint32_t)grid), dim3(64 * WM * WN), 0, stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return operator_fail(what, hip_msg("launch", e), WT_E_HIP);
   return WT_OK;
+}
+
+template <int Form, Epilogue Epi>
+wt_status run(const char *what, const ProductArgs &a, hipStream_t stream) {
+  if (!product_aligned(a, Form, Epi)) return launch<Form, Epi, 128, 128, 2, 2, false>(what, a, stream);
+  const int64_t rows = Form == kTN ? (int64_t)(a.m + 255) / 256 * a.n_experts : most_row_tiles(a, 256);
+  const int64_t tiles = rows * ((a.n + (Epi == Epilogue::kGated ? 127 : 255)) / (Epi == Epilogue::kGated ? 128 : 256));
+  return tiles < kCus ? launch<Form, Epi, 128, 128, 2, 2, true>(what, a, stream)
+                      : launch<Form, Epi, 256, 256, 2, 4, true>(what, a, stream);
 }
 
 }  // namespace

@@ -394,6 +394,27 @@ __device__ __forceinline__ void finish4(const ProductArgs &a, uint64_t out, int6
   }
 }
 
+template <int Form, Epilogue Epi, bool F4, int BM, int BN, int WM, int WN, int TM, int TN>
+__device__ __forceinline__ void finish_tile(const ProductArgs &a, const Rows &r, int m0, int n0, int m_left, int wm, int wn,
+                                            const f32x4 (&acc)[TM][TN]) {
+  using T = Tile<Form, Epi, F4, BM, BN, WM, WN>;
+  const int lane = threadIdx.x & 63;
+  const uint64_t out = a.out + (Form == kTN ? (uint64_t)(a.out_expert * r.expert) * (a.out_f32 ? 4 : 2) : 0);
+  constexpr int kCols = Epi == Epilogue::kGated ? TN / 2 : TN;
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int row = wm * (BM / WM) + 16 * i + (lane & 15);
+    if (row >= m_left) continue;
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) {
+      const int column = n0 + T::out_column(wn, j) + 4 * (lane >> 4);
+      if (column < a.n)
+        finish4<Epi>(a, out, (Form == kTN ? 0 : r.first) + m0 + row, column, a.n - column, acc[i][j],
+                     Epi == Epilogue::kGated ? acc[i][j + kCols] : acc[i][j]);
+    }
+  }
+}
+
 // ------------------------------------------------- operands of any alignment
 // The next step's chunks are loaded to registers before the present one is
 // computed and stored to the other half of shared memory behind it.
@@ -507,21 +528,181 @@ __global__ void __launch_bounds__(64 * WM * WN) product_any_kernel(ProductArgs a
     }
   }
 
-  const int lane = tid & 63;
-  const uint64_t out = a.out + (Form == kTN ? (uint64_t)(a.out_expert * r.expert) * (a.out_f32 ? 4 : 2) : 0);
-  constexpr int kCols = Epi == Epilogue::kGated ? T::kTN_ / 2 : T::kTN_;
-#pragma unroll
-  for (int i = 0; i < T::kTM; ++i) {
-    const int row = wm * (BM / WM) + 16 * i + (lane & 15);
-    if (row >= m_left) continue;
-#pragma unroll
-    for (int j = 0; j < kCols; ++j) {
-      const int column = n0 + T::out_column(wn, j) + 4 * (lane >> 4);
-      if (column < a.n)
-        finish4<Epi>(a, out, (Form == kTN ? 0 : r.first) + m0 + row, column, a.n - column, acc[i][j],
-                     Epi == Epilogue::kGated ? acc[i][j + kCols] : acc[i][j]);
-    }
+  finish_tile<Form, Epi, F4, BM, BN, WM, WN>(a, r, m0, n0, m_left, wm, wn, acc);
+}
+
+// ------------------------------------------------------ aligned operands
+// buffer_load ... lds copies 16 bytes a lane straight into shared memory, at
+// consecutive places of a wave (from M0 on), so the swizzle is in the addresses that are
+// read. What lies outside of [base, base + bytes) reads as 0 and touches no
+// memory: rows behind the last, and offsets set to kNowhere.
+constexpr uint32_t kNowhere = 0x80000000u;
+
+// The compiler does not count these loads: wait_and_meet() waits for all of them.
+__device__ __forceinline__ void copy16(u32x4 buffer, uint32_t lds, uint32_t offset) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(buffer) : "memory");
+}
+__device__ __forceinline__ void copy4(u32x4 buffer, uint32_t lds, uint32_t offset) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(buffer) : "memory");
+}
+
+// What this wave copied has arrived and what it read has been read; then the workgroup meets.
+__device__ __forceinline__ void wait_and_meet() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// A window over an operand that moves along the sum; everything in it is uniform.
+struct Window {
+  uint64_t base;
+  int64_t bytes;  // from base to the operand's end
+  __device__ __forceinline__ u32x4 buffer() const {
+    const int64_t n = bytes < 0 ? 0 : bytes < 0x7FFFFFF0 ? bytes : 0x7FFFFFF0;
+    u32x4 r;
+    r.x = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)base);
+    r.y = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(base >> 32)) & 0xFFFFu;
+    r.z = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)n);
+    r.w = 0x00020000u;
+    return r;
   }
+  __device__ __forceinline__ void move(int64_t by) {
+    base += (uint64_t)by;
+    bytes -= by;
+  }
+};
+
+template <int Form, Epilogue Epi, bool F4, int BM, int BN, int WM, int WN>
+__global__ void __launch_bounds__(64 * WM * WN, 2) product_kernel(ProductArgs a) {
+  using T = Tile<Form, Epi, F4, BM, BN, WM, WN>;
+  using PA = typename T::PlaceA;
+  using PB = typename T::PlaceB;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2][T::kLds];
+  Rows r;
+  int mt, nt;
+  const uint32_t n_tiles = (uint32_t)(a.n + T::kColumns - 1) / T::kColumns;
+  const bool mine = Form == kTN ? find_matrix(a, blockIdx.x, (uint32_t)(a.m + BM - 1) / BM, n_tiles, r, mt, nt)
+                                : find_rows<BM>(a, blockIdx.x, n_tiles, r, mt, nt);
+  if (!mine) return;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WN, wn = wave % WN;
+  const int m0 = mt * BM, n0 = nt * T::kColumns;
+  const int m_left = (Form == kTN ? a.m : r.count) - m0;
+  // bytes of a row along the sum, or rows across it
+  const int64_t row_bytes = F4 ? (int64_t)(a.k + 31) / 32 * 16 : 2 * (int64_t)a.k;
+  const int64_t K = Form == kTN ? r.count : a.k;
+  const int steps = (int)((K + T::kStep - 1) / T::kStep);
+
+  Window wa, wb;
+  uint32_t oa[PA::kEach], ob[PB::kEach];
+  auto index_of = [&](int64_t row) -> uint32_t {  // of the gathered operand, kNowhere if there is none
+    const int64_t i = a.row_index[row];
+    return i >= 0 && i < a.n_index_rows ? (uint32_t)i : kNowhere;
+  };
+  const bool gather_a = Form != kTN && !F4 && a.row_index, gather_b = Form == kTN && a.row_index;
+  if (T::kAcrossA) {
+    wa = {a.a + (uint64_t)(r.first * a.a_stride + 2 * (int64_t)m0), (K - 1) * a.a_stride + 2 * (int64_t)(a.m - m0)};
+  } else if (gather_a) {
+    wa = {a.a, (a.n_index_rows - 1) * a.a_stride + row_bytes};
+  } else {
+    wa = {a.a + (uint64_t)((r.first + m0) * a.a_stride), (int64_t)(m_left - 1) * a.a_stride + row_bytes};
+  }
+#pragma unroll
+  for (int i = 0; i < PA::kEach; ++i) {
+    int row, chunk;
+    PA::source(tid + i * T::kThreads, row, chunk);
+    uint32_t at = (uint32_t)row;
+    if (gather_a) at = row < m_left ? index_of(r.first + m0 + row) : kNowhere;
+    oa[i] = at == kNowhere ? kNowhere : at * (uint32_t)a.a_stride + 16u * chunk;
+  }
+  const uint64_t b_base = a.b + (Form == kTN ? 0 : (uint64_t)(a.b_expert * r.expert));
+  if (T::kAcrossB) {
+    const int64_t rows = gather_b ? a.n_index_rows : K;
+    wb = {b_base + (uint64_t)((Form == kTN && !gather_b ? r.first * a.b_stride : 0) + 2 * (int64_t)n0),
+          (rows - 1) * a.b_stride + 2 * (int64_t)(a.n - n0)};
+  } else {
+    const int64_t rows = Epi == Epilogue::kGated ? 2 * (int64_t)a.n : a.n;
+    wb = {b_base + (uint64_t)(n0 * a.b_stride), (rows - n0 - 1) * a.b_stride + row_bytes};
+  }
+#pragma unroll
+  for (int i = 0; i < PB::kEach; ++i) {
+    int row, chunk;
+    PB::source(tid + i * T::kThreads, row, chunk);
+    if (Epi == Epilogue::kGated && row >= T::kColumns) row += a.n - T::kColumns;  // up rows
+    ob[i] = (uint32_t)row * (uint32_t)a.b_stride + 16u * chunk;
+  }
+  uint32_t next_row[PB::kEach];  // of b, gathered: one step ahead
+  auto load_rows = [&](int step) {
+#pragma unroll
+    for (int i = 0; i < PB::kEach; ++i) {
+      int row, chunk;
+      PB::source(tid + i * T::kThreads, row, chunk);
+      const int64_t k = (int64_t)step * T::kStep + row;
+      next_row[i] = k < K ? index_of(r.first + k) : kNowhere;
+    }
+  };
+  if (gather_b && steps > 0) load_rows(0);
+
+  Window sa{}, sb{};
+  uint32_t osa = 0, osb = 0;
+  static_assert(!F4 || (BM * 2 == T::kThreads && BN * 2 == T::kThreads), "one word of scales to a thread");
+  if (F4) {
+    const int64_t nb = (a.k + 31) / 32, words = (nb + 3) / 4 * 4;
+    sa = {a.a_scales + (uint64_t)((r.first + m0) * a.a_scale_stride), (int64_t)(m_left - 1) * a.a_scale_stride + words};
+    const int64_t rows = Epi == Epilogue::kGated ? 2 * (int64_t)a.n : a.n;
+    sb = {a.b_scales + (uint64_t)(a.b_scale_expert * r.expert + n0 * a.b_scale_stride), (rows - n0 - 1) * a.b_scale_stride + words};
+    int row = tid >> 1;
+    osa = (uint32_t)row * (uint32_t)a.a_scale_stride + 4u * (tid & 1);
+    if (Epi == Epilogue::kGated && row >= T::kColumns) row += a.n - T::kColumns;
+    osb = (uint32_t)row * (uint32_t)a.b_scale_stride + 4u * (tid & 1);
+  }
+
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)&lds[0][0] + 1024u * wave;
+  auto fetch = [&](int step) {
+    const uint32_t to = lds0 + (step & 1) * T::kLds;
+    const u32x4 ba = wa.buffer(), bb = wb.buffer();
+    // the row's end lies within the last step: chunks behind it are not the next row's
+    const int64_t left = row_bytes - (int64_t)step * kStepBytes;
+    const bool cut = left < kStepBytes;
+#pragma unroll
+    for (int i = 0; i < PA::kEach; ++i) {
+      uint32_t at = oa[i];
+      if (!T::kAcrossA && cut) {
+        int row, chunk;
+        PA::source(tid + i * T::kThreads, row, chunk);
+        at = 16 * chunk < left ? at : kNowhere;
+      }
+      copy16(ba, to + i * T::kThreads * 16, at);
+    }
+#pragma unroll
+    for (int i = 0; i < PB::kEach; ++i) {
+      uint32_t at = ob[i];
+      int row, chunk;
+      PB::source(tid + i * T::kThreads, row, chunk);
+      if (!T::kAcrossB && cut) at = 16 * chunk < left ? at : kNowhere;
+      if (gather_b) at = next_row[i] == kNowhere ? kNowhere : next_row[i] * (uint32_t)a.b_stride + 16u * chunk;
+      copy16(bb, to + T::kLdsA + i * T::kThreads * 16, at);
+    }
+    wa.move(T::kAcrossA ? 64 * a.a_stride : kStepBytes);
+    if (!gather_b) wb.move(T::kAcrossB ? 64 * a.b_stride : kStepBytes);
+    if (F4) {
+      const uint32_t scales = to - 1024u * wave + T::kLdsA + T::kLdsB + 256u * wave;
+      copy4(sa.buffer(), scales, osa);
+      copy4(sb.buffer(), scales + BM * 8, osb);
+      sa.move(8);
+      sb.move(8);
+    }
+    if (gather_b && step + 1 < steps) load_rows(step + 1);
+  };
+
+  f32x4 acc[T::kTM][T::kTN_];
+#pragma unroll
+  for (int i = 0; i < T::kTM; ++i)
+#pragma unroll
+    for (int j = 0; j < T::kTN_; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+  if (steps > 0) fetch(0);
+  for (int step = 0; step < steps; ++step) {
+    // this step's operands are there, and nobody reads the other half any more
+    wait_and_meet();
+    if (step + 1 < steps) fetch(step + 1);
+    T::step(lds[step & 1], wm, wn, F4 ? (a.k + 31) / 32 - 8 * step : 0, acc);
+  }
+  finish_tile<Form, Epi, F4, BM, BN, WM, WN>(a, r, m0, n0, m_left, wm, wn, acc);
 }
 
 // Row tiles that n_rows rows of n_experts experts can make.

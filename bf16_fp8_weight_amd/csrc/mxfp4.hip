@@ -18,6 +18,7 @@
 namespace wt {
 namespace {
 
+constexpr int kCus = 256;
 constexpr int64_t kMaxGrid = ((int64_t)1 << 31) - 1;
 constexpr int kThreads = 256;
 constexpr int kLanes = 4;  // of a block, 8 elements each
@@ -142,18 +143,30 @@ wt_status check_round(const char *what, int32_t dtype, int64_t n_rows, int64_t n
   return WT_OK;
 }
 
-template <Epilogue Epi>
-wt_status run(const char *what, const ProductArgs &a, hipStream_t stream) {
-  constexpr int BM = 128, BN = 128;
+template <Epilogue Epi, int BM, int BN, int WM, int WN, bool Near>
+wt_status launch(const char *what, const ProductArgs &a, hipStream_t stream) {
   constexpr int columns = Epi == Epilogue::kGated ? BN / 2 : BN;
   const int64_t n_tiles = (a.n + columns - 1) / columns;
   const int64_t grid = (most_row_tiles(a, BM) * n_tiles + kXcds - 1) / kXcds * kXcds;
   if (grid > kMaxGrid) return operator_fail(what, "too many tiles");
   if (grid == 0) return WT_OK;
-  hipLaunchKernelGGL((product_any_kernel<kNT, Epi, true, BM, BN, 2, 2>), dim3((uint32_t)grid), dim3(256), 0, stream, a);
+  if constexpr (Near)
+    hipLaunchKernelGGL((product_kernel<kNT, Epi, true, BM, BN, WM, WN>), dim3((uint32_t)grid), dim3(64 * WM * WN), 0, stream, a);
+  else
+    hipLaunchKernelGGL((product_any_kernel<kNT, Epi, true, BM, BN, WM, WN>), dim3((uint32_t)grid), dim3(64 * WM * WN), 0, stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return operator_fail(what, hip_msg("launch", e), WT_E_HIP);
   return WT_OK;
+}
+
+template <Epilogue Epi>
+wt_status run(const char *what, const ProductArgs &a, hipStream_t stream) {
+  const int64_t far = (int64_t)1 << 31;
+  const bool near = a.a_stride <= far / 512 && a.b_stride <= far / 512 && (int64_t)(a.n + 512) * a.b_stride < far &&
+                    a.a_scale_stride <= far / 512 && a.b_scale_stride <= far / 512 && (int64_t)(a.n + 512) * a.b_scale_stride < far;
+  if (!near) return launch<Epi, 128, 128, 2, 2, false>(what, a, stream);
+  const int64_t tiles = most_row_tiles(a, 256) * ((a.n + (Epi == Epilogue::kGated ? 127 : 255)) / (Epi == Epilogue::kGated ? 128 : 256));
+  return tiles < kCus ? launch<Epi, 128, 128, 2, 2, true>(what, a, stream) : launch<Epi, 256, 256, 2, 4, true>(what, a, stream);
 }
 
 }  // namespace

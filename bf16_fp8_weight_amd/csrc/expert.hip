@@ -23,10 +23,11 @@ wt_status launch(const char *what, const ProductArgs &a, hipStream_t stream) {
   const int64_t grid = (rows * n_tiles + kXcds - 1) / kXcds * kXcds;
   if (grid > kMaxGrid) return operator_fail(what, "too many tiles");
   if (grid == 0) return WT_OK;
-  if constexpr (Aligned)
-    hipLaunchKernelGGL((product_kernel<Form, Epi, false, BM, BN, WM, WN>), dim3((uint32_t)grid), dim3(64 * WM * WN), 0, stream, a);
-  else
-    hipLaunchKernelGGL((product_any_kernel<Form, Epi, false, BM, BN, WM, WN>), dim3((uint32_t)grid), dim3(64 * WM * WN), 0, stream, a);
+  auto kernel = product_any_kernel<Form, Epi, false, 128, 128, 2, 2>;
+  if constexpr (Aligned) kernel = product_kernel<Form, Epi, false, BM, BN, WM, WN, false>;
+  if constexpr (Aligned && Form == kTN)
+    if (a.row_index) kernel = product_kernel<Form, Epi, false, BM, BN, WM, WN, true>;
+  hipLaunchKernelGGL(kernel, dim3((uint32_t)grid), dim3(64 * WM * WN), 0, stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return operator_fail(what, hip_msg("launch", e), WT_E_HIP);
   return WT_OK;

@@ -3,29 +3,35 @@
 // done with the sums. The definitions are in wt.h.
 //
 // A workgroup of WM x WN waves computes BM x BN results. Both operands pass
-// through shared memory in steps of 128 bytes along the sum (64 BF16 elements or
-// 256 MXFP4 codes), in 16-byte chunks:
+// through shared memory in steps of 64 bytes along the sum (32 BF16 elements or
+// 128 MXFP4 codes), in 16-byte chunks:
 //   - an operand whose rows run along the sum (a and b of NT, a of NN) as its rows
-//     of 8 chunks, chunk c of row r at slot c ^ (r & 7), so that the 16 rows that
-//     the lanes of a matrix instruction read at once lie in different banks;
-//   - one whose rows run across it (b of NN, a and b of TN) as it comes, 64 rows of
+//     of 4 chunks, chunk c of row r at slot c ^ (r / 2 & 3), so that the 8 rows that
+//     are read in one cycle lie in different banks;
+//   - one whose rows run across it (b of NN, a and b of TN) as it comes, 32 rows of
 //     BM or BN elements, read back transposed (ds_read_b64_tr_b16: a 16-lane group
 //     fetches 4 rows x 16 columns, each lane receiving a column); there chunk c
 //     of row k lies at slot c ^ swizzle(k), because those 4 rows would share banks.
-// The matrix instructions take b's tile as their first operand: a lane then holds
-// four neighbouring columns of one row of out.
+// The matrix instructions take b's tile as their first operand: a lane then holds four
+// neighbouring columns of one row of out. BF16 takes 16 x 16 x 32; 32 x 32 x 16 were
+// slower in the whole kernel (8192 x 8192 x 8192: 1240 to 1270 TFLOP/s against 1330 to
+// 1350). MXFP4 takes 32 x 32 x 64, which reach 8.8 PFLOP/s over registers alone (7.0 on
+// random values, under the power limit) where 16 x 16 x 128 reach 6.3 (5.7).
 #pragma once
 
 #include <hip/hip_runtime.h>
 
 #include <cfloat>
 #include <cstdint>
+#include <type_traits>
+#include <utility>
 
 #include "expert.h"
 
 namespace wt {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
@@ -33,9 +39,22 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 
+// Calls f with the integral constants 0 .. N - 1.
+template <class F, int... I>
+__device__ __forceinline__ void static_calls(F f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>()), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void static_for(F f) {
+  static_calls(f, std::make_integer_sequence<int, N>());
+}
+
 enum Form { kNT = WT_PRODUCT_NT, kNN = WT_PRODUCT_NN, kTN = WT_PRODUCT_TN };
 
-constexpr int kStepBytes = 128;  // of a row along the sum
+constexpr int kStepBytes = 64;  // of a row along the sum
+// MXFP4: a row's scales are copied for several steps at a time. One word to a row and
+// step made as many requests as the operands (8192 x 8192 x 8192 360 us).
+constexpr int kScaleSteps = 4, kScaleRow = 4 * kScaleSteps;
 
 // ------------------------------------------------------------- activations
 // Both are x s(y) with s(y) = 1 / (1 + exp(-y)): SiLU y = x; GELU's
@@ -179,18 +198,18 @@ __device__ __forceinline__ bool find_matrix(const ProductArgs &a, uint32_t block
 // that reads beside it (8 rows on), in different 32-byte slots.
 __device__ __forceinline__ uint32_t swizzle(uint32_t k) { return ((k & 3) | (k >> 3 & 1) << 2) << 1; }
 
-// One operand's tile of a step: N rows of the operand (along the sum) or 64 rows of N elements (across it).
+// One operand's tile of a step: N rows of the operand (along the sum) or 32 rows of N elements (across it).
 template <int N, bool Across, int Threads>
 struct Place {
-  static constexpr int kChunks = N * 8;  // 16-byte chunks
+  static constexpr int kChunks = N * 4;  // 16-byte chunks
   static constexpr int kEach = kChunks / Threads;
-  static constexpr int kRow = Across ? N / 8 : 8;  // chunks of a row in shared memory
+  static constexpr int kRow = Across ? N / 8 : 4;  // chunks of a row in shared memory
   static_assert(kChunks % Threads == 0, "chunks per thread");
   static_assert(!Across || N >= 128, "the swizzle spans 16 chunks");
   // Chunk q of the tile holds (row, chunk) of the operand.
   static __device__ __forceinline__ void source(int q, int &row, int &chunk) {
     row = q / kRow;
-    chunk = (q % kRow) ^ (int)(Across ? swizzle(row) : row & 7);
+    chunk = (q % kRow) ^ (int)(Across ? swizzle(row) : row >> 1 & 3);
   }
 };
 
@@ -213,12 +232,15 @@ template <int Form, Epilogue Epi, bool F4, int BM, int BN, int WM, int WN>
 struct Tile {
   static constexpr int kThreads = 64 * WM * WN;
   static constexpr bool kAcrossA = Form == kTN, kAcrossB = Form != kNT;
-  static constexpr int kStep = F4 ? 256 : 64;  // elements of the sum
-  static constexpr int kTM = BM / WM / 16, kTN_ = BN / WN / 16;
+  static constexpr int kStep = F4 ? 128 : 32;  // elements of the sum
+  static constexpr int kS = F4 ? 32 : 16;  // of a matrix instruction
+  static constexpr int kKK = F4 ? 2 : 1;   // matrix instructions along the sum
+  typedef typename std::conditional<F4, f32x16, f32x4>::type Acc;
+  static constexpr int kTM = BM / WM / kS, kTN_ = BN / WN / kS;
   static constexpr int kColumns = Epi == Epilogue::kGated ? BN / 2 : BN;  // of out (h)
   static constexpr int kLdsA = BM * kStepBytes, kLdsB = BN * kStepBytes;
-  static constexpr int kLdsScales = F4 ? (BM + BN) * 8 : 0;
-  static constexpr int kLds = kLdsA + kLdsB + kLdsScales;
+  static constexpr int kLds = kLdsA + kLdsB;
+  static constexpr int kLdsScales = F4 ? (BM + BN) * kScaleRow : 0;  // of kScaleSteps steps
   using PlaceA = Place<BM, kAcrossA, kThreads>;
   using PlaceB = Place<BN, kAcrossB, kThreads>;
 
@@ -234,183 +256,216 @@ struct Tile {
     return r < kColumns ? c : (int64_t)a.n + c;
   }
 
-  // First row of b's tile that matrix fragment j of wave column wn covers.
-  static __device__ __forceinline__ int b_frag(int wn, int j) {
-    if (Epi != Epilogue::kGated) return wn * (BN / WN) + 16 * j;
-    constexpr int half = kTN_ / 2;
-    return (j < half ? 0 : kColumns) + wn * (kColumns / WN) + 16 * (j % half);
-  }
-  static __device__ __forceinline__ int out_column(int wn, int j) {  // j < kTN_ / 2 when gated
-    return Epi == Epilogue::kGated ? wn * (kColumns / WN) + 16 * j : wn * (BN / WN) + 16 * j;
+  static constexpr int kWaveColumns = kColumns / WN;  // columns of out of a wave
+  // Row (column) of b's tile where fragment j begins, without the wave's first; gated: up fragments behind the gate's.
+  static constexpr int b_frag(int j) {
+    return Epi == Epilogue::kGated && j >= kTN_ / 2 ? kColumns + kS * (j - kTN_ / 2) : kS * j;
   }
 
-  // Fragment of an operand whose rows run along the sum: row r0 + lane % 16, chunk
-  // kk * 4 + lane / 16 (MXFP4: lane / 16 * 2 + kk, so that a lane's two scales are neighbours).
-  static __device__ __forceinline__ u32x4 read_along(const uint8_t *lds, int r0, int kk) {
-    const int lane = threadIdx.x & 63, g = lane >> 4;
-    const int chunk = (F4 ? g * 2 + kk : kk * 4 + g) ^ (lane & 7);
-    return *(const u32x4 *)(lds + (r0 + (lane & 15)) * kStepBytes + chunk * 16);
+  // Where a lane reads its part of the wave's first fragments (bytes into a step's operands). The lanes' part p = lane / kS takes
+  // chunk p of the sum (MXFP4: chunks 2 p and 2 p + 1, one for each matrix instruction). Fragment i of rows that run along the
+  // sum lies kS i rows on: row r0 + lane % kS, the other chunk in the neighbouring slot. Across: columns c0 .. c0 + 15; the
+  // swizzle moves chunks within 16, so that fragment i is found by an exclusive or.
+  struct Lane {
+    uint32_t a, b, sa, sb;
+  };
+  static __device__ __forceinline__ uint32_t lane_along(int r0) {
+    const uint32_t lane = threadIdx.x & 63;
+    return (r0 + lane % kS) * kStepBytes + ((lane / kS * kKK) ^ (lane >> 1 & 3)) * 16;
   }
-  // Fragment of one whose rows run across: columns c0 .. c0 + 15, the same places of the sum.
+  template <int N, int Each>
+  static __device__ __forceinline__ uint32_t lane_across(int c0) {
+    static_assert(kS == 16 && (Each == 64 || Each == 128), "a wave's columns do not carry into the swizzle");
+    const uint32_t lane = threadIdx.x & 63, i = lane & 15, k = (lane >> 4) * 8 + (i >> 2);
+    return k * (2 * N) + ((c0 / 8 + (i >> 1 & 1)) ^ swizzle(k)) * 16 + (i & 1) * 8;  // swizzle(k + 4) is the same
+  }
+  static __device__ __forceinline__ Lane lane_of(int wm, int wn) {
+    const uint32_t lane = threadIdx.x & 63, scale = lane % kS * kScaleRow + lane / kS * kKK;
+    const int r0 = wm * (BM / WM), c0 = wn * kWaveColumns;
+    Lane l;
+    if constexpr (kAcrossA) l.a = lane_across<BM, BM / WM>(r0);
+    else l.a = lane_along(r0);
+    if constexpr (kAcrossB) l.b = lane_across<BN, BN / WN>(c0) + kLdsA;
+    else l.b = lane_along(c0) + kLdsA;
+    l.sa = r0 * kScaleRow + scale;
+    l.sb = (BM + c0) * kScaleRow + scale;
+    return l;
+  }
+
+  typedef __attribute__((address_space(3))) const u32x4 lds_u32x4;
+  typedef __attribute__((address_space(3))) const uint16_t lds_u16;
+  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
   template <int N>
-  static __device__ __forceinline__ u32x4 read_across(const uint8_t *lds, int c0, int kk) {
-    const int lane = threadIdx.x & 63, g = lane >> 4, i = lane & 15;
-    const uint32_t k = kk * 32 + g * 8 + (i >> 2);
-    const uint32_t slot = (uint32_t)(c0 / 8 + ((i & 3) >> 1)) ^ swizzle(k);  // swizzle(k + 4) is the same
-    const uint8_t *p = lds + k * (2 * N) + slot * 16 + (i & 1) * 8;
-    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p));
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 4 * 2 * N));
+  static __device__ __forceinline__ u32x4 read_across(uint32_t at) {
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(uintptr_t)at);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(uintptr_t)(at + 4 * 2 * N));
     u32x4 v;
     __builtin_memcpy(&v, &lo, 8);
     __builtin_memcpy((char *)&v + 8, &hi, 8);
     return v;
   }
 
-  static __device__ __forceinline__ f32x4 multiply(u32x4 b, u32x4 a, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a), c, 0, 0, 0);
-  }
-  template <int Kk>
-  static __device__ __forceinline__ f32x4 multiply_f4(u32x4 b, u32x4 a, f32x4 c, uint32_t sb, uint32_t sa) {
-    const i32x8 vb = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
-    const i32x8 va = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(vb, va, c, 4, 4, Kk, (int)sb, Kk, (int)sa);
-  }
+  // A wave's share of a step's operands, in registers.
+  struct Fragments {
+    u32x4 a[kTM][kKK], b[kTN_][kKK];
+    uint32_t sa[F4 ? kTM : 1], sb[F4 ? kTN_ : 1];  // scales, two to a register
+  };
 
-  // Adds one step to the sums. `blocks`: scale blocks of the row that this step still has (MXFP4).
-  static __device__ __forceinline__ void step(const uint8_t *lds, int wm, int wn, int blocks, f32x4 (&acc)[kTM][kTN_]) {
-    const uint8_t *la = lds, *lb = lds + kLdsA;
-    if constexpr (F4) {
-      const int lane = threadIdx.x & 63, g = lane >> 4;
-      const uint8_t *sa = lds + kLdsA + kLdsB + (lane & 15) * 8 + g * 2, *sb = sa + BM * 8;
-      // scales behind the row's last block may be anything, NaN among it
-      const uint32_t keep = 2 * g + 1 < blocks ? 0xFFFFu : 2 * g < blocks ? 0xFFu : 0u;
-      uint32_t xa[kTM], xb[kTN_];
+  // Where a step's operands and scales lie in shared memory. keep: mask of the lane's scales that are the row's (what is
+  // behind them may be anything, NaN among it).
+  struct From {
+    uint32_t operands, scales, keep;
+  };
+  static __device__ __forceinline__ void read_a(const From &from, const Lane &l, int i, int kk, Fragments &f) {
+    if constexpr (kAcrossA) f.a[i][kk] = read_across<BM>(from.operands + (l.a ^ (uint32_t)(2 * kS * i)));
+    else f.a[i][kk] = *(lds_u32x4 *)(uintptr_t)(from.operands + (l.a ^ 16u * kk) + kS * i * kStepBytes);
+    if constexpr (F4)
+      if (kk == kKK - 1) f.sa[i] = *(lds_u16 *)(uintptr_t)(from.scales + l.sa + kS * kScaleRow * i) & from.keep;
+  }
+  static __device__ __forceinline__ void read_b(const From &from, const Lane &l, int j, int kk, Fragments &f) {
+    if constexpr (kAcrossB) f.b[j][kk] = read_across<BN>(from.operands + (l.b ^ (uint32_t)(2 * kS * j)));
+    else f.b[j][kk] = *(lds_u32x4 *)(uintptr_t)(from.operands + (l.b ^ 16u * kk) + b_frag(j) * kStepBytes);
+    if constexpr (F4)
+      if (kk == kKK - 1) f.sb[j] = *(lds_u16 *)(uintptr_t)(from.scales + l.sb + kScaleRow * b_frag(j)) & from.keep;
+  }
+  static __device__ __forceinline__ void read(const From &from, const Lane &l, Fragments &f) {
 #pragma unroll
-      for (int i = 0; i < kTM; ++i) xa[i] = *(const uint16_t *)(sa + (wm * (BM / WM) + 16 * i) * 8) & keep;
+    for (int kk = 0; kk < kKK; ++kk) {
 #pragma unroll
-      for (int j = 0; j < kTN_; ++j) xb[j] = *(const uint16_t *)(sb + b_frag(wn, j) * 8) & keep;
-      half_f4<0>(la, lb, wm, wn, xa, xb, acc);
-      half_f4<1>(la, lb, wm, wn, xa, xb, acc);
-    } else {
+      for (int j = 0; j < kTN_; ++j) read_b(from, l, j, kk, f);
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        u32x4 fa[kTM], fb[kTN_];
-#pragma unroll
-        for (int i = 0; i < kTM; ++i) {
-          const int r0 = wm * (BM / WM) + 16 * i;
-          fa[i] = kAcrossA ? read_across<BM>(la, r0, kk) : read_along(la, r0, kk);
-        }
-#pragma unroll
-        for (int j = 0; j < kTN_; ++j) fb[j] = kAcrossB ? read_across<BN>(lb, b_frag(wn, j), kk) : read_along(lb, b_frag(wn, j), kk);
-#pragma unroll
-        for (int i = 0; i < kTM; ++i)
-#pragma unroll
-          for (int j = 0; j < kTN_; ++j) acc[i][j] = multiply(fb[j], fa[i], acc[i][j]);
-      }
+      for (int i = 0; i < kTM; ++i) read_a(from, l, i, kk, f);
     }
   }
-  template <int Kk>
-  static __device__ __forceinline__ void half_f4(const uint8_t *la, const uint8_t *lb, int wm, int wn, const uint32_t (&xa)[kTM],
-                                                 const uint32_t (&xb)[kTN_], f32x4 (&acc)[kTM][kTN_]) {
-    u32x4 fa[kTM], fb[kTN_];
+  // `left`: scale blocks of the row from this step's first on.
+  static __device__ __forceinline__ uint32_t scales_kept(int64_t left) {
+    const int first = (threadIdx.x & 63) / kS * kKK;
+    return first + 1 < left ? 0xFFFFu : first < left ? 0xFFu : 0u;
+  }
+
+  // Row i of the products with chunk kk, a's fragment from fa and b's from fb.
+  template <int kk>
+  static __device__ __forceinline__ void multiply(const Fragments &fa, const Fragments &fb, int i, Acc (&acc)[kTM][kTN_]) {
 #pragma unroll
-    for (int i = 0; i < kTM; ++i) fa[i] = read_along(la, wm * (BM / WM) + 16 * i, Kk);
-#pragma unroll
-    for (int j = 0; j < kTN_; ++j) fb[j] = read_along(lb, b_frag(wn, j), Kk);
-#pragma unroll
-    for (int i = 0; i < kTM; ++i)
-#pragma unroll
-      for (int j = 0; j < kTN_; ++j) acc[i][j] = multiply_f4<Kk>(fb[j], fa[i], acc[i][j], xb[j], xa[i]);
+    for (int j = 0; j < kTN_; ++j) {
+      const u32x4 x = fb.b[j][kk], y = fa.a[i][kk];
+      if constexpr (F4) {
+        // the codes are the lower half of the operand, the upper is not looked at
+        const i32x8 b = (i32x8)__builtin_shufflevector(x, x, 0, 1, 2, 3, -1, -1, -1, -1);
+        const i32x8 a = (i32x8)__builtin_shufflevector(y, y, 0, 1, 2, 3, -1, -1, -1, -1);
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, acc[i][j], 4, 4, kk, (int)fb.sb[j], kk, (int)fa.sa[i]);
+      } else {
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), acc[i][j], 0, 0, 0);
+      }
+    }
   }
 };
 
 // ------------------------------------------------------------------ results
-__device__ __forceinline__ void store4(uint64_t out, int64_t at, f32x4 v, int n, bool f32, bool wide) {
-  if (f32) {
-    float *p = (float *)(uintptr_t)out + at;
-    if (wide && n >= 4) {
-      *(f32x4 *)p = v;
-    } else {
+// Of eight neighbouring columns `n` exist; `wide`: eight can be stored at once.
+template <class V>
+__device__ __forceinline__ void store8(uint64_t out, int64_t at, const float (&v)[8], int n, bool wide) {
+  V *p = (V *)(uintptr_t)out + at;
+  if (wide && n >= 8) {
+    typedef V V8 __attribute__((ext_vector_type(8)));
+    V8 r;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < n) p[i] = v[i];
-    }
-    return;
-  }
-  __bf16 *p = (__bf16 *)(uintptr_t)out + at;
-  const bf16x4 r = {(__bf16)v.x, (__bf16)v.y, (__bf16)v.z, (__bf16)v.w};
-  if (wide && n >= 4) {
-    *(bf16x4 *)p = r;
+    for (int i = 0; i < 8; ++i) r[i] = (V)v[i];
+    *(V8 *)p = r;
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < n) p[i] = r[i];
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = (V)v[i];
   }
 }
 
-__device__ __forceinline__ f32x4 load_pre(uint64_t pre, int64_t at, int n, bool wide) {
+__device__ __forceinline__ void load_pre(uint64_t pre, int64_t at, int n, bool wide, float (&v)[8]) {
   const __bf16 *p = (const __bf16 *)(uintptr_t)pre + at;
-  f32x4 v = {0, 0, 0, 0};
-  if (wide && n >= 4) {
-    const bf16x4 r = *(const bf16x4 *)p;
+  if (wide && n >= 8) {
+    const bf16x8 r = *(const bf16x8 *)p;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = (float)r[i];
+    for (int i = 0; i < 8; ++i) v[i] = (float)r[i];
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < n) v[i] = (float)p[i];
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? (float)p[i] : 0.0f;
   }
-  return v;
 }
 
-// What becomes of four neighbouring sums of one row: `row` of out, `column` of out (h), n of them exist.
+// What becomes of eight neighbouring sums of one row: `row` of out, `column` of out (h), n of them exist.
 template <Epilogue Epi>
-__device__ __forceinline__ void finish4(const ProductArgs &a, uint64_t out, int64_t row, int column, int n, f32x4 s, f32x4 up) {
+__device__ __forceinline__ void finish8(const ProductArgs &a, uint64_t out, int64_t row, int column, int n, const float (&s)[8],
+                                        const float (&up)[8]) {
   const bool wide = a.out_wide;
   if (Epi == Epilogue::kPlain) {
-    store4(out, row * a.out_stride + column, s, n, a.out_f32, wide);
+    if (a.out_f32) store8<float>(out, row * a.out_stride + column, s, n, wide);
+    else store8<__bf16>(out, row * a.out_stride + column, s, n, wide);
   } else if (Epi == Epilogue::kGated) {
     if (a.pre) {
-      store4(a.pre, row * a.pre_stride + column, s, n, false, wide);
-      store4(a.pre, row * a.pre_stride + a.n + column, up, n, false, wide);
+      store8<__bf16>(a.pre, row * a.pre_stride + column, s, n, wide);
+      store8<__bf16>(a.pre, row * a.pre_stride + a.n + column, up, n, wide);
     }
-    f32x4 h;
+    float h[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = activation(a.act, s[i]).value * up[i];
-    store4(out, row * a.out_stride + column, h, n, false, wide);
+    for (int i = 0; i < 8; ++i) h[i] = activation(a.act, s[i]).value * up[i];
+    store8<__bf16>(out, row * a.out_stride + column, h, n, wide);
   } else {
-    const f32x4 g = load_pre(a.pre, row * a.pre_stride + column, n, wide);
-    const f32x4 u = load_pre(a.pre, row * a.pre_stride + a.n + column, n, wide);
-    f32x4 dg, du;
+    float g[8], u[8], dg[8], du[8];
+    load_pre(a.pre, row * a.pre_stride + column, n, wide, g);
+    load_pre(a.pre, row * a.pre_stride + a.n + column, n, wide, u);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
       const Act t = activation(a.act, g[i]);
       dg[i] = s[i] * u[i] * t.slope;
       du[i] = s[i] * t.value;
     }
-    store4(out, row * a.out_stride + column, dg, n, false, wide);
-    store4(out, row * a.out_stride + a.n + column, du, n, false, wide);
+    store8<__bf16>(out, row * a.out_stride + column, dg, n, wide);
+    store8<__bf16>(out, row * a.out_stride + a.n + column, du, n, wide);
   }
 }
 
-template <int Form, Epilogue Epi, bool F4, int BM, int BN, int WM, int WN, int TM, int TN>
+// Eight neighbouring columns of a lane's row out of two fours of neighbouring columns, by exchange with another lane.
+// 16 x 16: lane group g = lane / 16 has columns 4 g .. of fragments x and y; the even groups get 4 g .. + 7 of x, the odd ones
+// 4 (g - 1) .. + 7 of y. 32 x 32: half h has columns 4 h .. of x and 8 + 4 h .. of the same fragment as y, and gets 8 h .. + 7.
+template <int S, class V>
+__device__ __forceinline__ void eight(const V &x, int x0, const V &y, int y0, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t p = __float_as_uint(x[x0 + i]), q = __float_as_uint(y[y0 + i]);
+    const auto r = S == 16 ? __builtin_amdgcn_permlane16_swap(p, q, false, false) : __builtin_amdgcn_permlane32_swap(p, q, false, false);
+    v[i] = __uint_as_float(r[0]);
+    v[4 + i] = __uint_as_float(r[1]);
+  }
+}
+
+template <int Form, Epilogue Epi, bool F4, int BM, int BN, int WM, int WN, class Acc, int TM, int TN>
 __device__ __forceinline__ void finish_tile(const ProductArgs &a, const Rows &r, int m0, int n0, int m_left, int wm, int wn,
-                                            const f32x4 (&acc)[TM][TN]) {
+                                            const Acc (&acc)[TM][TN]) {
   using T = Tile<Form, Epi, F4, BM, BN, WM, WN>;
-  const int lane = threadIdx.x & 63;
+  constexpr int S = T::kS;
+  const int lane = threadIdx.x & 63, g = lane / S;
   const uint64_t out = a.out + (Form == kTN ? (uint64_t)(a.out_expert * r.expert) * (a.out_f32 ? 4 : 2) : 0);
   constexpr int kCols = Epi == Epilogue::kGated ? TN / 2 : TN;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
-    const int row = wm * (BM / WM) + 16 * i + (lane & 15);
-    if (row >= m_left) continue;
+    const int row = wm * (BM / WM) + S * i + lane % S;
 #pragma unroll
-    for (int j = 0; j < kCols; ++j) {
-      const int column = n0 + T::out_column(wn, j) + 4 * (lane >> 4);
-      if (column < a.n)
-        finish4<Epi>(a, out, (Form == kTN ? 0 : r.first) + m0 + row, column, a.n - column, acc[i][j],
-                     Epi == Epilogue::kGated ? acc[i][j + kCols] : acc[i][j]);
+    for (int p = 0; p < kCols * S / 16; p += 2) {  // 32 columns
+      constexpr int kUp = Epi == Epilogue::kGated ? kCols : 0;
+      const int x = p * 16 / S, y = (p + 1) * 16 / S;
+#pragma unroll
+      for (int half = 0; half < S / 16; ++half) {
+        const int column = n0 + wn * T::kWaveColumns + 16 * p + (S == 16 ? 16 * (g & 1) + 8 * (g >> 1) : 16 * half + 8 * g);
+        float s[8], up[8];
+        if constexpr (S == 16) {
+          eight<S>(acc[i][x], 0, acc[i][y], 0, s);
+          if (kUp) eight<S>(acc[i][x + kUp], 0, acc[i][y + kUp], 0, up);
+        } else {
+          eight<S>(acc[i][x], 8 * half, acc[i][x], 8 * half + 4, s);
+          if (kUp) eight<S>(acc[i][x + kUp], 8 * half, acc[i][x + kUp], 8 * half + 4, up);
+        }
+        if (row < m_left && column < a.n)
+          finish8<Epi>(a, out, (Form == kTN ? 0 : r.first) + m0 + row, column, a.n - column, s, up);
+      }
     }
   }
 }
@@ -421,7 +476,7 @@ __device__ __forceinline__ void finish_tile(const ProductArgs &a, const Rows &r,
 template <int Form, Epilogue Epi, bool F4, int BM, int BN, int WM, int WN>
 __global__ void __launch_bounds__(64 * WM * WN) product_any_kernel(ProductArgs a) {
   using T = Tile<Form, Epi, F4, BM, BN, WM, WN>;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2][T::kLds];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2][T::kLds + T::kLdsScales];
   Rows r;
   int mt, nt;
   const uint32_t n_tiles = (uint32_t)(a.n + T::kColumns - 1) / T::kColumns;
@@ -435,7 +490,7 @@ __global__ void __launch_bounds__(64 * WM * WN) product_any_kernel(ProductArgs a
   const uint64_t b_base = a.b + (Form == kTN ? 0 : (uint64_t)(a.b_expert * r.expert));
 
   u32x4 ra[T::PlaceA::kEach], rb[T::PlaceB::kEach];
-  uint32_t rs[F4 ? 2 : 1] = {};
+  uint32_t rs = 0;
   auto gathered = [&](int64_t row) -> int64_t {  // a row of the row space to one of the operand, -1: zeros
     if (!a.row_index) return row;
     const int64_t i = a.row_index[row];
@@ -480,20 +535,18 @@ __global__ void __launch_bounds__(64 * WM * WN) product_any_kernel(ProductArgs a
         }
       }
     }
-    if constexpr (F4) {  // the scales of two rows' four blocks
-      static_assert(!F4 || (BM + BN) * 2 == 2 * T::kThreads, "two words of scales to a thread");
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int word = tid + i * T::kThreads, row = word >> 1;
-        const int64_t at = k0 / 32 + 4 * (word & 1);
-        rs[i] = 0;
-        if (at >= (a.k + 31) / 32) continue;
+    if constexpr (F4) {  // the scales of a row's four blocks
+      static_assert(!F4 || BM + BN == T::kThreads, "one word of scales to a thread");
+      const int row = tid;
+      const int64_t at = k0 / 32;
+      rs = 0;
+      {
         if (row < BM) {
-          if (row < m_left) rs[i] = *(const uint32_t *)(uintptr_t)(a.a_scales + (uint64_t)((r.first + m0 + row) * a.a_scale_stride + at));
+          if (row < m_left) rs = *(const uint32_t *)(uintptr_t)(a.a_scales + (uint64_t)((r.first + m0 + row) * a.a_scale_stride + at));
         } else {
           bool ok;
           const int64_t s = T::b_row(a, n0, row - BM, ok);
-          if (ok) rs[i] = *(const uint32_t *)(uintptr_t)(a.b_scales + (uint64_t)(a.b_scale_expert * r.expert + s * a.b_scale_stride + at));
+          if (ok) rs = *(const uint32_t *)(uintptr_t)(a.b_scales + (uint64_t)(a.b_scale_expert * r.expert + s * a.b_scale_stride + at));
         }
       }
     }
@@ -503,17 +556,16 @@ __global__ void __launch_bounds__(64 * WM * WN) product_any_kernel(ProductArgs a
     for (int i = 0; i < T::PlaceA::kEach; ++i) *(u32x4 *)(to + 16 * (tid + i * T::kThreads)) = ra[i];
 #pragma unroll
     for (int i = 0; i < T::PlaceB::kEach; ++i) *(u32x4 *)(to + T::kLdsA + 16 * (tid + i * T::kThreads)) = rb[i];
-    if constexpr (F4) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) *(uint32_t *)(to + T::kLdsA + T::kLdsB + 4 * (tid + i * T::kThreads)) = rs[i];
-    }
+    if constexpr (F4) *(uint32_t *)(to + T::kLds + kScaleRow * tid) = rs;
   };
 
-  f32x4 acc[T::kTM][T::kTN_];
+  typename T::Acc acc[T::kTM][T::kTN_];
 #pragma unroll
   for (int i = 0; i < T::kTM; ++i)
 #pragma unroll
-    for (int j = 0; j < T::kTN_; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    for (int j = 0; j < T::kTN_; ++j) acc[i][j] = typename T::Acc{};
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)&lds[0][0];
+  const typename T::Lane lane = T::lane_of(wm, wn);
   if (K > 0) {
     load(0);
     store(lds[0]);
@@ -522,7 +574,13 @@ __global__ void __launch_bounds__(64 * WM * WN) product_any_kernel(ProductArgs a
     for (int64_t k0 = 0; k0 < K; k0 += T::kStep, at ^= 1) {
       const bool more = k0 + T::kStep < K;
       if (more) load(k0 + T::kStep);
-      T::step(lds[at], wm, wn, F4 ? (int)((a.k - k0 + 31) / 32) : 0, acc);
+      typename T::Fragments f;
+      const uint32_t from = lds0 + at * (T::kLds + T::kLdsScales);
+      T::read({from, from + T::kLds, T::scales_kept((a.k - k0 + 31) / 32)}, lane, f);
+      static_for<T::kKK>([&](auto half) {
+#pragma unroll
+        for (int i = 0; i < T::kTM; ++i) T::template multiply<decltype(half)::value>(f, f, i, acc);
+      });
       if (more) store(lds[at ^ 1]);
       __syncthreads();
     }
@@ -538,42 +596,49 @@ __global__ void __launch_bounds__(64 * WM * WN) product_any_kernel(ProductArgs a
 // memory: rows behind the last, and offsets set to kNowhere.
 constexpr uint32_t kNowhere = 0x80000000u;
 
-// The compiler does not count these loads: wait_and_meet() waits for all of them.
+// The compiler does not count these loads: wait_and_meet() waits for them.
+template <int Add>
 __device__ __forceinline__ void copy16(u32x4 buffer, uint32_t lds, uint32_t offset) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(buffer) : "memory");
+  asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(buffer), "n"(Add) : "memory", "scc");
 }
+template <int Add>
 __device__ __forceinline__ void copy4(u32x4 buffer, uint32_t lds, uint32_t offset) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(buffer) : "memory");
+  asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(buffer), "n"(Add) : "memory", "scc");
 }
 
-// What this wave copied has arrived and what it read has been read; then the workgroup meets.
-__device__ __forceinline__ void wait_and_meet() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+// All but the last `Pending` of this wave's copies have arrived and what it read has been read; then the workgroup meets.
+template <int Pending>
+__device__ __forceinline__ void wait_and_meet() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(Pending) : "memory");
+}
 
-// A window over an operand that moves along the sum; everything in it is uniform.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)x); }
+__device__ __forceinline__ uint64_t uniform(uint64_t x) { return (uint64_t)uniform((uint32_t)(x >> 32)) << 32 | uniform((uint32_t)x); }
+
+// What a step copies of an operand: `bytes` from `base` on, `last_bytes` in the last step.
 struct Window {
   uint64_t base;
-  int64_t bytes;  // from base to the operand's end
-  __device__ __forceinline__ u32x4 buffer() const {
-    const int64_t n = bytes < 0 ? 0 : bytes < 0x7FFFFFF0 ? bytes : 0x7FFFFFF0;
-    u32x4 r;
-    r.x = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)base);
-    r.y = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(base >> 32)) & 0xFFFFu;
-    r.z = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)n);
-    r.w = 0x00020000u;
-    return r;
-  }
-  __device__ __forceinline__ void move(int64_t by) {
-    base += (uint64_t)by;
-    bytes -= by;
+  uint32_t move;  // bytes from step to step
+  uint32_t bytes, last_bytes;
+  __device__ __forceinline__ u32x4 buffer(bool last) const {
+    return u32x4{(uint32_t)base, (uint32_t)(base >> 32), last ? last_bytes : bytes, 0x00020000u};
   }
 };
 
-template <int Form, Epilogue Epi, bool F4, int BM, int BN, int WM, int WN>
+__device__ __forceinline__ Window window(uint64_t base, int64_t move, int64_t bytes, int64_t last_bytes) {
+  // (an operand without rows has less than no bytes)
+  return {uniform(base), uniform((uint32_t)move), uniform((uint32_t)max(bytes, (int64_t)0)), uniform((uint32_t)max(last_bytes, (int64_t)0))};
+}
+
+constexpr int kStages = 4;
+
+// Indexed: rows along the sum (b of TN) are taken through row_index.
+template <int Form, Epilogue Epi, bool F4, int BM, int BN, int WM, int WN, bool Indexed>
 __global__ void __launch_bounds__(64 * WM * WN, 2) product_kernel(ProductArgs a) {
   using T = Tile<Form, Epi, F4, BM, BN, WM, WN>;
   using PA = typename T::PlaceA;
   using PB = typename T::PlaceB;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2][T::kLds];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kStages * T::kLds + 2 * T::kLdsScales];
   Rows r;
   int mt, nt;
   const uint32_t n_tiles = (uint32_t)(a.n + T::kColumns - 1) / T::kColumns;
@@ -583,10 +648,14 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) product_kernel(ProductArgs a)
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WN, wn = wave % WN;
   const int m0 = mt * BM, n0 = nt * T::kColumns;
   const int m_left = (Form == kTN ? a.m : r.count) - m0;
-  // bytes of a row along the sum, or rows across it
-  const int64_t row_bytes = F4 ? (int64_t)(a.k + 31) / 32 * 16 : 2 * (int64_t)a.k;
   const int64_t K = Form == kTN ? r.count : a.k;
+  constexpr int kCopies = PA::kEach + PB::kEach;  // of a thread and step (scales come on top now and then)
   const int steps = (int)((K + T::kStep - 1) / T::kStep);
+
+  // Along the sum: bytes of a row that the last step has. Across it: rows.
+  const int64_t row_bytes = F4 ? (int64_t)(a.k + 31) / 32 * 16 : 2 * (int64_t)a.k;
+  const int last_bytes = (int)(row_bytes - (int64_t)(steps - 1) * kStepBytes);
+  const int last_rows = (int)(K - (int64_t)(steps - 1) * T::kStep);
 
   Window wa, wb;
   uint32_t oa[PA::kEach], ob[PB::kEach];
@@ -594,30 +663,34 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) product_kernel(ProductArgs a)
     const int64_t i = a.row_index[row];
     return i >= 0 && i < a.n_index_rows ? (uint32_t)i : kNowhere;
   };
-  const bool gather_a = Form != kTN && !F4 && a.row_index, gather_b = Form == kTN && a.row_index;
   if (T::kAcrossA) {
-    wa = {a.a + (uint64_t)(r.first * a.a_stride + 2 * (int64_t)m0), (K - 1) * a.a_stride + 2 * (int64_t)(a.m - m0)};
-  } else if (gather_a) {
-    wa = {a.a, (a.n_index_rows - 1) * a.a_stride + row_bytes};
+    const int64_t width = 2 * (int64_t)min(a.m - m0, BM);
+    wa = window(a.a + (uint64_t)(r.first * a.a_stride + 2 * (int64_t)m0), T::kStep * a.a_stride, (T::kStep - 1) * a.a_stride + width,
+                (last_rows - 1) * a.a_stride + width);
   } else {
-    wa = {a.a + (uint64_t)((r.first + m0) * a.a_stride), (int64_t)(m_left - 1) * a.a_stride + row_bytes};
+    const bool gather = !F4 && a.row_index;
+    const int64_t before = (gather ? a.n_index_rows - 1 : min(m_left, BM) - 1) * a.a_stride;
+    wa = window(a.a + (uint64_t)(gather ? 0 : (r.first + m0) * a.a_stride), kStepBytes, before + kStepBytes, before + last_bytes);
   }
 #pragma unroll
   for (int i = 0; i < PA::kEach; ++i) {
     int row, chunk;
     PA::source(tid + i * T::kThreads, row, chunk);
     uint32_t at = (uint32_t)row;
-    if (gather_a) at = row < m_left ? index_of(r.first + m0 + row) : kNowhere;
+    if (!T::kAcrossA && !F4 && a.row_index) at = row < m_left ? index_of(r.first + m0 + row) : kNowhere;
     oa[i] = at == kNowhere ? kNowhere : at * (uint32_t)a.a_stride + 16u * chunk;
   }
   const uint64_t b_base = a.b + (Form == kTN ? 0 : (uint64_t)(a.b_expert * r.expert));
   if (T::kAcrossB) {
-    const int64_t rows = gather_b ? a.n_index_rows : K;
-    wb = {b_base + (uint64_t)((Form == kTN && !gather_b ? r.first * a.b_stride : 0) + 2 * (int64_t)n0),
-          (rows - 1) * a.b_stride + 2 * (int64_t)(a.n - n0)};
+    const int64_t width = 2 * (int64_t)min(a.n - n0, BN);
+    const uint64_t base = b_base + (uint64_t)((Form == kTN && !Indexed ? r.first * a.b_stride : 0) + 2 * (int64_t)n0);
+    const int64_t all = (a.n_index_rows - 1) * a.b_stride + width;
+    wb = Indexed ? window(base, 0, all, all)
+                 : window(base, T::kStep * a.b_stride, (T::kStep - 1) * a.b_stride + width, (last_rows - 1) * a.b_stride + width);
   } else {
-    const int64_t rows = Epi == Epilogue::kGated ? 2 * (int64_t)a.n : a.n;
-    wb = {b_base + (uint64_t)(n0 * a.b_stride), (rows - n0 - 1) * a.b_stride + row_bytes};
+    // gated: the up rows lie a.n rows behind the gate rows
+    const int64_t before = (Epi == Epilogue::kGated ? a.n + min(a.n - n0, T::kColumns) - 1 : min(a.n - n0, BN) - 1) * a.b_stride;
+    wb = window(b_base + (uint64_t)(n0 * a.b_stride), kStepBytes, before + kStepBytes, before + last_bytes);
   }
 #pragma unroll
   for (int i = 0; i < PB::kEach; ++i) {
@@ -626,81 +699,132 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) product_kernel(ProductArgs a)
     if (Epi == Epilogue::kGated && row >= T::kColumns) row += a.n - T::kColumns;  // up rows
     ob[i] = (uint32_t)row * (uint32_t)a.b_stride + 16u * chunk;
   }
-  uint32_t next_row[PB::kEach];  // of b, gathered: one step ahead
-  auto load_rows = [&](int step) {
+  auto load_rows = [&](int step) {  // Indexed: one step ahead
 #pragma unroll
     for (int i = 0; i < PB::kEach; ++i) {
       int row, chunk;
       PB::source(tid + i * T::kThreads, row, chunk);
       const int64_t k = (int64_t)step * T::kStep + row;
-      next_row[i] = k < K ? index_of(r.first + k) : kNowhere;
+      const uint32_t at = k < K ? index_of(r.first + k) : kNowhere;
+      ob[i] = at == kNowhere ? kNowhere : at * (uint32_t)a.b_stride + 16u * chunk;
     }
   };
-  if (gather_b && steps > 0) load_rows(0);
+  if (Indexed && steps > 0) load_rows(0);
 
-  Window sa{}, sb{};
-  uint32_t osa = 0, osb = 0;
-  static_assert(!F4 || (BM * 2 == T::kThreads && BN * 2 == T::kThreads), "one word of scales to a thread");
+  // Scales: the first waves copy those of a's rows, the others those of b's, a row of kScaleSteps steps to a thread.
+  Window ws{};
+  uint32_t os = 0;
+  static_assert(!F4 || (BM + BN == T::kThreads && BM % 64 == 0), "a row of scales to a thread");
+  const int blocks = (a.k + 31) / 32, last_scales = (steps - 1) / kScaleSteps * kScaleSteps;
   if (F4) {
-    const int64_t nb = (a.k + 31) / 32, words = (nb + 3) / 4 * 4;
-    sa = {a.a_scales + (uint64_t)((r.first + m0) * a.a_scale_stride), (int64_t)(m_left - 1) * a.a_scale_stride + words};
-    const int64_t rows = Epi == Epilogue::kGated ? 2 * (int64_t)a.n : a.n;
-    sb = {a.b_scales + (uint64_t)(a.b_scale_expert * r.expert + n0 * a.b_scale_stride), (rows - n0 - 1) * a.b_scale_stride + words};
-    int row = tid >> 1;
-    osa = (uint32_t)row * (uint32_t)a.a_scale_stride + 4u * (tid & 1);
-    if (Epi == Epilogue::kGated && row >= T::kColumns) row += a.n - T::kColumns;
-    osb = (uint32_t)row * (uint32_t)a.b_scale_stride + 4u * (tid & 1);
+    const bool of_a = wave < BM / 64;
+    const int64_t stride = of_a ? a.a_scale_stride : a.b_scale_stride;
+    int row = of_a ? tid : tid - BM;
+    const int64_t rows = of_a ? min(m_left, BM) : Epi == Epilogue::kGated ? a.n + min(a.n - n0, T::kColumns) : min(a.n - n0, BN);
+    if (!of_a && Epi == Epilogue::kGated && row >= T::kColumns) row += a.n - T::kColumns;
+    ws = window(of_a ? a.a_scales + (uint64_t)((r.first + m0) * stride) : a.b_scales + (uint64_t)(a.b_scale_expert * r.expert + n0 * stride),
+                kScaleRow, (rows - 1) * stride + kScaleRow, (rows - 1) * stride + (blocks + 3) / 4 * 4 - 4 * last_scales);
+    os = (uint32_t)row * (uint32_t)stride;
   }
 
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)&lds[0][0] + 1024u * wave;
-  auto fetch = [&](int step) {
-    const uint32_t to = lds0 + (step & 1) * T::kLds;
-    const u32x4 ba = wa.buffer(), bb = wb.buffer();
-    // the row's end lies within the last step: chunks behind it are not the next row's
-    const int64_t left = row_bytes - (int64_t)step * kStepBytes;
-    const bool cut = left < kStepBytes;
-#pragma unroll
-    for (int i = 0; i < PA::kEach; ++i) {
-      uint32_t at = oa[i];
-      if (!T::kAcrossA && cut) {
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)&lds[0];
+  // One of a step's copies; the last step's rows along the sum may end before its 64 bytes.
+  auto copy = [&](auto piece, int step, bool last) {
+    constexpr int p = decltype(piece)::value;
+    const uint32_t to = uniform(lds0 + (uint32_t)(step % kStages) * T::kLds + 1024u * wave);
+    if constexpr (p < PA::kEach) {
+      uint32_t at = oa[p];
+      if (!T::kAcrossA && last) {
         int row, chunk;
-        PA::source(tid + i * T::kThreads, row, chunk);
-        at = 16 * chunk < left ? at : kNowhere;
+        PA::source(tid + p * T::kThreads, row, chunk);
+        at = 16 * chunk < last_bytes ? at : kNowhere;
       }
-      copy16(ba, to + i * T::kThreads * 16, at);
-    }
-#pragma unroll
-    for (int i = 0; i < PB::kEach; ++i) {
+      copy16<p * T::kThreads * 16>(wa.buffer(last), to, at);
+    } else {
+      constexpr int i = p - PA::kEach;
       uint32_t at = ob[i];
-      int row, chunk;
-      PB::source(tid + i * T::kThreads, row, chunk);
-      if (!T::kAcrossB && cut) at = 16 * chunk < left ? at : kNowhere;
-      if (gather_b) at = next_row[i] == kNowhere ? kNowhere : next_row[i] * (uint32_t)a.b_stride + 16u * chunk;
-      copy16(bb, to + T::kLdsA + i * T::kThreads * 16, at);
+      if (!T::kAcrossB && last) {
+        int row, chunk;
+        PB::source(tid + i * T::kThreads, row, chunk);
+        at = 16 * chunk < last_bytes ? at : kNowhere;
+      }
+      copy16<T::kLdsA + i * T::kThreads * 16>(wb.buffer(last), to, at);
     }
-    wa.move(T::kAcrossA ? 64 * a.a_stride : kStepBytes);
-    if (!gather_b) wb.move(T::kAcrossB ? 64 * a.b_stride : kStepBytes);
-    if (F4) {
-      const uint32_t scales = to - 1024u * wave + T::kLdsA + T::kLdsB + 256u * wave;
-      copy4(sa.buffer(), scales, osa);
-      copy4(sb.buffer(), scales + BM * 8, osb);
-      sa.move(8);
-      sb.move(8);
-    }
-    if (gather_b && step + 1 < steps) load_rows(step + 1);
+  };
+  auto copy_scales = [&](int step) {  // a multiple of kScaleSteps
+    const uint32_t to = uniform(lds0 + (uint32_t)(step / kScaleSteps % 2) * T::kLdsScales + 1024u * wave);
+    copy16<kStages * T::kLds>(ws.buffer(step == last_scales), to, os);
+    ws.base += ws.move;
+  };
+  auto advance = [&](int step) {  // behind the copies of `step`
+    wa.base += wa.move;
+    wb.base += wb.move;
+    if (Indexed && step + 1 < steps) load_rows(step + 1);
   };
 
-  f32x4 acc[T::kTM][T::kTN_];
+  typename T::Acc acc[T::kTM][T::kTN_];
 #pragma unroll
   for (int i = 0; i < T::kTM; ++i)
 #pragma unroll
-    for (int j = 0; j < T::kTN_; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-  if (steps > 0) fetch(0);
-  for (int step = 0; step < steps; ++step) {
-    // this step's operands are there, and nobody reads the other half any more
-    wait_and_meet();
-    if (step + 1 < steps) fetch(step + 1);
-    T::step(lds[step & 1], wm, wn, F4 ? (a.k + 31) / 32 - 8 * step : 0, acc);
+    for (int j = 0; j < T::kTN_; ++j) acc[i][j] = typename T::Acc{};
+
+  // A step's products use fragments that were read during the step before; the copies run kStages - 1 steps ahead. a's first
+  // fragments are read again as soon as their row of products is through; b's, which every row needs, and a's last, which
+  // would be late, have registers for two steps.
+  const typename T::Lane lane = T::lane_of(wm, wn);
+  typename T::Fragments f[2];
+  constexpr int kLate = F4 ? 1 : 2, kOnce = T::kTM - kLate;
+  auto from_step = [&](int step, bool tail) -> typename T::From {
+    return {lds0 + (uint32_t)(step % kStages) * T::kLds,
+            lds0 + kStages * T::kLds + (uint32_t)(step / kScaleSteps % 2) * T::kLdsScales + step % kScaleSteps * 4,
+            tail ? T::scales_kept(blocks - 4 * step) : 0xFFFFu};
+  };
+  auto turn = [&](auto tail, int step, typename T::Fragments &now, typename T::Fragments &next) {
+    constexpr bool Tail = decltype(tail)::value;
+    // the next step's operands are there, and nobody reads this step's any more
+    if (!Tail || step + kStages <= steps) wait_and_meet<(kStages - 2) * kCopies>();
+    else wait_and_meet<0>();
+    const typename T::From from = from_step(step + 1, Tail);
+    const int ahead = step + kStages;
+    if (F4 && ahead % kScaleSteps == 0 && (!Tail || ahead < steps)) copy_scales(ahead);
+    constexpr int kRows = T::kKK * T::kTM;  // of products
+    static_for<kRows>([&](auto row) {
+      constexpr int u = decltype(row)::value, i = u % T::kTM, kk = u / T::kTM;
+      if constexpr (u < kLate * T::kKK) T::read_a(from, lane, kOnce + u / T::kKK, u % T::kKK, next);
+      static_for<T::kKK * T::kTN_>([&](auto col) {
+        constexpr int v = decltype(col)::value;
+        if constexpr (v * kRows / (T::kKK * T::kTN_) / 2 == u) T::read_b(from, lane, v % T::kTN_, v / T::kTN_, next);
+      });
+      if (!Tail || ahead < steps) static_for<kCopies>([&](auto piece) {
+          if constexpr (decltype(piece)::value * kRows / kCopies == u) copy(piece, ahead, Tail && ahead == steps - 1);
+        });
+      T::template multiply<kk>(i < kOnce ? f[0] : now, now, i, acc);
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (i < kOnce) T::read_a(from, lane, i, kk, f[0]);
+    });
+    if (!Tail || ahead < steps) advance(ahead);
+  };
+  if (steps > 0) {
+#pragma unroll 1
+    for (int i = 0; i < kStages && i < steps; ++i) {
+      if (F4 && i % kScaleSteps == 0) copy_scales(i);
+      static_for<kCopies>([&](auto piece) { copy(piece, i, i == steps - 1); });
+      advance(i);
+    }
+    if (steps >= kStages) wait_and_meet<(kStages - 1) * kCopies>();
+    else wait_and_meet<0>();
+    T::read(from_step(0, true), lane, f[0]);
+    int step = 0;
+#pragma unroll 1
+    for (; step + 1 + kStages < steps - 1; step += 2) {
+      turn(std::false_type(), step, f[0], f[1]);
+      turn(std::false_type(), step + 1, f[1], f[0]);
+    }
+#pragma unroll 1
+    for (; step < steps; step += 2) {
+      turn(std::true_type(), step, f[0], f[1]);
+      if (step + 1 < steps) turn(std::true_type(), step + 1, f[1], f[0]);
+    }
   }
   finish_tile<Form, Epi, F4, BM, BN, WM, WN>(a, r, m0, n0, m_left, wm, wn, acc);
 }

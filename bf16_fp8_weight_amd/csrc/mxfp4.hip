@@ -151,7 +151,7 @@ wt_status launch(const char *what, const ProductArgs &a, hipStream_t stream) {
   if (grid > kMaxGrid) return operator_fail(what, "too many tiles");
   if (grid == 0) return WT_OK;
   if constexpr (Near)
-    hipLaunchKernelGGL((product_kernel<kNT, Epi, true, BM, BN, WM, WN>), dim3((uint32_t)grid), dim3(64 * WM * WN), 0, stream, a);
+    hipLaunchKernelGGL((product_kernel<kNT, Epi, true, BM, BN, WM, WN, false>), dim3((uint32_t)grid), dim3(64 * WM * WN), 0, stream, a);
   else
     hipLaunchKernelGGL((product_any_kernel<kNT, Epi, true, BM, BN, WM, WN>), dim3((uint32_t)grid), dim3(64 * WM * WN), 0, stream, a);
   const hipError_t e = hipGetLastError();

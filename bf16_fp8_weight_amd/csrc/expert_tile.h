@@ -6,8 +6,8 @@
 // through shared memory in steps of 64 bytes along the sum (32 BF16 elements or
 // 128 MXFP4 codes), in 16-byte chunks:
 //   - an operand whose rows run along the sum (a and b of NT, a of NN) as its rows
-//     of 4 chunks, chunk c of row r at slot c ^ (r / 2 & 3), so that the 8 rows that
-//     are read in one cycle lie in different banks;
+//     of 4 chunks, chunk c of row r at slot c ^ swizzle_along(r), so that what is read
+//     in one cycle lies in different banks;
 //   - one whose rows run across it (b of NN, a and b of TN) as it comes, 32 rows of
 //     BM or BN elements, read back transposed (ds_read_b64_tr_b16: a 16-lane group
 //     fetches 4 rows x 16 columns, each lane receiving a column); there chunk c
@@ -107,90 +107,141 @@ __device__ __forceinline__ void expert_rows(const ProductArgs &a, int e, int &fi
   count = (int)max((int64_t)0, min(end, (int64_t)n_rows) - first);
 }
 
-__device__ __forceinline__ uint32_t wave_scan(uint32_t x) {  // inclusive, over 64 lanes
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint32_t y = __shfl_up(x, d);
-    if (lane >= d) x += y;
-  }
-  return x;
+template <int Ctrl, int RowMask>
+__device__ __forceinline__ uint32_t dpp_add(uint32_t x) {
+  return x + (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, Ctrl, RowMask, 0xF, false);
 }
+// Sums of a lane's value and those of the lanes before it, over the wave.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
+  x = dpp_add<0x111, 0xF>(x);  // row_shr:1, 2, 4, 8: within 16 lanes
+  x = dpp_add<0x112, 0xF>(x);
+  x = dpp_add<0x114, 0xF>(x);
+  x = dpp_add<0x118, 0xF>(x);
+  x = dpp_add<0x142, 0xA>(x);  // rows 1 and 3 take in the last lane of rows 0 and 2
+  return dpp_add<0x143, 0xC>(x);  // rows 2 and 3 that of row 1
+}
+__device__ __forceinline__ uint32_t last_lane(uint32_t x) { return (uint32_t)__builtin_amdgcn_readlane((int)x, 63); }
 
-// Tile t of the row tiles x column tiles of all experts, or false if there are
-// not that many. Workgroups go round the 8 XCDs, each with an L2 of its own: tiles are
-// dealt so that an XCD's are neighbours. Within an expert up to kRowGroup row tiles
-// take turns under one column tile, so that what the XCD's 32 CUs read at a time are few
-// rows of both operands.
+// Workgroups go round the 8 XCDs, each with an L2 of its own: tiles are dealt so that
+// an XCD's are neighbours. Up to kRowGroup row tiles take turns under one
+// column tile, so that what the XCD's 32 CUs read at a time are few rows of both operands.
 constexpr int kXcds = 8, kRowGroup = 8;
 
+// Place u among m_tiles x n_tiles tiles.
+__device__ __forceinline__ void place_tile(uint32_t u, uint32_t m_tiles, uint32_t n_tiles, int &mt, int &nt) {
+  const uint32_t group = u / (kRowGroup * n_tiles), in = u - group * kRowGroup * n_tiles;
+  const uint32_t height = min(m_tiles - group * kRowGroup, (uint32_t)kRowGroup);
+  nt = (int)(in / height);
+  mt = (int)(group * kRowGroup + in - (uint32_t)nt * height);
+}
+
+// The lane (of the first n, at most 64) whose value comes at place `order` when they are sorted from the largest down.
+__device__ __forceinline__ int lane_in_order(int value, int n, int order) {
+  const int lane = threadIdx.x & 63;
+  int rank = 0;
+  for (int i = 0; i < n; ++i) {
+    const int v = __builtin_amdgcn_readlane(value, i);
+    rank += v > value || (v == value && i < lane);
+  }
+  return __builtin_ctzll(__ballot(lane < n && rank == order));
+}
+
+// The tile of a workgroup, or false if there are not that many. Each XCD gets an eighth of all experts' tiles. With
+// a.rests_last the tiles that hold the rest of an expert's rows come behind all others, the largest first (up to 64 experts):
+// they take less time (products of rows that are not there are left out), so they fill up the last round.
 template <int BM>
 __device__ __forceinline__ bool find_rows(const ProductArgs &a, uint32_t block, uint32_t n_tiles, Rows &r, int &mt, int &nt) {
   const int lane = threadIdx.x & 63, E = a.n_experts;
-  uint32_t total = 0;
   int first = 0, count = 0;
-  uint32_t mine = 0, scan = 0;
+  uint32_t mine = 0, scan = 0, all = 0, all_rests = 0;
+  auto look = [&](int base) {
+    first = count = 0;
+    if (base + lane < E) expert_rows(a, base + lane, first, count);
+    mine = (uint32_t)(count + (a.rests_last ? 0 : BM - 1)) / BM;
+  };
   for (int base = 0; base < E; base += 64) {
-    mine = 0;
-    if (base + lane < E) {
-      expert_rows(a, base + lane, first, count);
-      mine = (uint32_t)(count + BM - 1) / BM;
-    }
+    look(base);
     scan = wave_scan(mine);
-    total += __builtin_amdgcn_readlane(scan, 63);
+    all += last_lane(scan);
+    if (a.rests_last) all_rests += (uint32_t)__popcll(__ballot((uint32_t)count % BM != 0));
   }
-  const uint64_t tiles = (uint64_t)total * n_tiles;
-  const uint64_t per = (tiles + kXcds - 1) / kXcds;
-  if (block / kXcds >= per) return false;
-  const uint64_t t64 = (uint64_t)(block % kXcds) * per + block / kXcds;
-  if (t64 >= tiles) return false;
-  // the expert that holds row tile t / n_tiles
-  const uint32_t at = (uint32_t)(t64 / n_tiles);
-  uint32_t before = 0;
+  const uint64_t tiles = (uint64_t)all * n_tiles, per = (tiles + kXcds - 1) / kXcds;
+  uint64_t t = (uint64_t)(block % kXcds) * per + block / kXcds;
+  const bool rest = block / kXcds >= per;
+  if (rest) {
+    t = block - per * kXcds;  // dealt one by one
+    if (t >= (uint64_t)all_rests * n_tiles) return false;
+  } else if (t >= tiles) {
+    return false;
+  }
+  uint32_t at = (uint32_t)(t / n_tiles), before = 0;  // row tile
+  if (rest) nt = (int)(t - (uint64_t)at * n_tiles);
   for (int base = 0; base < E; base += 64) {
-    if (E > 64) {
-      mine = 0;
-      if (base + lane < E) {
-        expert_rows(a, base + lane, first, count);
-        mine = (uint32_t)(count + BM - 1) / BM;
+    if (E > 64) look(base);
+    int l = -1;
+    if (rest) {
+      const uint32_t rows = (uint32_t)count % BM;
+      if (E <= 64) {
+        l = lane_in_order((int)rows, E, (int)at);
+      } else {
+        scan = wave_scan(rows != 0);
+        const uint64_t hit = __ballot(at - before < scan && rows != 0);
+        if (hit) l = __builtin_ctzll(hit);
       }
-      scan = wave_scan(mine);
+    } else {
+      if (E > 64) scan = wave_scan(mine);
+      const uint64_t hit = __ballot(at - before < scan && mine > 0);
+      if (hit) l = __builtin_ctzll(hit);
     }
-    const uint64_t hit = __ballot(at - before < scan && mine > 0);
-    if (hit) {
-      const int l = __builtin_ctzll(hit);
+    if (l >= 0) {
       r.expert = base + l;
       r.first = __builtin_amdgcn_readlane(first, l);
       r.count = __builtin_amdgcn_readlane(count, l);
-      const uint32_t m_tiles = __builtin_amdgcn_readlane(mine, l);
-      const uint32_t begin = before + __builtin_amdgcn_readlane(scan, l) - m_tiles;
-      const uint32_t u = (uint32_t)(t64 - (uint64_t)begin * n_tiles);  // within the expert
-      const uint32_t group = u / (kRowGroup * n_tiles), in = u - group * kRowGroup * n_tiles;
-      const uint32_t height = min(m_tiles - group * kRowGroup, (uint32_t)kRowGroup);
-      nt = (int)(in / height);
-      mt = (int)(group * kRowGroup + in - (uint32_t)nt * height);
+      if (rest) {
+        mt = r.count / BM;
+      } else {
+        const uint32_t m_tiles = (uint32_t)__builtin_amdgcn_readlane((int)mine, l);
+        const uint32_t begin = before + (uint32_t)__builtin_amdgcn_readlane((int)scan, l) - m_tiles;
+        place_tile((uint32_t)(t - (uint64_t)begin * n_tiles), m_tiles, n_tiles, mt, nt);
+      }
       return true;
     }
-    before += __builtin_amdgcn_readlane(scan, 63);
+    before += last_lane(scan);
   }
   return false;
 }
 
-// TN: every expert has m x n tiles, whether it has rows or not.
+// TN: every expert has m x n tiles, whether it has rows or not, and the time of a tile goes by the rows. Each XCD gets an eighth
+// of every expert's tiles, those of the experts with the most rows first (up to 64 experts; more are taken as they come).
 __device__ __forceinline__ bool find_matrix(const ProductArgs &a, uint32_t block, uint32_t m_tiles, uint32_t n_tiles, Rows &r,
                                             int &mt, int &nt) {
-  const uint32_t each = m_tiles * n_tiles, tiles = each * a.n_experts, per = (tiles + kXcds - 1) / kXcds;
-  const uint32_t t = block % kXcds * per + block / kXcds;
-  if (block / kXcds >= per || t >= tiles) return false;
-  r.expert = t / each;
-  int first;
-  expert_rows(a, r.expert, first, r.count);
-  r.first = first;
-  const uint32_t u = t - r.expert * each, group = u / (kRowGroup * n_tiles), in = u - group * kRowGroup * n_tiles;
-  const uint32_t height = min(m_tiles - group * kRowGroup, (uint32_t)kRowGroup);
-  nt = (int)(in / height);
-  mt = (int)(group * kRowGroup + in - (uint32_t)nt * height);
+  const int lane = threadIdx.x & 63, E = a.n_experts;
+  const uint32_t each = m_tiles * n_tiles, per = (each + kXcds - 1) / kXcds;
+  const uint32_t slot = block / kXcds, order = slot / per;
+  // the XCDs take turns in getting an expert's last part, which may be smaller
+  const uint32_t u = (block + order) % kXcds * per + slot % per;
+  if (order >= (uint32_t)E || u >= each) return false;
+  int first = 0, count = -1;
+  r.expert = (int)order;
+  if (E > 1 && E <= 64) {
+    if (lane < E) expert_rows(a, lane, first, count);
+    r.expert = lane_in_order(count, E, (int)order);
+    r.first = __builtin_amdgcn_readlane(first, r.expert);
+    r.count = __builtin_amdgcn_readlane(count, r.expert);
+  } else {
+    expert_rows(a, r.expert, first, count);
+    r.first = __builtin_amdgcn_readfirstlane(first);
+    r.count = __builtin_amdgcn_readfirstlane(count);
+  }
+  place_tile(u, m_tiles, n_tiles, mt, nt);
   return true;
+}
+
+// Workgroups that deal out all tiles.
+inline int64_t grid_of(const ProductArgs &a, int form, int bm, int64_t n_tiles) {
+  if (form == kTN) return (((int64_t)(a.m + bm - 1) / bm * n_tiles + kXcds - 1) / kXcds) * kXcds * a.n_experts;
+  const int64_t rests = a.n_rows < a.n_experts ? a.n_rows : a.n_experts;
+  return ((a.n_rows / bm * n_tiles + kXcds - 1) / kXcds + (rests * n_tiles + kXcds - 1) / kXcds) * kXcds;
 }
 
 // ------------------------------------------------------------ shared memory
@@ -198,8 +249,14 @@ __device__ __forceinline__ bool find_matrix(const ProductArgs &a, uint32_t block
 // that reads beside it (8 rows on), in different 32-byte slots.
 __device__ __forceinline__ uint32_t swizzle(uint32_t k) { return ((k & 3) | (k >> 3 & 1) << 2) << 1; }
 
+// Rows along the sum, 64 bytes each: ds_read_b128 serves the lanes 0-3, 12-15, 20-23 and 24-27 together (then 4-11, 16-19 and
+// 28-31, and so on), which are rows 0-15 in two chunks for BF16 and the rows of these numbers for MXFP4. Without this split
+// MXFP4's reads took twice as long.
+template <bool F4>
+__device__ __forceinline__ uint32_t swizzle_along(uint32_t row) { return F4 ? row >> 2 & 3 : row >> 1 & 3; }
+
 // One operand's tile of a step: N rows of the operand (along the sum) or 32 rows of N elements (across it).
-template <int N, bool Across, int Threads>
+template <int N, bool Across, bool F4, int Threads>
 struct Place {
   static constexpr int kChunks = N * 4;  // 16-byte chunks
   static constexpr int kEach = kChunks / Threads;
@@ -209,7 +266,7 @@ struct Place {
   // Chunk q of the tile holds (row, chunk) of the operand.
   static __device__ __forceinline__ void source(int q, int &row, int &chunk) {
     row = q / kRow;
-    chunk = (q % kRow) ^ (int)(Across ? swizzle(row) : row >> 1 & 3);
+    chunk = (q % kRow) ^ (int)(Across ? swizzle(row) : swizzle_along<F4>(row));
   }
 };
 
@@ -241,8 +298,8 @@ struct Tile {
   static constexpr int kLdsA = BM * kStepBytes, kLdsB = BN * kStepBytes;
   static constexpr int kLds = kLdsA + kLdsB;
   static constexpr int kLdsScales = F4 ? (BM + BN) * kScaleRow : 0;  // of kScaleSteps steps
-  using PlaceA = Place<BM, kAcrossA, kThreads>;
-  using PlaceB = Place<BN, kAcrossB, kThreads>;
+  using PlaceA = Place<BM, kAcrossA, F4, kThreads>;
+  using PlaceB = Place<BN, kAcrossB, F4, kThreads>;
 
   // Row of b's matrix that row r of the tile holds; the gated forms have gate rows
   // in the lower half and the same columns' up rows in the upper.
@@ -271,7 +328,7 @@ struct Tile {
   };
   static __device__ __forceinline__ uint32_t lane_along(int r0) {
     const uint32_t lane = threadIdx.x & 63;
-    return (r0 + lane % kS) * kStepBytes + ((lane / kS * kKK) ^ (lane >> 1 & 3)) * 16;
+    return (r0 + lane % kS) * kStepBytes + ((lane / kS * kKK) ^ swizzle_along<F4>(lane % kS)) * 16;
   }
   template <int N, int Each>
   static __device__ __forceinline__ uint32_t lane_across(int c0) {
@@ -779,7 +836,8 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) product_kernel(ProductArgs a)
             lds0 + kStages * T::kLds + (uint32_t)(step / kScaleSteps % 2) * T::kLdsScales + step % kScaleSteps * 4,
             tail ? T::scales_kept(blocks - 4 * step) : 0xFFFFu};
   };
-  auto turn = [&](auto tail, int step, typename T::Fragments &now, typename T::Fragments &next) {
+  auto turn = [&](auto rows, auto tail, int step, typename T::Fragments &now, typename T::Fragments &next) {
+    constexpr int Live = decltype(rows)::value;
     constexpr bool Tail = decltype(tail)::value;
     // the next step's operands are there, and nobody reads this step's any more
     if (!Tail || step + kStages <= steps) wait_and_meet<(kStages - 2) * kCopies>();
@@ -790,17 +848,17 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) product_kernel(ProductArgs a)
     constexpr int kRows = T::kKK * T::kTM;  // of products
     static_for<kRows>([&](auto row) {
       constexpr int u = decltype(row)::value, i = u % T::kTM, kk = u / T::kTM;
-      if constexpr (u < kLate * T::kKK) T::read_a(from, lane, kOnce + u / T::kKK, u % T::kKK, next);
+      if constexpr (u < kLate * T::kKK && Live == T::kTM) T::read_a(from, lane, kOnce + u / T::kKK, u % T::kKK, next);
       static_for<T::kKK * T::kTN_>([&](auto col) {
         constexpr int v = decltype(col)::value;
-        if constexpr (v * kRows / (T::kKK * T::kTN_) / 2 == u) T::read_b(from, lane, v % T::kTN_, v / T::kTN_, next);
+        if constexpr (v * kRows / (T::kKK * T::kTN_) / 2 == u && Live > 0) T::read_b(from, lane, v % T::kTN_, v / T::kTN_, next);
       });
       if (!Tail || ahead < steps) static_for<kCopies>([&](auto piece) {
           if constexpr (decltype(piece)::value * kRows / kCopies == u) copy(piece, ahead, Tail && ahead == steps - 1);
         });
-      T::template multiply<kk>(i < kOnce ? f[0] : now, now, i, acc);
+      if constexpr (i < Live) T::template multiply<kk>(i < kOnce ? f[0] : now, now, i, acc);
       __builtin_amdgcn_sched_barrier(0);
-      if constexpr (i < kOnce) T::read_a(from, lane, i, kk, f[0]);
+      if constexpr (i < kOnce && i < Live) T::read_a(from, lane, i, kk, f[0]);
     });
     if (!Tail || ahead < steps) advance(ahead);
   };
@@ -814,26 +872,27 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) product_kernel(ProductArgs a)
     if (steps >= kStages) wait_and_meet<(kStages - 1) * kCopies>();
     else wait_and_meet<0>();
     T::read(from_step(0, true), lane, f[0]);
-    int step = 0;
+    // rows: fragments of a that the wave multiplies
+    auto loop = [&](auto rows) {
+      int step = 0;
 #pragma unroll 1
-    for (; step + 1 + kStages < steps - 1; step += 2) {
-      turn(std::false_type(), step, f[0], f[1]);
-      turn(std::false_type(), step + 1, f[1], f[0]);
-    }
+      for (; step + 1 + kStages < steps - 1; step += 2) {
+        turn(rows, std::false_type(), step, f[0], f[1]);
+        turn(rows, std::false_type(), step + 1, f[1], f[0]);
+      }
 #pragma unroll 1
-    for (; step < steps; step += 2) {
-      turn(std::true_type(), step, f[0], f[1]);
-      if (step + 1 < steps) turn(std::true_type(), step + 1, f[1], f[0]);
-    }
+      for (; step < steps; step += 2) {
+        turn(rows, std::true_type(), step, f[0], f[1]);
+        if (step + 1 < steps) turn(rows, std::true_type(), step + 1, f[1], f[0]);
+      }
+    };
+    // an expert's last tile: waves leave out all or half of their rows if there are none
+    const int live = m_left - wm * (BM / WM);
+    if (Form == kTN || live > BM / WM / 2) loop(std::integral_constant<int, T::kTM>());
+    else if (live > 0) loop(std::integral_constant<int, T::kTM / 2>());
+    else loop(std::integral_constant<int, 0>());
   }
   finish_tile<Form, Epi, F4, BM, BN, WM, WN>(a, r, m0, n0, m_left, wm, wn, acc);
-}
-
-// Row tiles that n_rows rows of n_experts experts can make.
-inline int64_t most_row_tiles(const ProductArgs &a, int bm) {
-  const int64_t experts = a.offsets ? a.n_experts : 1;
-  const int64_t some = a.n_rows < experts ? a.n_rows : experts;  // with rows
-  return (a.n_rows - some) / bm + some;
 }
 
 }  // namespace wt

@@ -144,10 +144,11 @@ wt_status check_round(const char *what, int32_t dtype, int64_t n_rows, int64_t n
 }
 
 template <Epilogue Epi, int BM, int BN, int WM, int WN, bool Near>
-wt_status launch(const char *what, const ProductArgs &a, hipStream_t stream) {
+wt_status launch(const char *what, ProductArgs a, hipStream_t stream) {
   constexpr int columns = Epi == Epilogue::kGated ? BN / 2 : BN;
   const int64_t n_tiles = (a.n + columns - 1) / columns;
-  const int64_t grid = (most_row_tiles(a, BM) * n_tiles + kXcds - 1) / kXcds * kXcds;
+  const int64_t grid = grid_of(a, kNT, BM, n_tiles);
+  a.rests_last = grid <= 2 * kCus;  // as in expert.hip
   if (grid > kMaxGrid) return operator_fail(what, "too many tiles");
   if (grid == 0) return WT_OK;
   if constexpr (Near)
@@ -165,7 +166,8 @@ wt_status run(const char *what, const ProductArgs &a, hipStream_t stream) {
   const bool near = a.a_stride <= far / 512 && a.b_stride <= far / 512 && (int64_t)(a.n + 512) * a.b_stride < far &&
                     a.a_scale_stride <= far / 512 && a.b_scale_stride <= far / 512 && (int64_t)(a.n + 512) * a.b_scale_stride < far;
   if (!near) return launch<Epi, 128, 128, 2, 2, false>(what, a, stream);
-  const int64_t tiles = most_row_tiles(a, 256) * ((a.n + (Epi == Epilogue::kGated ? 127 : 255)) / (Epi == Epilogue::kGated ? 128 : 256));
+  const int columns = Epi == Epilogue::kGated ? 128 : 256;
+  const int64_t tiles = grid_of(a, kNT, 256, (a.n + columns - 1) / columns);
   return tiles < kCus ? launch<Epi, 128, 128, 2, 2, true>(what, a, stream) : launch<Epi, 256, 256, 2, 4, true>(what, a, stream);
 }
 

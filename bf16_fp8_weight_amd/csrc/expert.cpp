@@ -161,14 +161,14 @@ wt_status mxfp4_product_args(const char *what, const wt_mxfp4_product_desc *d, P
 bool product_aligned(const ProductArgs &a, int form, Epilogue epi) {
   const int64_t far = (int64_t)1 << 31;
   const int64_t bits = (int64_t)(a.a | a.b) | a.a_stride | a.b_stride | a.b_expert;
-  if (bits % 16) return false;
+  if (bits % 4) return false;
   const bool tn = form == WT_PRODUCT_TN;
   // 256 rows of a tile, and a step along the sum behind the last
   if (a.a_stride > far / 512 || a.b_stride > far / 512) return false;
   if (a.row_index && a.n_index_rows * (tn ? a.b_stride : a.a_stride) >= far) return false;
   if (epi == Epilogue::kGated && (int64_t)(a.n + 512) * a.b_stride >= far) return false;
   if (tn) return a.m % 2 == 0 && a.n % 2 == 0;
-  return a.k % 8 == 0 && (form == WT_PRODUCT_NT || a.n % 2 == 0);
+  return a.k % 2 == 0 && (form == WT_PRODUCT_NT || a.n % 2 == 0);
 }
 
 }  // namespace wt

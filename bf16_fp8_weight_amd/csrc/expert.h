@@ -30,9 +30,9 @@ struct ProductArgs {
 enum class Epilogue { kPlain, kGated, kGatedBack };
 
 // Whether a product's operands can be copied to shared memory in 16-byte pieces
-// under 31-bit offsets (the kernels' windows): addresses and strides are multiples of 16
-// bytes, rows along the sum end on one, rows across it on a word; a tile's rows, a
-// gathered array and an expert's gate rows span less than 2^31 bytes.
+// under 31-bit offsets (the kernels' windows): addresses, strides and the ends of rows are
+// multiples of 4 bytes; a tile's rows, a gathered array and an expert's gate rows
+// span less than 2^31 bytes.
 bool product_aligned(const ProductArgs &a, int form, Epilogue epi);
 
 // Fills *a from a description that it has checked; `what` names the call in the

@@ -51,10 +51,9 @@ __device__ __forceinline__ void static_for(F f) {
 
 enum Form { kNT = WT_PRODUCT_NT, kNN = WT_PRODUCT_NN, kTN = WT_PRODUCT_TN };
 
-constexpr int kStepBytes = 64;  // of a row along the sum
-// MXFP4: a row's scales are copied for several steps at a time. One word to a row and
-// step made as many requests as the operands (8192 x 8192 x 8192 360 us).
-constexpr int kScaleSteps = 4, kScaleRow = 4 * kScaleSteps;
+// MXFP4: a row's scales are copied for 512 codes at a time. Those of 128, a word to
+// a row, made as many requests as the operands (8192 x 8192 x 8192 360 us).
+constexpr int kScaleRow = 16;
 
 // ------------------------------------------------------------- activations
 // Both are x s(y) with s(y) = 1 / (1 + exp(-y)): SiLU y = x; GELU's
@@ -246,27 +245,28 @@ inline int64_t grid_of(const ProductArgs &a, int form, int bm, int64_t n_tiles) 
 
 // ------------------------------------------------------------ shared memory
 // Rows across the sum: the 4 rows of a 16-lane group, and those of the group
-// that reads beside it (8 rows on), in different 32-byte slots.
-__device__ __forceinline__ uint32_t swizzle(uint32_t k) { return ((k & 3) | (k >> 3 & 1) << 2) << 1; }
+// that reads beside it (8 rows on), in different 32-byte slots; rows of 64 elements have four.
+template <int N>
+__device__ __forceinline__ uint32_t swizzle(uint32_t k) { return ((k & 3) | (N >= 128 ? k >> 3 & 1 : 0) << 2) << 1; }
 
-// Rows along the sum, 64 bytes each: ds_read_b128 serves the lanes 0-3, 12-15, 20-23 and 24-27 together (then 4-11, 16-19 and
+// Rows along the sum, 64 or 128 bytes each: ds_read_b128 serves the lanes 0-3, 12-15, 20-23 and 24-27 together (then 4-11, 16-19 and
 // 28-31, and so on), which are rows 0-15 in two chunks for BF16 and the rows of these numbers for MXFP4. Without this split
 // MXFP4's reads took twice as long.
-template <bool F4>
-__device__ __forceinline__ uint32_t swizzle_along(uint32_t row) { return F4 ? row >> 2 & 3 : row >> 1 & 3; }
+template <bool F4, int Sub>
+__device__ __forceinline__ uint32_t swizzle_along(uint32_t row) { return Sub == 2 ? row >> 1 & 7 : F4 ? row >> 2 & 3 : row >> 1 & 3; }
 
-// One operand's tile of a step: N rows of the operand (along the sum) or 32 rows of N elements (across it).
-template <int N, bool Across, bool F4, int Threads>
+// One operand's tile of a step: N rows of the operand (along the sum) or 32 Sub rows of N elements (across it).
+template <int N, bool Across, bool F4, int Sub, int Threads>
 struct Place {
-  static constexpr int kChunks = N * 4;  // 16-byte chunks
+  static constexpr int kChunks = N * 4 * Sub;  // 16-byte chunks
   static constexpr int kEach = kChunks / Threads;
-  static constexpr int kRow = Across ? N / 8 : 4;  // chunks of a row in shared memory
+  static constexpr int kRow = Across ? N / 8 : 4 * Sub;  // chunks of a row in shared memory
   static_assert(kChunks % Threads == 0, "chunks per thread");
-  static_assert(!Across || N >= 128, "the swizzle spans 16 chunks");
+  static_assert(!Across || N >= 64, "the swizzle spans 8 or 16 chunks");
   // Chunk q of the tile holds (row, chunk) of the operand.
   static __device__ __forceinline__ void source(int q, int &row, int &chunk) {
     row = q / kRow;
-    chunk = (q % kRow) ^ (int)(Across ? swizzle(row) : swizzle_along<F4>(row));
+    chunk = (q % kRow) ^ (int)(Across ? swizzle<N>(row) : swizzle_along<F4, Sub>(row));
   }
 };
 
@@ -285,21 +285,27 @@ __device__ __forceinline__ u32x4 load_chunk(uint64_t p, int64_t valid) {
 }
 
 // ----------------------------------------------------------------- the tile
-template <int Form, Epilogue Epi, bool F4, int BM, int BN, int WM, int WN>
+// Sub: steps are 64 Sub bytes along the sum.
+template <int Form, Epilogue Epi, bool F4, int BM, int BN, int WM, int WN, int Sub>
 struct Tile {
+  static constexpr int kForm = Form;
+  static constexpr Epilogue kEpi = Epi;
   static constexpr int kThreads = 64 * WM * WN;
   static constexpr bool kAcrossA = Form == kTN, kAcrossB = Form != kNT;
-  static constexpr int kStep = F4 ? 128 : 32;  // elements of the sum
+  static constexpr int kStepBytes = 64 * Sub, kStep = (F4 ? 128 : 32) * Sub;  // of a row along the sum; elements
+  static constexpr int kSub = Sub, kScaleSteps = 4 / Sub;  // steps of a row of scales
   static constexpr int kS = F4 ? 32 : 16;  // of a matrix instruction
-  static constexpr int kKK = F4 ? 2 : 1;   // matrix instructions along the sum
+  static constexpr int kPer = F4 ? 2 : 1, kKK = kPer * Sub;  // matrix instructions along 64 bytes of the sum, and along a step
   typedef typename std::conditional<F4, f32x16, f32x4>::type Acc;
   static constexpr int kTM = BM / WM / kS, kTN_ = BN / WN / kS;
   static constexpr int kColumns = Epi == Epilogue::kGated ? BN / 2 : BN;  // of out (h)
   static constexpr int kLdsA = BM * kStepBytes, kLdsB = BN * kStepBytes;
   static constexpr int kLds = kLdsA + kLdsB;
-  static constexpr int kLdsScales = F4 ? (BM + BN) * kScaleRow : 0;  // of kScaleSteps steps
-  using PlaceA = Place<BM, kAcrossA, F4, kThreads>;
-  using PlaceB = Place<BN, kAcrossB, F4, kThreads>;
+  // Scales of kScaleSteps steps, copied 64 rows at a time
+  static constexpr int kScaleRowsA = (BM + 63) / 64 * 64, kScaleRowsB = (BN + 63) / 64 * 64;
+  static constexpr int kLdsScales = F4 ? (kScaleRowsA + kScaleRowsB) * kScaleRow : 0;
+  using PlaceA = Place<BM, kAcrossA, F4, Sub, kThreads>;
+  using PlaceB = Place<BN, kAcrossB, F4, Sub, kThreads>;
 
   // Row of b's matrix that row r of the tile holds; the gated forms have gate rows
   // in the lower half and the same columns' up rows in the upper.
@@ -319,25 +325,25 @@ struct Tile {
     return Epi == Epilogue::kGated && j >= kTN_ / 2 ? kColumns + kS * (j - kTN_ / 2) : kS * j;
   }
 
-  // Where a lane reads its part of the wave's first fragments (bytes into a step's operands). The lanes' part p = lane / kS takes
-  // chunk p of the sum (MXFP4: chunks 2 p and 2 p + 1, one for each matrix instruction). Fragment i of rows that run along the
-  // sum lies kS i rows on: row r0 + lane % kS, the other chunk in the neighbouring slot. Across: columns c0 .. c0 + 15; the
-  // swizzle moves chunks within 16, so that fragment i is found by an exclusive or.
+  // Where a lane reads its part of the wave's first fragments (bytes into a step's operands). Of each 64 bytes of the sum the
+  // lanes' part p = lane / kS takes chunk p (MXFP4: chunks 2 p and 2 p + 1, one for each matrix instruction). Fragment i of rows
+  // that run along the sum lies kS i rows on: row r0 + lane % kS; its other chunks are found by an exclusive or. Across: columns
+  // c0 .. c0 + 15; the swizzle moves chunks within 16, so that fragment i is found by an exclusive or.
   struct Lane {
     uint32_t a, b, sa, sb;
   };
   static __device__ __forceinline__ uint32_t lane_along(int r0) {
     const uint32_t lane = threadIdx.x & 63;
-    return (r0 + lane % kS) * kStepBytes + ((lane / kS * kKK) ^ swizzle_along<F4>(lane % kS)) * 16;
+    return (r0 + lane % kS) * kStepBytes + ((lane / kS * kPer) ^ swizzle_along<F4, Sub>(lane % kS)) * 16;
   }
   template <int N, int Each>
   static __device__ __forceinline__ uint32_t lane_across(int c0) {
-    static_assert(kS == 16 && (Each == 64 || Each == 128), "a wave's columns do not carry into the swizzle");
+    static_assert(kS == 16 && (Each == 32 || Each == 64 || Each == 128), "a wave's columns do not carry into the swizzle");
     const uint32_t lane = threadIdx.x & 63, i = lane & 15, k = (lane >> 4) * 8 + (i >> 2);
-    return k * (2 * N) + ((c0 / 8 + (i >> 1 & 1)) ^ swizzle(k)) * 16 + (i & 1) * 8;  // swizzle(k + 4) is the same
+    return k * (2 * N) + ((c0 / 8 + (i >> 1 & 1)) ^ swizzle<N>(k)) * 16 + (i & 1) * 8;  // swizzle(k + 4) is the same
   }
   static __device__ __forceinline__ Lane lane_of(int wm, int wn) {
-    const uint32_t lane = threadIdx.x & 63, scale = lane % kS * kScaleRow + lane / kS * kKK;
+    const uint32_t lane = threadIdx.x & 63, scale = lane % kS * kScaleRow + lane / kS * kPer;
     const int r0 = wm * (BM / WM), c0 = wn * kWaveColumns;
     Lane l;
     if constexpr (kAcrossA) l.a = lane_across<BM, BM / WM>(r0);
@@ -345,7 +351,7 @@ struct Tile {
     if constexpr (kAcrossB) l.b = lane_across<BN, BN / WN>(c0) + kLdsA;
     else l.b = lane_along(c0) + kLdsA;
     l.sa = r0 * kScaleRow + scale;
-    l.sb = (BM + c0) * kScaleRow + scale;
+    l.sb = (kScaleRowsA + c0) * kScaleRow + scale;
     return l;
   }
 
@@ -365,25 +371,29 @@ struct Tile {
   // A wave's share of a step's operands, in registers.
   struct Fragments {
     u32x4 a[kTM][kKK], b[kTN_][kKK];
-    uint32_t sa[F4 ? kTM : 1], sb[F4 ? kTN_ : 1];  // scales, two to a register
+    uint32_t sa[F4 ? kTM : 1][Sub], sb[F4 ? kTN_ : 1][Sub];  // scales, two to a register
   };
 
   // Where a step's operands and scales lie in shared memory. keep: mask of the lane's scales that are the row's (what is
   // behind them may be anything, NaN among it).
   struct From {
-    uint32_t operands, scales, keep;
+    uint32_t operands, scales, keep[Sub];
   };
+  // The exclusive or that finds matrix instruction kk's chunk.
+  static constexpr uint32_t chunk_bits(int kk) { return 64u * (kk / kPer) + 16u * (kk % kPer); }
   static __device__ __forceinline__ void read_a(const From &from, const Lane &l, int i, int kk, Fragments &f) {
-    if constexpr (kAcrossA) f.a[i][kk] = read_across<BM>(from.operands + (l.a ^ (uint32_t)(2 * kS * i)));
-    else f.a[i][kk] = *(lds_u32x4 *)(uintptr_t)(from.operands + (l.a ^ 16u * kk) + kS * i * kStepBytes);
+    if constexpr (kAcrossA) f.a[i][kk] = read_across<BM>(from.operands + (l.a ^ (uint32_t)(2 * kS * i)) + 64 * BM * kk);
+    else f.a[i][kk] = *(lds_u32x4 *)(uintptr_t)(from.operands + (l.a ^ chunk_bits(kk)) + kS * i * kStepBytes);
     if constexpr (F4)
-      if (kk == kKK - 1) f.sa[i] = *(lds_u16 *)(uintptr_t)(from.scales + l.sa + kS * kScaleRow * i) & from.keep;
+      if (kk % kPer == kPer - 1)
+        f.sa[i][kk / kPer] = *(lds_u16 *)(uintptr_t)(from.scales + l.sa + kS * kScaleRow * i + 4 * (kk / kPer)) & from.keep[kk / kPer];
   }
   static __device__ __forceinline__ void read_b(const From &from, const Lane &l, int j, int kk, Fragments &f) {
-    if constexpr (kAcrossB) f.b[j][kk] = read_across<BN>(from.operands + (l.b ^ (uint32_t)(2 * kS * j)));
-    else f.b[j][kk] = *(lds_u32x4 *)(uintptr_t)(from.operands + (l.b ^ 16u * kk) + b_frag(j) * kStepBytes);
+    if constexpr (kAcrossB) f.b[j][kk] = read_across<BN>(from.operands + (l.b ^ (uint32_t)(2 * kS * j)) + 64 * BN * kk);
+    else f.b[j][kk] = *(lds_u32x4 *)(uintptr_t)(from.operands + (l.b ^ chunk_bits(kk)) + b_frag(j) * kStepBytes);
     if constexpr (F4)
-      if (kk == kKK - 1) f.sb[j] = *(lds_u16 *)(uintptr_t)(from.scales + l.sb + kScaleRow * b_frag(j)) & from.keep;
+      if (kk % kPer == kPer - 1)
+        f.sb[j][kk / kPer] = *(lds_u16 *)(uintptr_t)(from.scales + l.sb + kScaleRow * b_frag(j) + 4 * (kk / kPer)) & from.keep[kk / kPer];
   }
   static __device__ __forceinline__ void read(const From &from, const Lane &l, Fragments &f) {
 #pragma unroll
@@ -395,9 +405,16 @@ struct Tile {
     }
   }
   // `left`: scale blocks of the row from this step's first on.
-  static __device__ __forceinline__ uint32_t scales_kept(int64_t left) {
-    const int first = (threadIdx.x & 63) / kS * kKK;
-    return first + 1 < left ? 0xFFFFu : first < left ? 0xFFu : 0u;
+  static __device__ __forceinline__ From from_of(uint32_t operands, uint32_t scales, int64_t left) {
+    From f;
+    f.operands = operands;
+    f.scales = scales;
+#pragma unroll
+    for (int u = 0; u < Sub; ++u) {
+      const int first = 4 * u + (threadIdx.x & 63) / kS * kPer;
+      f.keep[u] = first + 1 < left ? 0xFFFFu : first < left ? 0xFFu : 0u;
+    }
+    return f;
   }
 
   // Row i of the products with chunk kk, a's fragment from fa and b's from fb.
@@ -410,7 +427,8 @@ struct Tile {
         // the codes are the lower half of the operand, the upper is not looked at
         const i32x8 b = (i32x8)__builtin_shufflevector(x, x, 0, 1, 2, 3, -1, -1, -1, -1);
         const i32x8 a = (i32x8)__builtin_shufflevector(y, y, 0, 1, 2, 3, -1, -1, -1, -1);
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, acc[i][j], 4, 4, kk, (int)fb.sb[j], kk, (int)fa.sa[i]);
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b, a, acc[i][j], 4, 4, kk % kPer, (int)fb.sb[j][kk / kPer],
+                                                                    kk % kPer, (int)fa.sa[i][kk / kPer]);
       } else {
         acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), acc[i][j], 0, 0, 0);
       }
@@ -494,24 +512,25 @@ __device__ __forceinline__ void eight(const V &x, int x0, const V &y, int y0, fl
   }
 }
 
-template <int Form, Epilogue Epi, bool F4, int BM, int BN, int WM, int WN, class Acc, int TM, int TN>
-__device__ __forceinline__ void finish_tile(const ProductArgs &a, const Rows &r, int m0, int n0, int m_left, int wm, int wn,
+// T: the tile; acc: sums of TM x TN fragments from row row0 of the tile and column column0 of out on.
+template <class T, class Acc, int TM, int TN>
+__device__ __forceinline__ void finish_tile(const ProductArgs &a, const Rows &r, int m0, int m_left, int row0, int column0,
                                             const Acc (&acc)[TM][TN]) {
-  using T = Tile<Form, Epi, F4, BM, BN, WM, WN>;
-  constexpr int S = T::kS;
+  constexpr int S = T::kS, Form = T::kForm;
+  constexpr Epilogue Epi = T::kEpi;
   const int lane = threadIdx.x & 63, g = lane / S;
   const uint64_t out = a.out + (Form == kTN ? (uint64_t)(a.out_expert * r.expert) * (a.out_f32 ? 4 : 2) : 0);
   constexpr int kCols = Epi == Epilogue::kGated ? TN / 2 : TN;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
-    const int row = wm * (BM / WM) + S * i + lane % S;
+    const int row = row0 + S * i + lane % S;
 #pragma unroll
     for (int p = 0; p < kCols * S / 16; p += 2) {  // 32 columns
       constexpr int kUp = Epi == Epilogue::kGated ? kCols : 0;
       const int x = p * 16 / S, y = (p + 1) * 16 / S;
 #pragma unroll
       for (int half = 0; half < S / 16; ++half) {
-        const int column = n0 + wn * T::kWaveColumns + 16 * p + (S == 16 ? 16 * (g & 1) + 8 * (g >> 1) : 16 * half + 8 * g);
+        const int column = column0 + 16 * p + (S == 16 ? 16 * (g & 1) + 8 * (g >> 1) : 16 * half + 8 * g);
         float s[8], up[8];
         if constexpr (S == 16) {
           eight<S>(acc[i][x], 0, acc[i][y], 0, s);
@@ -530,9 +549,9 @@ __device__ __forceinline__ void finish_tile(const ProductArgs &a, const Rows &r,
 // ------------------------------------------------- operands of any alignment
 // The next step's chunks are loaded to registers before the present one is
 // computed and stored to the other half of shared memory behind it.
-template <int Form, Epilogue Epi, bool F4, int BM, int BN, int WM, int WN>
+template <int Form, Epilogue Epi, bool F4, int BM, int BN, int WM, int WN, int Sub>
 __global__ void __launch_bounds__(64 * WM * WN) product_any_kernel(ProductArgs a) {
-  using T = Tile<Form, Epi, F4, BM, BN, WM, WN>;
+  using T = Tile<Form, Epi, F4, BM, BN, WM, WN, Sub>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2][T::kLds + T::kLdsScales];
   Rows r;
   int mt, nt;
@@ -547,7 +566,7 @@ __global__ void __launch_bounds__(64 * WM * WN) product_any_kernel(ProductArgs a
   const uint64_t b_base = a.b + (Form == kTN ? 0 : (uint64_t)(a.b_expert * r.expert));
 
   u32x4 ra[T::PlaceA::kEach], rb[T::PlaceB::kEach];
-  uint32_t rs = 0;
+  uint32_t rs[Sub] = {};
   auto gathered = [&](int64_t row) -> int64_t {  // a row of the row space to one of the operand, -1: zeros
     if (!a.row_index) return row;
     const int64_t i = a.row_index[row];
@@ -592,18 +611,19 @@ __global__ void __launch_bounds__(64 * WM * WN) product_any_kernel(ProductArgs a
         }
       }
     }
-    if constexpr (F4) {  // the scales of a row's four blocks
-      static_assert(!F4 || BM + BN == T::kThreads, "one word of scales to a thread");
-      const int row = tid;
-      const int64_t at = k0 / 32;
-      rs = 0;
-      {
-        if (row < BM) {
-          if (row < m_left) rs = *(const uint32_t *)(uintptr_t)(a.a_scales + (uint64_t)((r.first + m0 + row) * a.a_scale_stride + at));
+    if constexpr (F4) {  // the scales of a row's blocks
+      static_assert(!F4 || BM + BN == T::kThreads, "a row of scales to a thread");
+#pragma unroll
+      for (int u = 0; u < Sub; ++u) {
+        const int64_t at = k0 / 32 + 4 * u;
+        rs[u] = 0;
+        if (at >= (a.k + 31) / 32) continue;
+        if (tid < BM) {
+          if (tid < m_left) rs[u] = *(const uint32_t *)(uintptr_t)(a.a_scales + (uint64_t)((r.first + m0 + tid) * a.a_scale_stride + at));
         } else {
           bool ok;
-          const int64_t s = T::b_row(a, n0, row - BM, ok);
-          if (ok) rs = *(const uint32_t *)(uintptr_t)(a.b_scales + (uint64_t)(a.b_scale_expert * r.expert + s * a.b_scale_stride + at));
+          const int64_t s = T::b_row(a, n0, tid - BM, ok);
+          if (ok) rs[u] = *(const uint32_t *)(uintptr_t)(a.b_scales + (uint64_t)(a.b_scale_expert * r.expert + s * a.b_scale_stride + at));
         }
       }
     }
@@ -613,7 +633,10 @@ __global__ void __launch_bounds__(64 * WM * WN) product_any_kernel(ProductArgs a
     for (int i = 0; i < T::PlaceA::kEach; ++i) *(u32x4 *)(to + 16 * (tid + i * T::kThreads)) = ra[i];
 #pragma unroll
     for (int i = 0; i < T::PlaceB::kEach; ++i) *(u32x4 *)(to + T::kLdsA + 16 * (tid + i * T::kThreads)) = rb[i];
-    if constexpr (F4) *(uint32_t *)(to + T::kLds + kScaleRow * tid) = rs;
+    if constexpr (F4) {
+#pragma unroll
+      for (int u = 0; u < Sub; ++u) *(uint32_t *)(to + T::kLds + kScaleRow * tid + 4 * u) = rs[u];
+    }
   };
 
   typename T::Acc acc[T::kTM][T::kTN_];
@@ -633,7 +656,7 @@ __global__ void __launch_bounds__(64 * WM * WN) product_any_kernel(ProductArgs a
       if (more) load(k0 + T::kStep);
       typename T::Fragments f;
       const uint32_t from = lds0 + at * (T::kLds + T::kLdsScales);
-      T::read({from, from + T::kLds, T::scales_kept((a.k - k0 + 31) / 32)}, lane, f);
+      T::read(T::from_of(from, from + T::kLds, (a.k - k0 + 31) / 32), lane, f);
       static_for<T::kKK>([&](auto half) {
 #pragma unroll
         for (int i = 0; i < T::kTM; ++i) T::template multiply<decltype(half)::value>(f, f, i, acc);
@@ -643,7 +666,7 @@ __global__ void __launch_bounds__(64 * WM * WN) product_any_kernel(ProductArgs a
     }
   }
 
-  finish_tile<Form, Epi, F4, BM, BN, WM, WN>(a, r, m0, n0, m_left, wm, wn, acc);
+  finish_tile<T>(a, r, m0, m_left, wm * (BM / WM), n0 + wn * T::kWaveColumns, acc);
 }
 
 // ------------------------------------------------------ aligned operands
@@ -653,7 +676,7 @@ __global__ void __launch_bounds__(64 * WM * WN) product_any_kernel(ProductArgs a
 // memory: rows behind the last, and offsets set to kNowhere.
 constexpr uint32_t kNowhere = 0x80000000u;
 
-// The compiler does not count these loads: wait_and_meet() waits for them.
+// The compiler does not count these loads: wait_for_copies() waits for them.
 template <int Add>
 __device__ __forceinline__ void copy16(u32x4 buffer, uint32_t lds, uint32_t offset) {
   asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(buffer), "n"(Add) : "memory", "scc");
@@ -664,9 +687,10 @@ __device__ __forceinline__ void copy4(u32x4 buffer, uint32_t lds, uint32_t offse
 }
 
 // All but the last `Pending` of this wave's copies have arrived and what it read has been read; then the workgroup meets.
-template <int Pending>
-__device__ __forceinline__ void wait_and_meet() {
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(Pending) : "memory");
+template <int Pending, bool Meet>
+__device__ __forceinline__ void wait_for_copies() {
+  if (Meet) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(Pending) : "memory");
+  else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(Pending) : "memory");
 }
 
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)x); }
@@ -678,7 +702,7 @@ struct Window {
   uint32_t move;  // bytes from step to step
   uint32_t bytes, last_bytes;
   __device__ __forceinline__ u32x4 buffer(bool last) const {
-    return u32x4{(uint32_t)base, (uint32_t)(base >> 32), last ? last_bytes : bytes, 0x00020000u};
+    return u32x4{uniform((uint32_t)base), uniform((uint32_t)(base >> 32)), uniform(last ? last_bytes : bytes), 0x00020000u};
   }
 };
 
@@ -687,39 +711,48 @@ __device__ __forceinline__ Window window(uint64_t base, int64_t move, int64_t by
   return {uniform(base), uniform((uint32_t)move), uniform((uint32_t)max(bytes, (int64_t)0)), uniform((uint32_t)max(last_bytes, (int64_t)0))};
 }
 
-constexpr int kStages = 4;
-
+// WM x WN waves share a tile (Split = 1), or Split waves take a part of the sum each, of the same tile and with operands of
+// their own, and add up their sums in the end (WM = WN = 1).
 // Indexed: rows along the sum (b of TN) are taken through row_index.
-template <int Form, Epilogue Epi, bool F4, int BM, int BN, int WM, int WN, bool Indexed>
-__global__ void __launch_bounds__(64 * WM * WN, 2) product_kernel(ProductArgs a) {
-  using T = Tile<Form, Epi, F4, BM, BN, WM, WN>;
+template <int Form, Epilogue Epi, bool F4, int BM, int BN, int WM, int WN, int Split, int Sub, int kStages, bool Indexed>
+__global__ void __launch_bounds__(64 * WM * WN * Split, WM * WN * Split == 4 && Sub * Split * kStages * (BM + BN) > 1280 ? 1 : 2) product_kernel(ProductArgs a) {
+  using T = Tile<Form, Epi, F4, BM, BN, WM, WN, Sub>;
+  constexpr int kStepBytes = T::kStepBytes, kScaleSteps = T::kScaleSteps;
   using PA = typename T::PlaceA;
   using PB = typename T::PlaceB;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kStages * T::kLds + 2 * T::kLdsScales];
+  static_assert(Split == 1 || (WM == 1 && WN == 1), "a wave has the whole tile or the whole sum");
+  constexpr int kIndexSteps = 2 / Sub, kIndexPairs = kStages / kIndexSteps + 2,
+                kIndexRows = Indexed ? 256 * kIndexPairs : 0;  // of a wave: 64 row numbers, that is steps; how often; bytes
+  constexpr int kScaleRing = kStages / kScaleSteps + 1;
+  constexpr int kRing = kStages * T::kLds + kScaleRing * T::kLdsScales;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Split * kRing + WM * WN * Split * kIndexRows];
   Rows r;
   int mt, nt;
   const uint32_t n_tiles = (uint32_t)(a.n + T::kColumns - 1) / T::kColumns;
   const bool mine = Form == kTN ? find_matrix(a, blockIdx.x, (uint32_t)(a.m + BM - 1) / BM, n_tiles, r, mt, nt)
                                 : find_rows<BM>(a, blockIdx.x, n_tiles, r, mt, nt);
   if (!mine) return;
-  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WN, wn = wave % WN;
+  const int waves = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int part = Split > 1 ? waves : 0, wave = Split > 1 ? 0 : waves, wm = wave / WN, wn = wave % WN;
+  const int tid = Split > 1 ? threadIdx.x & 63 : threadIdx.x;  // among those that share the tile
   const int m0 = mt * BM, n0 = nt * T::kColumns;
   const int m_left = (Form == kTN ? a.m : r.count) - m0;
   const int64_t K = Form == kTN ? r.count : a.k;
-  constexpr int kCopies = PA::kEach + PB::kEach;  // of a thread and step (scales come on top now and then)
-  const int steps = (int)((K + T::kStep - 1) / T::kStep);
+  constexpr int kCopies = PA::kEach + PB::kEach;  // of a thread and step (scales and row numbers come on top now and then)
+  const int all_steps = (int)((K + T::kStep - 1) / T::kStep);
+  // This wave's steps of the sum: whole kScaleSteps of them for MXFP4.
+  constexpr int kUnit = F4 ? kScaleSteps : 1;
+  const int units = (all_steps + kUnit - 1) / kUnit;
+  const int step0 = units * part / Split * kUnit, steps = min(units * (part + 1) / Split * kUnit, all_steps) - step0;
+  const int last_step = all_steps - 1 - step0;  // of the sum, counted from step0
 
   // Along the sum: bytes of a row that the last step has. Across it: rows.
   const int64_t row_bytes = F4 ? (int64_t)(a.k + 31) / 32 * 16 : 2 * (int64_t)a.k;
-  const int last_bytes = (int)(row_bytes - (int64_t)(steps - 1) * kStepBytes);
-  const int last_rows = (int)(K - (int64_t)(steps - 1) * T::kStep);
+  const int last_bytes = (int)(row_bytes - (int64_t)(all_steps - 1) * kStepBytes);
+  const int last_rows = (int)(K - (int64_t)(all_steps - 1) * T::kStep);
 
   Window wa, wb;
   uint32_t oa[PA::kEach], ob[PB::kEach];
-  auto index_of = [&](int64_t row) -> uint32_t {  // of the gathered operand, kNowhere if there is none
-    const int64_t i = a.row_index[row];
-    return i >= 0 && i < a.n_index_rows ? (uint32_t)i : kNowhere;
-  };
   if (T::kAcrossA) {
     const int64_t width = 2 * (int64_t)min(a.m - m0, BM);
     wa = window(a.a + (uint64_t)(r.first * a.a_stride + 2 * (int64_t)m0), T::kStep * a.a_stride, (T::kStep - 1) * a.a_stride + width,
@@ -734,7 +767,10 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) product_kernel(ProductArgs a)
     int row, chunk;
     PA::source(tid + i * T::kThreads, row, chunk);
     uint32_t at = (uint32_t)row;
-    if (!T::kAcrossA && !F4 && a.row_index) at = row < m_left ? index_of(r.first + m0 + row) : kNowhere;
+    if (!T::kAcrossA && !F4 && a.row_index) {
+      const int64_t from = row < m_left ? a.row_index[r.first + m0 + row] : -1;
+      at = from >= 0 && from < a.n_index_rows ? (uint32_t)from : kNowhere;
+    }
     oa[i] = at == kNowhere ? kNowhere : at * (uint32_t)a.a_stride + 16u * chunk;
   }
   const uint64_t b_base = a.b + (Form == kTN ? 0 : (uint64_t)(a.b_expert * r.expert));
@@ -756,35 +792,61 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) product_kernel(ProductArgs a)
     if (Epi == Epilogue::kGated && row >= T::kColumns) row += a.n - T::kColumns;  // up rows
     ob[i] = (uint32_t)row * (uint32_t)a.b_stride + 16u * chunk;
   }
-  auto load_rows = [&](int step) {  // Indexed: one step ahead
+  wa.base += (uint64_t)step0 * wa.move;
+  wb.base += (uint64_t)step0 * wb.move;
+
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)&lds[0] + part * kRing;
+
+  // Indexed: each wave copies the numbers of 64 rows at a time, kIndexPairs of them ahead.
+  typedef __attribute__((address_space(3))) const int32_t lds_i32;
+  const uint32_t lds_index = lds0 + (uint32_t)(Split - part) * kRing + (uint32_t)waves * kIndexRows;
+  const Window wi = Indexed ? window((uint64_t)(uintptr_t)(a.row_index + r.first), 0, 4 * K, 4 * K) : Window{};
+  auto copy_index = [&](int step) {  // a multiple of kIndexSteps
+    const uint32_t at = 4u * (uint32_t)((step0 + step) * T::kStep + (threadIdx.x & 63));
+    copy4<0>(wi.buffer(false), uniform(lds_index + (uint32_t)(step / kIndexSteps % kIndexPairs) * 256), at);
+  };
+  auto load_rows = [&](int step) {  // where b's rows of a step lie
 #pragma unroll
     for (int i = 0; i < PB::kEach; ++i) {
       int row, chunk;
       PB::source(tid + i * T::kThreads, row, chunk);
-      const int64_t k = (int64_t)step * T::kStep + row;
-      const uint32_t at = k < K ? index_of(r.first + k) : kNowhere;
-      ob[i] = at == kNowhere ? kNowhere : at * (uint32_t)a.b_stride + 16u * chunk;
+      const int from = *(lds_i32 *)(uintptr_t)(lds_index + (uint32_t)(step % (kIndexSteps * kIndexPairs)) * (128 * Sub) + 4 * row);
+      const bool there = (int64_t)(step0 + step) * T::kStep + row < K && from >= 0 && from < a.n_index_rows;
+      ob[i] = there ? (uint32_t)from * (uint32_t)a.b_stride + 16u * chunk : kNowhere;
     }
   };
-  if (Indexed && steps > 0) load_rows(0);
 
-  // Scales: the first waves copy those of a's rows, the others those of b's, a row of kScaleSteps steps to a thread.
-  Window ws{};
-  uint32_t os = 0;
-  static_assert(!F4 || (BM + BN == T::kThreads && BM % 64 == 0), "a row of scales to a thread");
-  const int blocks = (a.k + 31) / 32, last_scales = (steps - 1) / kScaleSteps * kScaleSteps;
-  if (F4) {
-    const bool of_a = wave < BM / 64;
-    const int64_t stride = of_a ? a.a_scale_stride : a.b_scale_stride;
-    int row = of_a ? tid : tid - BM;
-    const int64_t rows = of_a ? min(m_left, BM) : Epi == Epilogue::kGated ? a.n + min(a.n - n0, T::kColumns) : min(a.n - n0, BN);
-    if (!of_a && Epi == Epilogue::kGated && row >= T::kColumns) row += a.n - T::kColumns;
-    ws = window(of_a ? a.a_scales + (uint64_t)((r.first + m0) * stride) : a.b_scales + (uint64_t)(a.b_scale_expert * r.expert + n0 * stride),
-                kScaleRow, (rows - 1) * stride + kScaleRow, (rows - 1) * stride + (blocks + 3) / 4 * 4 - 4 * last_scales);
-    os = (uint32_t)row * (uint32_t)stride;
+  // Scales: 64 rows of a or b, kScaleSteps steps of each, to a copy; the waves that share the tile take turns.
+  constexpr int kScaleJobs = F4 ? (T::kScaleRowsA + T::kScaleRowsB) / 64 : 0, kScaleCopies = kScaleJobs / (WM * WN);
+  static_assert(kScaleJobs % (WM * WN) == 0, "as many copies for every wave");
+  Window ws[kScaleCopies > 0 ? kScaleCopies : 1];
+  uint32_t os[kScaleCopies > 0 ? kScaleCopies : 1];
+  const int blocks = (a.k + 31) / 32, last_scales = (all_steps - 1) / kScaleSteps * kScaleSteps;
+  if constexpr (F4) {
+#pragma unroll
+    for (int i = 0; i < kScaleCopies; ++i) {
+      const int job = wave + i * WM * WN;
+      const bool of_a = job < T::kScaleRowsA / 64;
+      const int64_t stride = of_a ? a.a_scale_stride : a.b_scale_stride;
+      int row = (of_a ? job : job - T::kScaleRowsA / 64) * 64 + (threadIdx.x & 63);
+      const bool there = row < (of_a ? BM : BN);
+      const int64_t rows = of_a ? min(m_left, BM) : Epi == Epilogue::kGated ? a.n + min(a.n - n0, T::kColumns) : min(a.n - n0, BN);
+      if (!of_a && Epi == Epilogue::kGated && row >= T::kColumns) row += a.n - T::kColumns;
+      ws[i] = window((of_a ? a.a_scales + (uint64_t)((r.first + m0) * stride)
+                           : a.b_scales + (uint64_t)(a.b_scale_expert * r.expert + n0 * stride)) + (uint64_t)step0 * (4 * Sub),
+                     kScaleRow, (rows - 1) * stride + kScaleRow, (rows - 1) * stride + (blocks + 3) / 4 * 4 - 4 * Sub * last_scales);
+      os[i] = there ? (uint32_t)row * (uint32_t)stride : kNowhere;
+    }
   }
+  auto copy_scales = [&](int step) {  // a multiple of kScaleSteps
+#pragma unroll
+    for (int i = 0; i < kScaleCopies; ++i) {
+      const uint32_t to = uniform(lds0 + kStages * T::kLds + (uint32_t)(step / kScaleSteps % kScaleRing) * T::kLdsScales + 1024u * (wave + i * WM * WN));
+      copy16<0>(ws[i].buffer(step0 + step == last_scales), to, os[i]);
+      ws[i].base += ws[i].move;
+    }
+  };
 
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)&lds[0];
   // One of a step's copies; the last step's rows along the sum may end before its 64 bytes.
   auto copy = [&](auto piece, int step, bool last) {
     constexpr int p = decltype(piece)::value;
@@ -808,11 +870,6 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) product_kernel(ProductArgs a)
       copy16<T::kLdsA + i * T::kThreads * 16>(wb.buffer(last), to, at);
     }
   };
-  auto copy_scales = [&](int step) {  // a multiple of kScaleSteps
-    const uint32_t to = uniform(lds0 + (uint32_t)(step / kScaleSteps % 2) * T::kLdsScales + 1024u * wave);
-    copy16<kStages * T::kLds>(ws.buffer(step == last_scales), to, os);
-    ws.base += ws.move;
-  };
   auto advance = [&](int step) {  // behind the copies of `step`
     wa.base += wa.move;
     wb.base += wb.move;
@@ -830,31 +887,48 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) product_kernel(ProductArgs a)
   // would be late, have registers for two steps.
   const typename T::Lane lane = T::lane_of(wm, wn);
   typename T::Fragments f[2];
-  constexpr int kLate = F4 ? 1 : 2, kOnce = T::kTM - kLate;
+  constexpr int kLate = F4 || T::kTM < 2 ? 1 : 2, kOnce = T::kTM - kLate;
   auto from_step = [&](int step, bool tail) -> typename T::From {
-    return {lds0 + (uint32_t)(step % kStages) * T::kLds,
-            lds0 + kStages * T::kLds + (uint32_t)(step / kScaleSteps % 2) * T::kLdsScales + step % kScaleSteps * 4,
-            tail ? T::scales_kept(blocks - 4 * step) : 0xFFFFu};
+    return T::from_of(lds0 + (uint32_t)(step % kStages) * T::kLds,
+                      lds0 + kStages * T::kLds + (uint32_t)(step / kScaleSteps % kScaleRing) * T::kLdsScales + step % kScaleSteps * (4 * Sub),
+                      tail ? blocks - 4 * Sub * (step0 + step) : 4 * Sub);
+  };
+  // Rows along the sum that end within a 16-byte chunk: what was copied behind their end becomes 0.
+  auto cut_last = [&](int step) {
+    if (F4 || last_bytes % 16 == 0) return;
+    constexpr int kRowsAlong = BM + (T::kAcrossB ? 0 : BN);
+    typedef __attribute__((address_space(3))) uint16_t lds_u16;
+    for (int row = tid; row < kRowsAlong; row += T::kThreads) {
+      const int in = row < BM ? row : row - BM;
+      const uint32_t at = lds0 + (uint32_t)(step % kStages) * T::kLds + (row < BM ? 0 : T::kLdsA) + in * kStepBytes +
+                          ((uint32_t)(last_bytes / 16) ^ swizzle_along<F4, Sub>(in)) * 16;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (2 * e >= last_bytes % 16) *(lds_u16 *)(uintptr_t)(at + 2 * e) = 0;
+    }
+    wait_for_copies<63, Split == 1>();
   };
   auto turn = [&](auto rows, auto tail, int step, typename T::Fragments &now, typename T::Fragments &next) {
     constexpr int Live = decltype(rows)::value;
     constexpr bool Tail = decltype(tail)::value;
     // the next step's operands are there, and nobody reads this step's any more
-    if (!Tail || step + kStages <= steps) wait_and_meet<(kStages - 2) * kCopies>();
-    else wait_and_meet<0>();
+    if (!Tail || step + kStages <= steps) wait_for_copies<(kStages - 2) * kCopies, Split == 1>();
+    else wait_for_copies<0, Split == 1>();
+    if (Tail && Form != kTN && step + 1 == last_step) cut_last(step + 1);
     const typename T::From from = from_step(step + 1, Tail);
     const int ahead = step + kStages;
     if (F4 && ahead % kScaleSteps == 0 && (!Tail || ahead < steps)) copy_scales(ahead);
+    if (Indexed && step % kIndexSteps == 0 && step + kIndexSteps * kIndexPairs < steps) copy_index(step + kIndexSteps * kIndexPairs);
     constexpr int kRows = T::kKK * T::kTM;  // of products
     static_for<kRows>([&](auto row) {
       constexpr int u = decltype(row)::value, i = u % T::kTM, kk = u / T::kTM;
-      if constexpr (u < kLate * T::kKK && Live == T::kTM) T::read_a(from, lane, kOnce + u / T::kKK, u % T::kKK, next);
+      if constexpr (u < kLate * T::kKK && kOnce + u / T::kKK < Live) T::read_a(from, lane, kOnce + u / T::kKK, u % T::kKK, next);
       static_for<T::kKK * T::kTN_>([&](auto col) {
         constexpr int v = decltype(col)::value;
         if constexpr (v * kRows / (T::kKK * T::kTN_) / 2 == u && Live > 0) T::read_b(from, lane, v % T::kTN_, v / T::kTN_, next);
       });
       if (!Tail || ahead < steps) static_for<kCopies>([&](auto piece) {
-          if constexpr (decltype(piece)::value * kRows / kCopies == u) copy(piece, ahead, Tail && ahead == steps - 1);
+          if constexpr (decltype(piece)::value * kRows / kCopies == u) copy(piece, ahead, Tail && ahead == last_step);
         });
       if constexpr (i < Live) T::template multiply<kk>(i < kOnce ? f[0] : now, now, i, acc);
       __builtin_amdgcn_sched_barrier(0);
@@ -863,14 +937,21 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) product_kernel(ProductArgs a)
     if (!Tail || ahead < steps) advance(ahead);
   };
   if (steps > 0) {
+    if (Indexed) {
+#pragma unroll 1
+      for (int i = 0; i < kIndexSteps * kIndexPairs && i < steps; i += kIndexSteps) copy_index(i);
+      wait_for_copies<0, false>();
+      load_rows(0);
+    }
 #pragma unroll 1
     for (int i = 0; i < kStages && i < steps; ++i) {
       if (F4 && i % kScaleSteps == 0) copy_scales(i);
-      static_for<kCopies>([&](auto piece) { copy(piece, i, i == steps - 1); });
+      static_for<kCopies>([&](auto piece) { copy(piece, i, i == last_step); });
       advance(i);
     }
-    if (steps >= kStages) wait_and_meet<(kStages - 1) * kCopies>();
-    else wait_and_meet<0>();
+    if (steps >= kStages) wait_for_copies<(kStages - 1) * kCopies, Split == 1>();
+    else wait_for_copies<0, Split == 1>();
+    if (Form != kTN && last_step == 0) cut_last(0);
     T::read(from_step(0, true), lane, f[0]);
     // rows: fragments of a that the wave multiplies
     auto loop = [&](auto rows) {
@@ -888,11 +969,46 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) product_kernel(ProductArgs a)
     };
     // an expert's last tile: waves leave out all or half of their rows if there are none
     const int live = m_left - wm * (BM / WM);
-    if (Form == kTN || live > BM / WM / 2) loop(std::integral_constant<int, T::kTM>());
-    else if (live > 0) loop(std::integral_constant<int, T::kTM / 2>());
-    else loop(std::integral_constant<int, 0>());
+    constexpr bool kWhole = Form == kTN || Split > 1;
+    if (kWhole || live > BM / WM / 2) loop(std::integral_constant<int, T::kTM>());
+    else if (live > 0) loop(std::integral_constant<int, kWhole ? T::kTM : T::kTM / 2>());
+    else loop(std::integral_constant<int, kWhole ? T::kTM : 0>());
   }
-  finish_tile<Form, Epi, F4, BM, BN, WM, WN>(a, r, m0, n0, m_left, wm, wn, acc);
+  if constexpr (Split == 1) {
+    finish_tile<T>(a, r, m0, m_left, wm * (BM / WM), n0 + wn * T::kWaveColumns, acc);
+  } else {
+    // Row i of the fragments is added up, in the order of the parts, and finished by wave i.
+    constexpr int kWords = sizeof(typename T::Acc) / 16, kPart = T::kTM * T::kTN_ * kWords;  // of 16 bytes and 64 lanes
+    static_assert(Split * kPart * 1024 <= Split * kRing && T::kTM <= Split, "sums take the place of the operands");
+    typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+    const uint32_t sums = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t *)&lds[0] + 16 * tid;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < T::kTM; ++i)
+#pragma unroll
+      for (int j = 0; j < T::kTN_; ++j)
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+          f32x4 v;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * w + e];
+          *(lds_f32x4 *)(uintptr_t)(sums + 1024 * (part * kPart + (i * T::kTN_ + j) * kWords + w)) = v;
+        }
+    __syncthreads();
+    if (part >= T::kTM) return;
+    typename T::Acc sum[1][T::kTN_];
+#pragma unroll
+    for (int j = 0; j < T::kTN_; ++j)
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) {
+        f32x4 v = {0, 0, 0, 0};
+#pragma unroll
+        for (int p = 0; p < Split; ++p) v += *(lds_f32x4 *)(uintptr_t)(sums + 1024 * (p * kPart + (part * T::kTN_ + j) * kWords + w));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[0][j][4 * w + e] = v[e];
+      }
+    finish_tile<T>(a, r, m0, m_left, part * T::kS, n0, sum);
+  }
 }
 
 }  // namespace wt

@@ -143,7 +143,7 @@ wt_status check_round(const char *what, int32_t dtype, int64_t n_rows, int64_t n
   return WT_OK;
 }
 
-template <Epilogue Epi, int BM, int BN, int WM, int WN, bool Near>
+template <Epilogue Epi, int BM, int BN, int WM, int WN, int Split, int Sub, int Stages, bool Near>
 wt_status launch(const char *what, ProductArgs a, hipStream_t stream) {
   constexpr int columns = Epi == Epilogue::kGated ? BN / 2 : BN;
   const int64_t n_tiles = (a.n + columns - 1) / columns;
@@ -152,23 +152,30 @@ wt_status launch(const char *what, ProductArgs a, hipStream_t stream) {
   if (grid > kMaxGrid) return operator_fail(what, "too many tiles");
   if (grid == 0) return WT_OK;
   if constexpr (Near)
-    hipLaunchKernelGGL((product_kernel<kNT, Epi, true, BM, BN, WM, WN, false>), dim3((uint32_t)grid), dim3(64 * WM * WN), 0, stream, a);
+    hipLaunchKernelGGL((product_kernel<kNT, Epi, true, BM, BN, WM, WN, Split, Sub, Stages, false>), dim3((uint32_t)grid), dim3(64 * WM * WN * Split), 0, stream, a);
   else
-    hipLaunchKernelGGL((product_any_kernel<kNT, Epi, true, BM, BN, WM, WN>), dim3((uint32_t)grid), dim3(64 * WM * WN), 0, stream, a);
+    hipLaunchKernelGGL((product_any_kernel<kNT, Epi, true, BM, BN, WM, WN, Sub>), dim3((uint32_t)grid), dim3(64 * WM * WN * Split), 0, stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return operator_fail(what, hip_msg("launch", e), WT_E_HIP);
   return WT_OK;
 }
 
+// Which kernel, as in expert.hip. Measured on MI355X, us (k x n; kernel 32 | 128 | 256 = rows of a tile): one row, 2816 x 1024 6.6 | 8.4 |
+// 12.2; 64 rows, 1024 x 2816 gated 6.5 | 7.9 | 9.9; 256 rows 14.4 | 8.3 | 16.9; 4096 rows - | 29.5 | 35.1; 2048 rows, 4096 x 4096
+// 95 | 26.8 | 31.5; 4096 rows - | 49.1 | 46.7; 256 rows of 96 experts, 7168 x 2048 gated 300 | 258 | 304; 2000 rows of 24
+// experts - | 100 | 108; 8192 cubed - | 327 | 296.
 template <Epilogue Epi>
 wt_status run(const char *what, const ProductArgs &a, hipStream_t stream) {
   const int64_t far = (int64_t)1 << 31;
+  // 31-bit offsets within a tile's rows, as in product_aligned()
   const bool near = a.a_stride <= far / 512 && a.b_stride <= far / 512 && (int64_t)(a.n + 512) * a.b_stride < far &&
                     a.a_scale_stride <= far / 512 && a.b_scale_stride <= far / 512 && (int64_t)(a.n + 512) * a.b_scale_stride < far;
-  if (!near) return launch<Epi, 128, 128, 2, 2, false>(what, a, stream);
-  const int columns = Epi == Epilogue::kGated ? 128 : 256;
-  const int64_t tiles = grid_of(a, kNT, 256, (a.n + columns - 1) / columns);
-  return tiles < kCus ? launch<Epi, 128, 128, 2, 2, true>(what, a, stream) : launch<Epi, 256, 256, 2, 4, true>(what, a, stream);
+  if (!near) return launch<Epi, 128, 128, 2, 2, 1, 2, 2, false>(what, a, stream);
+  const int64_t halves = Epi == Epilogue::kGated ? 2 : 1;
+  auto tiles = [&](int rows, int columns) { return grid_of(a, kNT, rows, (a.n * halves + columns - 1) / columns); };
+  if (tiles(32, 64) <= kCus) return launch<Epi, 32, 64, 1, 1, 4, 2, 2, true>(what, a, stream);
+  if (tiles(256, 256) >= kCus && a.n_rows >= 128 * (int64_t)a.n_experts) return launch<Epi, 256, 256, 2, 4, 1, 1, 4, true>(what, a, stream);
+  return launch<Epi, 128, 128, 2, 2, 1, 2, 2, true>(what, a, stream);
 }
 
 }  // namespace

@@ -98,8 +98,6 @@ wt_status product_args(const char *what, const wt_product_desc *d, Epilogue epi,
   a->k = tn ? 0 : (int32_t)d->k;
   a->act = d->act;
   a->out_f32 = d->out_dtype == WT_DT_F32;
-  a->out_wide = a->out % 16 == 0 && d->out_stride % 8 == 0 && a->out_expert % 8 == 0 &&
-                (epi == Epilogue::kPlain || (d->n % 8 == 0 && a->pre % 16 == 0 && a->pre_stride % 8 == 0));
   return WT_OK;
 }
 
@@ -154,7 +152,6 @@ wt_status mxfp4_product_args(const char *what, const wt_mxfp4_product_desc *d, P
   a->k = (int32_t)d->k;
   a->act = d->act;
   a->out_f32 = d->out_dtype == WT_DT_F32;
-  a->out_wide = a->out % 16 == 0 && d->out_stride % 8 == 0;
   return WT_OK;
 }
 

@@ -24,7 +24,6 @@ struct ProductArgs {
   int32_t m, n, k;      // n: columns of out (of h in the gated forms)
   int32_t act, out_f32;
   int32_t rests_last;   // order of the tiles, see find_rows()
-  int32_t out_wide;     // eight columns of out (and pre) can be stored at once
 };
 
 enum class Epilogue { kPlain, kGated, kGatedBack };

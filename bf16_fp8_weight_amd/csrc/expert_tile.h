@@ -270,17 +270,38 @@ struct Place {
   }
 };
 
-// Eight BF16 elements of which the first `valid` exist, at any 2-byte address.
+// Global memory at a byte address, at any alignment of 2 bytes. (Through generic pointers the accesses would count as
+// shared memory's too, and every read of a step would wait for the next step's loads.)
+template <class V, int Align = 2>
+__device__ __forceinline__ V load_at(uint64_t p) {
+  typedef V Any __attribute__((aligned(Align)));
+  return *(const __attribute__((address_space(1))) Any *)(uintptr_t)p;
+}
+template <class V>
+__device__ __forceinline__ void store_at(uint64_t p, V v) {
+  typedef V Any __attribute__((aligned(2)));
+  *(__attribute__((address_space(1))) Any *)(uintptr_t)p = v;
+}
+
+// Eight BF16 elements of which the first `valid` exist.
 __device__ __forceinline__ u32x4 load_chunk(uint64_t p, int64_t valid) {
   u32x4 v = {0, 0, 0, 0};
-  const uint16_t *s = (const uint16_t *)(uintptr_t)p;
   if (valid >= 8) {
-    __builtin_memcpy(&v, s, 16);
+    v = load_at<u32x4>(p);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < valid) v[i >> 1] |= (uint32_t)s[i] << (16 * (i & 1));
+      if (i < valid) v[i >> 1] |= (uint32_t)load_at<uint16_t>(p + 2 * i) << (16 * (i & 1));
   }
+  return v;
+}
+
+// The last `n` (uniform, 1 to 7) of eight elements as the first ones; what lies behind them is not looked at.
+__device__ __forceinline__ u32x4 last_first(u32x4 v, int n) {
+  const int drop = 8 - n;
+  if (drop & 4) v = u32x4{v.z, v.w, 0, 0};
+  if (drop & 2) v = u32x4{v.y, v.z, v.w, 0};
+  if (drop & 1) v = u32x4{v.x >> 16 | v.y << 16, v.y >> 16 | v.z << 16, v.z >> 16 | v.w << 16, v.w >> 16};
   return v;
 }
 
@@ -307,15 +328,10 @@ struct Tile {
   using PlaceA = Place<BM, kAcrossA, F4, Sub, kThreads>;
   using PlaceB = Place<BN, kAcrossB, F4, Sub, kThreads>;
 
-  // Row of b's matrix that row r of the tile holds; the gated forms have gate rows
-  // in the lower half and the same columns' up rows in the upper.
-  static __device__ __forceinline__ int64_t b_row(const ProductArgs &a, int n0, int r, bool &ok) {
-    if (Epi != Epilogue::kGated) {
-      ok = n0 + r < a.n;
-      return n0 + r;
-    }
-    const int c = n0 + r % kColumns;
-    ok = c < a.n;
+  // Row of b's matrix that row r of the tile holds (its last one for those behind it); the gated forms have gate rows in the
+  // lower half and the same columns' up rows in the upper.
+  static __device__ __forceinline__ int64_t b_row(const ProductArgs &a, int n0, int r) {
+    const int c = min(n0 + r % kColumns, a.n - 1);
     return r < kColumns ? c : (int64_t)a.n + c;
   }
 
@@ -437,32 +453,29 @@ struct Tile {
 };
 
 // ------------------------------------------------------------------ results
-// Of eight neighbouring columns `n` exist; `wide`: eight can be stored at once.
+// Of eight neighbouring columns `n` exist.
 template <class V>
-__device__ __forceinline__ void store8(uint64_t out, int64_t at, const float (&v)[8], int n, bool wide) {
-  V *p = (V *)(uintptr_t)out + at;
-  if (wide && n >= 8) {
-    typedef V V8 __attribute__((ext_vector_type(8)));
+__device__ __forceinline__ void store8(uint64_t out, int64_t at, const float (&v)[8], int n) {
+  const uint64_t p = out + (uint64_t)at * sizeof(V);
+  typedef V V8 __attribute__((ext_vector_type(8)));
+  if (n >= 8) {
     V8 r;
 #pragma unroll
     for (int i = 0; i < 8; ++i) r[i] = (V)v[i];
-    *(V8 *)p = r;
+    store_at<V8>(p, r);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = (V)v[i];
+      if (i < n) store_at<V>(p + sizeof(V) * i, (V)v[i]);
   }
 }
 
-__device__ __forceinline__ void load_pre(uint64_t pre, int64_t at, int n, bool wide, float (&v)[8]) {
-  const __bf16 *p = (const __bf16 *)(uintptr_t)pre + at;
-  if (wide && n >= 8) {
-    const bf16x8 r = *(const bf16x8 *)p;
+__device__ __forceinline__ void load_pre(uint64_t pre, int64_t at, int n, float (&v)[8]) {
+  const u32x4 w = load_chunk(pre + 2 * (uint64_t)at, n);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = (float)r[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? (float)p[i] : 0.0f;
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
 }
 
@@ -470,31 +483,30 @@ __device__ __forceinline__ void load_pre(uint64_t pre, int64_t at, int n, bool w
 template <Epilogue Epi>
 __device__ __forceinline__ void finish8(const ProductArgs &a, uint64_t out, int64_t row, int column, int n, const float (&s)[8],
                                         const float (&up)[8]) {
-  const bool wide = a.out_wide;
   if (Epi == Epilogue::kPlain) {
-    if (a.out_f32) store8<float>(out, row * a.out_stride + column, s, n, wide);
-    else store8<__bf16>(out, row * a.out_stride + column, s, n, wide);
+    if (a.out_f32) store8<float>(out, row * a.out_stride + column, s, n);
+    else store8<__bf16>(out, row * a.out_stride + column, s, n);
   } else if (Epi == Epilogue::kGated) {
     if (a.pre) {
-      store8<__bf16>(a.pre, row * a.pre_stride + column, s, n, wide);
-      store8<__bf16>(a.pre, row * a.pre_stride + a.n + column, up, n, wide);
+      store8<__bf16>(a.pre, row * a.pre_stride + column, s, n);
+      store8<__bf16>(a.pre, row * a.pre_stride + a.n + column, up, n);
     }
     float h[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[i] = activation(a.act, s[i]).value * up[i];
-    store8<__bf16>(out, row * a.out_stride + column, h, n, wide);
+    store8<__bf16>(out, row * a.out_stride + column, h, n);
   } else {
     float g[8], u[8], dg[8], du[8];
-    load_pre(a.pre, row * a.pre_stride + column, n, wide, g);
-    load_pre(a.pre, row * a.pre_stride + a.n + column, n, wide, u);
+    load_pre(a.pre, row * a.pre_stride + column, n, g);
+    load_pre(a.pre, row * a.pre_stride + a.n + column, n, u);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const Act t = activation(a.act, g[i]);
       dg[i] = s[i] * u[i] * t.slope;
       du[i] = s[i] * t.value;
     }
-    store8<__bf16>(out, row * a.out_stride + column, dg, n, wide);
-    store8<__bf16>(out, row * a.out_stride + a.n + column, du, n, wide);
+    store8<__bf16>(out, row * a.out_stride + column, dg, n);
+    store8<__bf16>(out, row * a.out_stride + a.n + column, du, n);
   }
 }
 
@@ -565,51 +577,110 @@ __global__ void __launch_bounds__(64 * WM * WN) product_any_kernel(ProductArgs a
   const int m_left = (Form == kTN ? a.m : r.count) - m0;
   const uint64_t b_base = a.b + (Form == kTN ? 0 : (uint64_t)(a.b_expert * r.expert));
 
-  u32x4 ra[T::PlaceA::kEach], rb[T::PlaceB::kEach];
+  // Of each chunk: where it lies in the first step, how many of its elements exist (along the sum: of its row; across it: of
+  // the columns), and its row in the step. The chunks that a step has in full are loaded without a question.
+  constexpr int kA = T::PlaceA::kEach, kB = T::PlaceB::kEach;
+  u32x4 ra[kA], rb[kB];
   uint32_t rs[Sub] = {};
-  auto gathered = [&](int64_t row) -> int64_t {  // a row of the row space to one of the operand, -1: zeros
-    if (!a.row_index) return row;
-    const int64_t i = a.row_index[row];
-    return i >= 0 && i < a.n_index_rows ? i : -1;
-  };
+  uint64_t pa[kA], pb[kB];
+  int64_t va[kA], vb[kB];
+  bool cut_a[kA] = {}, cut_b[kB] = {};
   const int64_t f4_row = (int64_t)(a.k + 31) / 32 * 16;  // bytes of codes
-  auto load = [&](int64_t k0) {  // k0 in elements
+  const int64_t along = F4 ? f4_row / 16 * 8 : a.k;      // elements, codes in chunks that count as 8
+  const bool gather_b = Form == kTN && a.row_index;
+  bool full = true;
 #pragma unroll
-    for (int i = 0; i < T::PlaceA::kEach; ++i) {
-      int row, chunk;
-      T::PlaceA::source(tid + i * T::kThreads, row, chunk);
-      ra[i] = u32x4{0, 0, 0, 0};
-      if (F4) {
-        const int64_t at = k0 / 2 + 16 * chunk;
-        if (row < m_left && at < f4_row) ra[i] = *(const u32x4 *)(uintptr_t)(a.a + (uint64_t)((r.first + m0 + row) * a.a_stride + at));
-      } else if (T::kAcrossA) {
-        if (k0 + row < K)
-          ra[i] = load_chunk(a.a + (uint64_t)((r.first + k0 + row) * a.a_stride + 2 * (int64_t)(m0 + 8 * chunk)), m_left - 8 * chunk);
-      } else if (row < m_left) {
-        const int64_t s = gathered(r.first + m0 + row);
-        if (s >= 0) ra[i] = load_chunk(a.a + (uint64_t)(s * a.a_stride + 2 * (k0 + 8 * chunk)), K - k0 - 8 * chunk);
+  for (int i = 0; i < kA; ++i) {
+    int row, chunk;
+    T::PlaceA::source(tid + i * T::kThreads, row, chunk);
+    if (T::kAcrossA) {
+      pa[i] = a.a + (uint64_t)((r.first + row) * a.a_stride + 2 * (int64_t)(m0 + 8 * chunk));
+      va[i] = m_left - 8 * chunk;
+      // columns that do not exist may hold anything: the tile's first ones; a chunk that ends behind the last column is loaded
+      // as the eight before it and moved
+      if (va[i] <= 0 && m_left >= 8) pa[i] -= 16 * chunk, va[i] = 8;
+      cut_a[i] = va[i] > 0 && va[i] < 8;
+      if (cut_a[i] && a.m >= 8) pa[i] -= 2 * (8 - va[i]);
+      full = full && (va[i] >= 8 || (cut_a[i] && a.m >= 8));
+    } else {
+      // so may rows that do not exist
+      int64_t from = r.first + m0 + min(row, m_left - 1);
+      bool there = true;
+      if (!F4 && a.row_index) {
+        from = a.row_index[from];
+        there = from >= 0 && from < a.n_index_rows;
       }
+      pa[i] = a.a + (uint64_t)(there ? from * a.a_stride + 16 * chunk : 0);
+      va[i] = there ? along - 8 * chunk : 0;
+      full = full && there;
     }
+  }
 #pragma unroll
-    for (int i = 0; i < T::PlaceB::kEach; ++i) {
+  for (int i = 0; i < kB; ++i) {
+    int row, chunk;
+    T::PlaceB::source(tid + i * T::kThreads, row, chunk);
+    if (T::kAcrossB) {
+      pb[i] = b_base + (uint64_t)((gather_b ? 0 : (Form == kTN ? r.first + row : row) * a.b_stride) + 2 * (int64_t)(n0 + 8 * chunk));
+      vb[i] = a.n - n0 - 8 * chunk;
+      if (vb[i] <= 0 && a.n - n0 >= 8) pb[i] -= 16 * chunk, vb[i] = 8;
+      cut_b[i] = vb[i] > 0 && vb[i] < 8;
+      if (cut_b[i] && a.n >= 8) pb[i] -= 2 * (8 - vb[i]);
+      full = full && (vb[i] >= 8 || (cut_b[i] && a.n >= 8));
+    } else {
+      pb[i] = b_base + (uint64_t)(T::b_row(a, n0, row) * a.b_stride + 16 * chunk);
+      vb[i] = along - 8 * chunk;
+    }
+  }
+  full = __all(full);
+  // the tiles with the last columns, if those do not fill a chunk
+  const bool cuts_a = T::kAcrossA && m_left < BM && a.m % 8, cuts_b = T::kAcrossB && a.n - n0 < BN && a.n % 8;
+  auto load = [&](int64_t k0) __attribute__((always_inline)) {  // k0 in elements
+    const int64_t k1 = F4 ? k0 / 4 : k0;  // as `along` counts
+    const bool whole = full && (F4 ? k1 + T::kStep / 4 <= along : k0 + T::kStep <= K);
+    const uint64_t move_a = (uint64_t)(T::kAcrossA ? k0 * a.a_stride : 2 * k1), move_b = (uint64_t)(T::kAcrossB ? k0 * a.b_stride : 2 * k1);
+    uint64_t at_b[kB];
+    bool there_b[kB];
+#pragma unroll
+    for (int i = 0; i < kB; ++i) {
       int row, chunk;
       T::PlaceB::source(tid + i * T::kThreads, row, chunk);
-      rb[i] = u32x4{0, 0, 0, 0};
-      if (T::kAcrossB) {
-        if (k0 + row < K) {
-          const int64_t s = Form == kTN ? gathered(r.first + k0 + row) : k0 + row;
-          if (s >= 0) rb[i] = load_chunk(b_base + (uint64_t)(s * a.b_stride + 2 * (int64_t)(n0 + 8 * chunk)), a.n - n0 - 8 * chunk);
-        }
-      } else {
-        bool ok;
-        const int64_t s = T::b_row(a, n0, row, ok);
-        if (F4) {
-          const int64_t at = k0 / 2 + 16 * chunk;
-          if (ok && at < f4_row) rb[i] = *(const u32x4 *)(uintptr_t)(b_base + (uint64_t)(s * a.b_stride + at));
-        } else if (ok) {
-          rb[i] = load_chunk(b_base + (uint64_t)(s * a.b_stride + 2 * (k0 + 8 * chunk)), K - k0 - 8 * chunk);
-        }
+      at_b[i] = pb[i] + move_b;
+      there_b[i] = !T::kAcrossB || k0 + row < K;
+      if (gather_b && there_b[i]) {
+        const int64_t from = a.row_index[r.first + k0 + row];
+        there_b[i] = from >= 0 && from < a.n_index_rows;
+        at_b[i] = pb[i] + (uint64_t)(there_b[i] ? from * a.b_stride : 0);
       }
+    }
+    if (whole) {
+#pragma unroll
+      for (int i = 0; i < kA; ++i) ra[i] = load_at<u32x4>(pa[i] + move_a);
+      if (gather_b) {
+#pragma unroll
+        for (int i = 0; i < kB; ++i) rb[i] = there_b[i] ? load_at<u32x4>(at_b[i]) : u32x4{0, 0, 0, 0};
+      } else {
+#pragma unroll
+        for (int i = 0; i < kB; ++i) rb[i] = load_at<u32x4>(at_b[i]);
+      }
+      if (cuts_a) {
+#pragma unroll
+        for (int i = 0; i < kA; ++i) ra[i] = cut_a[i] ? last_first(ra[i], a.m % 8) : ra[i];
+      }
+      if (cuts_b) {
+#pragma unroll
+        for (int i = 0; i < kB; ++i) rb[i] = cut_b[i] ? last_first(rb[i], a.n % 8) : rb[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kA; ++i) {
+        int row, chunk;
+        T::PlaceA::source(tid + i * T::kThreads, row, chunk);
+        ra[i] = load_chunk(pa[i] + move_a + (cut_a[i] && a.m >= 8 ? 2 * (8 - va[i]) : 0),
+                           T::kAcrossA ? (k0 + row < K ? va[i] : 0) : va[i] - k1);
+      }
+#pragma unroll
+      for (int i = 0; i < kB; ++i)
+        rb[i] = load_chunk(at_b[i] + (cut_b[i] && a.n >= 8 ? 2 * (8 - vb[i]) : 0), T::kAcrossB ? (there_b[i] ? vb[i] : 0) : vb[i] - k1);
     }
     if constexpr (F4) {  // the scales of a row's blocks
       static_assert(!F4 || BM + BN == T::kThreads, "a row of scales to a thread");
@@ -619,11 +690,10 @@ __global__ void __launch_bounds__(64 * WM * WN) product_any_kernel(ProductArgs a
         rs[u] = 0;
         if (at >= (a.k + 31) / 32) continue;
         if (tid < BM) {
-          if (tid < m_left) rs[u] = *(const uint32_t *)(uintptr_t)(a.a_scales + (uint64_t)((r.first + m0 + tid) * a.a_scale_stride + at));
+          rs[u] = load_at<uint32_t>(a.a_scales + (uint64_t)((r.first + m0 + min(tid, m_left - 1)) * a.a_scale_stride + at));
         } else {
-          bool ok;
-          const int64_t s = T::b_row(a, n0, tid - BM, ok);
-          if (ok) rs[u] = *(const uint32_t *)(uintptr_t)(a.b_scales + (uint64_t)(a.b_scale_expert * r.expert + s * a.b_scale_stride + at));
+          const int64_t s = T::b_row(a, n0, tid - BM);
+          rs[u] = load_at<uint32_t>(a.b_scales + (uint64_t)(a.b_scale_expert * r.expert + s * a.b_scale_stride + at));
         }
       }
     }
@@ -657,7 +727,7 @@ __global__ void __launch_bounds__(64 * WM * WN) product_any_kernel(ProductArgs a
       typename T::Fragments f;
       const uint32_t from = lds0 + at * (T::kLds + T::kLdsScales);
       T::read(T::from_of(from, from + T::kLds, (a.k - k0 + 31) / 32), lane, f);
-      static_for<T::kKK>([&](auto half) {
+      static_for<T::kKK>([&](auto half) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < T::kTM; ++i) T::template multiply<decltype(half)::value>(f, f, i, acc);
       });
@@ -801,11 +871,11 @@ __global__ void __launch_bounds__(64 * WM * WN * Split, WM * WN * Split == 4 && 
   typedef __attribute__((address_space(3))) const int32_t lds_i32;
   const uint32_t lds_index = lds0 + (uint32_t)(Split - part) * kRing + (uint32_t)waves * kIndexRows;
   const Window wi = Indexed ? window((uint64_t)(uintptr_t)(a.row_index + r.first), 0, 4 * K, 4 * K) : Window{};
-  auto copy_index = [&](int step) {  // a multiple of kIndexSteps
+  auto copy_index = [&](int step) __attribute__((always_inline)) {  // a multiple of kIndexSteps
     const uint32_t at = 4u * (uint32_t)((step0 + step) * T::kStep + (threadIdx.x & 63));
     copy4<0>(wi.buffer(false), uniform(lds_index + (uint32_t)(step / kIndexSteps % kIndexPairs) * 256), at);
   };
-  auto load_rows = [&](int step) {  // where b's rows of a step lie
+  auto load_rows = [&](int step) __attribute__((always_inline)) {  // where b's rows of a step lie
 #pragma unroll
     for (int i = 0; i < PB::kEach; ++i) {
       int row, chunk;
@@ -838,7 +908,7 @@ __global__ void __launch_bounds__(64 * WM * WN * Split, WM * WN * Split == 4 && 
       os[i] = there ? (uint32_t)row * (uint32_t)stride : kNowhere;
     }
   }
-  auto copy_scales = [&](int step) {  // a multiple of kScaleSteps
+  auto copy_scales = [&](int step) __attribute__((always_inline)) {  // a multiple of kScaleSteps
 #pragma unroll
     for (int i = 0; i < kScaleCopies; ++i) {
       const uint32_t to = uniform(lds0 + kStages * T::kLds + (uint32_t)(step / kScaleSteps % kScaleRing) * T::kLdsScales + 1024u * (wave + i * WM * WN));
@@ -848,7 +918,7 @@ __global__ void __launch_bounds__(64 * WM * WN * Split, WM * WN * Split == 4 && 
   };
 
   // One of a step's copies; the last step's rows along the sum may end before its 64 bytes.
-  auto copy = [&](auto piece, int step, bool last) {
+  auto copy = [&](auto piece, int step, bool last) __attribute__((always_inline)) {
     constexpr int p = decltype(piece)::value;
     const uint32_t to = uniform(lds0 + (uint32_t)(step % kStages) * T::kLds + 1024u * wave);
     if constexpr (p < PA::kEach) {
@@ -870,7 +940,7 @@ __global__ void __launch_bounds__(64 * WM * WN * Split, WM * WN * Split == 4 && 
       copy16<T::kLdsA + i * T::kThreads * 16>(wb.buffer(last), to, at);
     }
   };
-  auto advance = [&](int step) {  // behind the copies of `step`
+  auto advance = [&](int step) __attribute__((always_inline)) {  // behind the copies of `step`
     wa.base += wa.move;
     wb.base += wb.move;
     if (Indexed && step + 1 < steps) load_rows(step + 1);
@@ -888,13 +958,13 @@ __global__ void __launch_bounds__(64 * WM * WN * Split, WM * WN * Split == 4 && 
   const typename T::Lane lane = T::lane_of(wm, wn);
   typename T::Fragments f[2];
   constexpr int kLate = F4 || T::kTM < 2 ? 1 : 2, kOnce = T::kTM - kLate;
-  auto from_step = [&](int step, bool tail) -> typename T::From {
+  auto from_step = [&](int step, bool tail) __attribute__((always_inline)) -> typename T::From {
     return T::from_of(lds0 + (uint32_t)(step % kStages) * T::kLds,
                       lds0 + kStages * T::kLds + (uint32_t)(step / kScaleSteps % kScaleRing) * T::kLdsScales + step % kScaleSteps * (4 * Sub),
                       tail ? blocks - 4 * Sub * (step0 + step) : 4 * Sub);
   };
   // Rows along the sum that end within a 16-byte chunk: what was copied behind their end becomes 0.
-  auto cut_last = [&](int step) {
+  auto cut_last = [&](int step) __attribute__((always_inline)) {
     if (F4 || last_bytes % 16 == 0) return;
     constexpr int kRowsAlong = BM + (T::kAcrossB ? 0 : BN);
     typedef __attribute__((address_space(3))) uint16_t lds_u16;
@@ -908,7 +978,7 @@ __global__ void __launch_bounds__(64 * WM * WN * Split, WM * WN * Split == 4 && 
     }
     wait_for_copies<63, Split == 1>();
   };
-  auto turn = [&](auto rows, auto tail, int step, typename T::Fragments &now, typename T::Fragments &next) {
+  auto turn = [&](auto rows, auto tail, int step, typename T::Fragments &now, typename T::Fragments &next) __attribute__((always_inline)) {
     constexpr int Live = decltype(rows)::value;
     constexpr bool Tail = decltype(tail)::value;
     // the next step's operands are there, and nobody reads this step's any more
@@ -920,14 +990,14 @@ __global__ void __launch_bounds__(64 * WM * WN * Split, WM * WN * Split == 4 && 
     if (F4 && ahead % kScaleSteps == 0 && (!Tail || ahead < steps)) copy_scales(ahead);
     if (Indexed && step % kIndexSteps == 0 && step + kIndexSteps * kIndexPairs < steps) copy_index(step + kIndexSteps * kIndexPairs);
     constexpr int kRows = T::kKK * T::kTM;  // of products
-    static_for<kRows>([&](auto row) {
+    static_for<kRows>([&](auto row) __attribute__((always_inline)) {
       constexpr int u = decltype(row)::value, i = u % T::kTM, kk = u / T::kTM;
       if constexpr (u < kLate * T::kKK && kOnce + u / T::kKK < Live) T::read_a(from, lane, kOnce + u / T::kKK, u % T::kKK, next);
-      static_for<T::kKK * T::kTN_>([&](auto col) {
+      static_for<T::kKK * T::kTN_>([&](auto col) __attribute__((always_inline)) {
         constexpr int v = decltype(col)::value;
         if constexpr (v * kRows / (T::kKK * T::kTN_) / 2 == u && Live > 0) T::read_b(from, lane, v % T::kTN_, v / T::kTN_, next);
       });
-      if (!Tail || ahead < steps) static_for<kCopies>([&](auto piece) {
+      if (!Tail || ahead < steps) static_for<kCopies>([&](auto piece) __attribute__((always_inline)) {
           if constexpr (decltype(piece)::value * kRows / kCopies == u) copy(piece, ahead, Tail && ahead == last_step);
         });
       if constexpr (i < Live) T::template multiply<kk>(i < kOnce ? f[0] : now, now, i, acc);
@@ -946,7 +1016,7 @@ __global__ void __launch_bounds__(64 * WM * WN * Split, WM * WN * Split == 4 && 
 #pragma unroll 1
     for (int i = 0; i < kStages && i < steps; ++i) {
       if (F4 && i % kScaleSteps == 0) copy_scales(i);
-      static_for<kCopies>([&](auto piece) { copy(piece, i, i == last_step); });
+      static_for<kCopies>([&](auto piece) __attribute__((always_inline)) { copy(piece, i, i == last_step); });
       advance(i);
     }
     if (steps >= kStages) wait_for_copies<(kStages - 1) * kCopies, Split == 1>();
@@ -954,7 +1024,7 @@ __global__ void __launch_bounds__(64 * WM * WN * Split, WM * WN * Split == 4 && 
     if (Form != kTN && last_step == 0) cut_last(0);
     T::read(from_step(0, true), lane, f[0]);
     // rows: fragments of a that the wave multiplies
-    auto loop = [&](auto rows) {
+    auto loop = [&](auto rows) __attribute__((always_inline)) {
       int step = 0;
 #pragma unroll 1
       for (; step + 1 + kStages < steps - 1; step += 2) {

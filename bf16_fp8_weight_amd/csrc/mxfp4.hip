@@ -10,6 +10,7 @@
 #include <string>
 
 #include "expert_tile.h"
+#include "fp8_math.h"
 #include "hip_util.h"
 #include "plan.h"
 #include "wave.h"
@@ -34,12 +35,14 @@ struct RoundArgs {
 template <bool F32>
 __device__ __forceinline__ void load8(uint64_t x, uint64_t at, int valid, float (&v)[8]) {
   if (F32) {
-    const float *p = (const float *)(uintptr_t)x + at;
+    const uint64_t p = x + 4 * at;
     if (valid >= 8) {
-      __builtin_memcpy(v, p, 32);
+      const f32x4 lo = load_at<f32x4>(p), hi = load_at<f32x4>(p + 16);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = lo[i], v[4 + i] = hi[i];
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = i < valid ? p[i] : 0.0f;
+      for (int i = 0; i < 8; ++i) v[i] = i < valid ? load_at<float>(p + 4 * i) : 0.0f;
     }
   } else {
     const u32x4 w = load_chunk(x + 2 * at, valid);
@@ -82,8 +85,8 @@ __global__ void __launch_bounds__(kThreads) mxfp4_quantize_kernel(RoundArgs a) {
   q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[2], v[3], scale, 1);
   q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[4], v[5], scale, 2);
   q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[6], v[7], scale, 3);
-  *(uint32_t *)(uintptr_t)(a.codes + (uint64_t)((int64_t)i * a.code_stride + c0 / 2)) = bad ? 0u : q;
-  if (l == 0) ((uint8_t *)(uintptr_t)a.scales)[(int64_t)i * a.scale_stride + b] = (uint8_t)c;
+  st_global<uint32_t>(a.codes + (uint64_t)((int64_t)i * a.code_stride + c0 / 2), bad ? 0u : q);
+  if (l == 0) st_global<uint8_t>(a.scales + (uint64_t)((int64_t)i * a.scale_stride + b), (uint8_t)c);
 }
 
 // A code's value times a power of two is exact: values have at most two digits.
@@ -96,8 +99,8 @@ __global__ void __launch_bounds__(kThreads) mxfp4_dequantize_kernel(RoundArgs a)
   const int64_t c0 = 32 * (int64_t)b + 8 * l;
   if (c0 >= a.cols) return;
   const int n = (int)min((int64_t)8, a.cols - c0);
-  const uint32_t q = *(const uint32_t *)(uintptr_t)(a.codes + (uint64_t)((int64_t)i * a.code_stride + c0 / 2));
-  const int c = ((const uint8_t *)(uintptr_t)a.scales)[(int64_t)i * a.scale_stride + b];
+  const uint32_t q = ld_global<uint32_t>(a.codes + (uint64_t)((int64_t)i * a.code_stride + c0 / 2));
+  const int c = ld_global<uint8_t>(a.scales + (uint64_t)((int64_t)i * a.scale_stride + b));
   const float scale = scale_of(c);
   typedef float f32x2 __attribute__((ext_vector_type(2)));
   const f32x2 p[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 0), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.0f, 1),
@@ -105,29 +108,9 @@ __global__ void __launch_bounds__(kThreads) mxfp4_dequantize_kernel(RoundArgs a)
   float v[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = c == 255 ? __uint_as_float(0x7FC00000u) : p[e >> 1][e & 1] * scale;
-  const uint64_t at = (uint64_t)((int64_t)i * a.x_stride + c0);
-  if (F32) {
-    float *o = (float *)(uintptr_t)a.x + at;
-    if (n == 8) {
-      __builtin_memcpy(o, v, 32);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e < n) o[e] = v[e];
-    }
-  } else {
-    __bf16 *o = (__bf16 *)(uintptr_t)a.x + at;
-    bf16x8 r;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) r[e] = (__bf16)v[e];
-    if (n == 8) {
-      __builtin_memcpy(o, &r, 16);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e < n) o[e] = r[e];
-    }
-  }
+  const int64_t at = (int64_t)i * a.x_stride + c0;
+  if (F32) store8<float>(a.x, at, v, n);
+  else store8<__bf16>(a.x, at, v, n);
 }
 
 wt_status check_round(const char *what, int32_t dtype, int64_t n_rows, int64_t n_out, int64_t cols, int64_t x_stride,

@@ -9,6 +9,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,7 +19,7 @@ LIB_PATH = os.path.join(PKG, "libwt.so")
 
 SOURCES = ["plan.cpp", "schedule.cpp", "host_api.cpp", "runtime.cpp", "prep_kernels.hip", "progress.hip", "act_quant.hip",
            "adamw.cpp", "adamw.hip", "router.hip", "dispatch.hip",
-           "expert.cpp", "expert.hip", "mxfp4.hip"]
+           "expert.cpp", "expert.hip", "expert_nt.hip", "expert_nn.hip", "expert_tn.hip", "mxfp4.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
@@ -35,8 +36,8 @@ def build(verbose: bool = False, save_temps_dir: str | None = None, defines=(), 
     `defines` are extra -D options (kernel tuning knobs)."""
     objdir = os.path.join(ROOT, "_build", "default" if not defines else "_".join(d.replace("=", "") for d in defines))
     os.makedirs(objdir, exist_ok=True)
-    objs = []
-    for src in SOURCES:
+
+    def compile_one(src: str) -> str:
         path = os.path.join(CSRC, src)
         obj = os.path.join(objdir, src + ".o")
         cmd = [HIPCC, *COMMON, *DEVICE, *("-D" + d for d in defines), "-c", path, "-o", obj]
@@ -45,7 +46,11 @@ def build(verbose: bool = False, save_temps_dir: str | None = None, defines=(), 
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True, cwd=save_temps_dir or objdir)
-        objs.append(obj)
+        return obj
+
+    # the sources with the most kernels come last in SOURCES: start them first
+    with ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+        objs = list(pool.map(compile_one, reversed(SOURCES)))[::-1]
     target = out or LIB_PATH
     tmp = target + ".tmp%d" % os.getpid()
     link = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]

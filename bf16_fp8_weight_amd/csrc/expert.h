@@ -8,6 +8,8 @@
 
 #include "wt.h"
 
+struct ihipStream_t;  // hipStream_t is a pointer to it
+
 namespace wt {
 
 // What a product's kernel takes. Addresses and strides of a, b and their scales
@@ -42,6 +44,10 @@ wt_status mxfp4_product_args(const char *what, const wt_mxfp4_product_desc *d, P
 
 // The caller's error text, set; returns st.
 wt_status operator_fail(const char *what, const std::string &m, wt_status st = WT_E_INVAL);
+
+// Enqueues a product of form Form (WT_PRODUCT_*): expert_nt.hip, expert_nn.hip, expert_tn.hip.
+template <int Form, Epilogue Epi>
+wt_status run_product(const char *what, const ProductArgs &a, ihipStream_t *stream);
 
 constexpr int64_t kProductMaxRows = (int64_t)1 << 27;
 constexpr int64_t kProductMaxSize = (int64_t)1 << 24;

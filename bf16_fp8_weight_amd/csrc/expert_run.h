@@ -1,0 +1,63 @@
+// expert_run.h -- which kernel a product of given sizes takes, and its launch.
+// Included by one source for each form, which compiles that form's kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <string>
+
+#include "expert_tile.h"
+#include "hip_util.h"
+
+namespace wt {
+
+constexpr int kCus = 256;
+constexpr int64_t kMaxGrid = ((int64_t)1 << 31) - 1;
+
+template <int Form, Epilogue Epi, int BM, int BN, int WM, int WN, int Split, int Sub, int Stages, bool Aligned>
+wt_status launch(const char *what, ProductArgs a, hipStream_t stream) {
+  constexpr int columns = Epi == Epilogue::kGated ? BN / 2 : BN;
+  const int64_t n_tiles = (a.n + columns - 1) / columns;
+  const int64_t grid = grid_of(a, Form, BM, n_tiles);
+  // Measured (us): gradient of 8192 rows of 12 experts x 2048 columns, 304 tiles, 353 with the rests last and 398 without;
+  // x 7168 columns, 1064 tiles, 499 and 473; 16384 rows of 24 experts x 2048 gated, 1216 tiles, 1017 and 937: the rests'
+  // weights are read twice.
+  a.rests_last = grid <= 2 * kCus;
+  if (grid > kMaxGrid) return operator_fail(what, "too many tiles");
+  if (grid == 0) return WT_OK;
+  auto kernel = product_any_kernel<Form, Epi, false, 128, 128, 2, 2, 2>;
+  if constexpr (Aligned) kernel = product_kernel<Form, Epi, false, BM, BN, WM, WN, Split, Sub, Stages, false>;
+  if constexpr (Aligned && Form == kTN)
+    if (a.row_index) kernel = product_kernel<Form, Epi, false, BM, BN, WM, WN, Split, Sub, Stages, true>;
+  hipLaunchKernelGGL(kernel, dim3((uint32_t)grid), dim3(64 * WM * WN * Split), 0, stream, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return operator_fail(what, hip_msg("launch", e), WT_E_HIP);
+  return WT_OK;
+}
+
+// Which kernel. All rules go by the number of tiles (an upper bound, since the rows of each expert are on the device)
+// against 256 CUs. Measured on MI355X, us (k x n; kernel 16 | 64 | 128 x8 | 128 | 256 = rows of a tile, x8: eight waves):
+//   64 rows, 2048 x 2048, NT: 6.7 | 9.7 | 12.6 | 16.2                  200 rows, 512 x 512: 6.3 | 6.2 | 8.3 | 8.1
+//   64 rows, 1024 x 2816 gated: 9.8 | 7.7 | 9.2 | 11.3 | 13.2            256 rows: 26.5 | 15.0 | 12.2 | 12.0 | 26.5
+//   1024 rows, 2048 x 2048, NT: 49.7 | 24.4 | 20.3 | 24.6                1024 rows, 1024 x 2816 gated: - | 44.6 | 20.1 | 17.3 | 27.8
+//   1003 rows of 5 experts, NN, 2736 x 1000: 41.4 | 31.4 | 30.9 | 36.6 | 54.8
+//   4096 rows, 4096 x 4096, NT: - | - | 152 | 114 | 106                  TN: - | - | 132 | 117 | 102
+//   2000 rows of 24 experts, 7168 x 2048 gated: - | - | 372 | 300 | 336; 8192 cubed, NT: - | - | 1196 | 1010 | 804
+//   256 rows of 96 experts, 7168 x 2048 gated: 945 | 986 | 868 | 859 | 981; 2048 x 7168: 492 | 532 | 418 | 445 | 462
+// A tile's copies are what bounds the small ones: 64 x 64 moves twice the bytes of 128 x 128 for each product. Waves that split
+// the sum shorten the chain of steps when there is less than a tile for each CU; 256 x 256 pays from one round of tiles on.
+template <int Form, Epilogue Epi>
+wt_status run_product(const char *what, const ProductArgs &a, hipStream_t stream) {
+  if (!product_aligned(a, Form, Epi)) return launch<Form, Epi, 128, 128, 2, 2, 1, 2, 2, false>(what, a, stream);
+  const int64_t halves = Epi == Epilogue::kGated ? 2 : 1;  // of a tile's columns are out's
+  auto tiles = [&](int rows, int columns) { return grid_of(a, Form, rows, (a.n * halves + columns - 1) / columns); };
+  if constexpr (Form != kTN)
+    if (tiles(16, 64) <= kCus) return launch<Form, Epi, 16, 64, 1, 1, 8, 2, 2, true>(what, a, stream);
+  if (tiles(64, 64) <= kCus) return launch<Form, Epi, 64, 64, 1, 1, 4, 1, 4, true>(what, a, stream);
+  if (tiles(256, 256) >= kCus && (Form == kTN || a.n_rows >= 128 * (int64_t)a.n_experts))
+    return launch<Form, Epi, 256, 256, 2, 4, 1, 1, 4, true>(what, a, stream);
+  return tiles(128, 128) >= kCus ? launch<Form, Epi, 128, 128, 2, 2, 1, 2, 2, true>(what, a, stream)
+                                 : launch<Form, Epi, 128, 128, 4, 2, 1, 1, 4, true>(what, a, stream);
+}
+
+}  // namespace wt

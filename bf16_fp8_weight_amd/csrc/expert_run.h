@@ -36,16 +36,18 @@ wt_status launch(const char *what, ProductArgs a, hipStream_t stream) {
 }
 
 // Which kernel. All rules go by the number of tiles (an upper bound, since the rows of each expert are on the device)
-// against 256 CUs. Measured on MI355X, us (k x n; kernel 16 | 64 | 128 x8 | 128 | 256 = rows of a tile, x8: eight waves):
-//   64 rows, 2048 x 2048, NT: 6.7 | 9.7 | 12.6 | 16.2                  200 rows, 512 x 512: 6.3 | 6.2 | 8.3 | 8.1
-//   64 rows, 1024 x 2816 gated: 9.8 | 7.7 | 9.2 | 11.3 | 13.2            256 rows: 26.5 | 15.0 | 12.2 | 12.0 | 26.5
-//   1024 rows, 2048 x 2048, NT: 49.7 | 24.4 | 20.3 | 24.6                1024 rows, 1024 x 2816 gated: - | 44.6 | 20.1 | 17.3 | 27.8
-//   1003 rows of 5 experts, NN, 2736 x 1000: 41.4 | 31.4 | 30.9 | 36.6 | 54.8
-//   4096 rows, 4096 x 4096, NT: - | - | 152 | 114 | 106                  TN: - | - | 132 | 117 | 102
-//   2000 rows of 24 experts, 7168 x 2048 gated: - | - | 372 | 300 | 336; 8192 cubed, NT: - | - | 1196 | 1010 | 804
-//   256 rows of 96 experts, 7168 x 2048 gated: 945 | 986 | 868 | 859 | 981; 2048 x 7168: 492 | 532 | 418 | 445 | 462
-// A tile's copies are what bounds the small ones: 64 x 64 moves twice the bytes of 128 x 128 for each product. Waves that split
-// the sum shorten the chain of steps when there is less than a tile for each CU; 256 x 256 pays from one round of tiles on.
+// against 256 CUs. Measured on MI355X, us (k x n; kernel 16 | 64 | 64w = 64 x 128 | 128x = eight waves | 128 | 256 = rows of a tile):
+//   64 rows, 2048 x 2048, NT: 6.7 | 9.0 | 13.0 | 12.6 | 16.1          64 rows, 1024 x 2816 gated: 9.8 | 7.4 | - | 9.2 | 11.3 | 13.2
+//   200 rows, 512 x 512, NN: 6.3 | 5.9 | 6.9 | 8.8 | 8.3              256 rows, 2816 x 1024 gated: 26.5 | 11.6 | 16.5 | 23.0 | 22.5
+//   512 rows, 2048 x 2048, NT: - | 12.2 | 13.3 | 18.0 | 17.6          256 rows, 1024 x 2816 gated: - | 11.0 | 9.6 | 12.3 | 12.1
+//   1024 rows, 2048 x 2048, NT: 49.7 | 21.1 | 15.5 | 20.3 | 24.5      1024 rows, 2816 x 1024 gated: - | 28.4 | 21.3 | 27.2 | 32.3
+//   1003 rows of 5 experts, NN, 2736 x 1000: 41.4 | 29.8 | 21.8 | 30.9 | 36.6 | 54.8; 2048 rows, NT, 2048 x 1536: - | 30.6 | 25.2 | 20.8 | 24.9
+//   4096 rows, 4096 x 4096, NT: - | - | - | 152 | 114 | 106           TN: - | - | - | 132 | 117 | 102
+//   2000 rows of 24 experts, 7168 x 2048 gated: - | - | - | 372 | 300 | 336; 8192 cubed, NT: - | - | - | 1196 | 1010 | 804
+//   256 rows of 96 experts, 7168 x 2048 gated: 945 | 986 | - | 868 | 859 | 981; 2048 x 7168: 492 | 532 | - | 418 | 445 | 462
+// A tile's way through shared memory is what bounds the small ones (a step of 64 x 128 takes 0.13 us, of 128 x 128 0.2 to
+// 0.25), so they pay as long as each has a CU of its own. Waves that split the sum shorten the chain of steps (two stages,
+// which leave room for two workgroups, are up to 7 % faster than four); 256 x 256 pays from one round of tiles on.
 template <int Form, Epilogue Epi>
 wt_status run_product(const char *what, const ProductArgs &a, hipStream_t stream) {
   if (!product_aligned(a, Form, Epi)) return launch<Form, Epi, 128, 128, 2, 2, 1, 2, 2, false>(what, a, stream);
@@ -53,7 +55,8 @@ wt_status run_product(const char *what, const ProductArgs &a, hipStream_t stream
   auto tiles = [&](int rows, int columns) { return grid_of(a, Form, rows, (a.n * halves + columns - 1) / columns); };
   if constexpr (Form != kTN)
     if (tiles(16, 64) <= kCus) return launch<Form, Epi, 16, 64, 1, 1, 8, 2, 2, true>(what, a, stream);
-  if (tiles(64, 64) <= kCus) return launch<Form, Epi, 64, 64, 1, 1, 4, 1, 4, true>(what, a, stream);
+  if (tiles(64, 64) <= kCus) return launch<Form, Epi, 64, 64, 1, 1, 4, 1, 2, true>(what, a, stream);
+  if (tiles(64, 128) <= kCus) return launch<Form, Epi, 64, 128, 2, 2, 1, 1, 4, true>(what, a, stream);
   if (tiles(256, 256) >= kCus && (Form == kTN || a.n_rows >= 128 * (int64_t)a.n_experts))
     return launch<Form, Epi, 256, 256, 2, 4, 1, 1, 4, true>(what, a, stream);
   return tiles(128, 128) >= kCus ? launch<Form, Epi, 128, 128, 2, 2, 1, 2, 2, true>(what, a, stream)

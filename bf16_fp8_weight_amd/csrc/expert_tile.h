@@ -246,7 +246,8 @@ __device__ __forceinline__ bool find_matrix(const ProductArgs &a, uint32_t block
 // Workgroups that deal out all tiles.
 inline int64_t grid_of(const ProductArgs &a, int form, int bm, int64_t n_tiles) {
   if (form == kTN) return (((int64_t)(a.m + bm - 1) / bm * n_tiles + kXcds - 1) / kXcds) * kXcds * a.n_experts;
-  const int64_t rests = a.n_rows < a.n_experts ? a.n_rows : a.n_experts;
+  // experts' last tiles; how many there are is known here for a dense layer
+  const int64_t rests = !a.offsets ? a.n_rows % bm != 0 : a.n_rows < a.n_experts ? a.n_rows : a.n_experts;
   return ((a.n_rows / bm * n_tiles + kXcds - 1) / kXcds + (rests * n_tiles + kXcds - 1) / kXcds) * kXcds;
 }
 

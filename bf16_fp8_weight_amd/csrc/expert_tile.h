@@ -801,7 +801,8 @@ __global__ void __launch_bounds__(64 * WM * WN * Split, WM * WN * Split == 4 && 
   static_assert(Split == 1 || (WM == 1 && WN == 1), "a wave has the whole tile or the whole sum");
   constexpr int kIndexSteps = 2 / Sub, kIndexPairs = kStages / kIndexSteps + 2,
                 kIndexRows = Indexed ? 256 * kIndexPairs : 0;  // of a wave: 64 row numbers, that is steps; how often; bytes
-  constexpr int kScaleRing = kStages / kScaleSteps + 1;
+  // rows of scales: those of the steps that are copied ahead, and of the present step's
+  constexpr int kScaleRing = (kStages + kScaleSteps - 1) / kScaleSteps + 1;
   constexpr int kRing = kStages * T::kLds + kScaleRing * T::kLdsScales;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Split * kRing + WM * WN * Split * kIndexRows];
   Rows r;

@@ -546,11 +546,18 @@ wt_status wt_dispatch_rows(const int32_t *index, int64_t n_tokens, int32_t top_k
  *
  * A NaN or an infinity in an operand reaches exactly the results whose sum it is
  * part of. Sums run in an order that depends on the sizes alone: a call repeats
- * bit for bit. Arrays with rows (and TN's out) whose strides are multiples of 8
- * elements and whose addresses are multiples of 16 bytes, with even sizes (k a
- * multiple of 8 in NT, and for a in NN), take the fast path; any other shape a
- * general one, same results to rounding. No workspace; every call may be
- * captured. Calls on the same arrays must be ordered. */
+ * bit for bit.
+ *
+ * Speed. Arrays whose addresses, row and expert strides are even numbers of
+ * elements, with even sizes (NT: k; NN: k and n; TN: m and n) and spans below
+ * 2^31 bytes (256 rows of any operand, a gathered array as a whole, an expert's gate
+ * and up rows) are copied to shared memory 16 bytes at a time; all others pass through
+ * registers, with the same results to rounding (2001 rows, k = 4001, n = 777, us: NT 76
+ * against 28 for 2000 rows, k = 4000, n = 776; NN 106 against 26; 4001 x 777 weights' gradient 61 against 21).
+ *
+ * out must not overlap an operand, with one exception: wt_gated_backward may write over
+ * pre (out = pre, out_stride = pre_stride). No workspace; every call may be captured.
+ * Calls on the same arrays must be ordered. */
 enum { WT_PRODUCT_NT = 0, WT_PRODUCT_NN = 1, WT_PRODUCT_TN = 2 };
 enum { WT_ACT_SILU = 0, WT_ACT_GELU = 1 };
 
@@ -628,7 +635,9 @@ wt_status wt_mxfp4_dequantize(const void *codes, int64_t code_row_stride, const 
  * are the expert's own (gather while quantizing). Strides of codes and scales are in bytes.
  * Codes: 16-byte aligned, strides multiples of 16 and rows >= 16 ceil(k / 32) bytes whose codes
  * beyond k are 0, as wt_mxfp4_quantize writes them; scales: 4-byte aligned,
- * strides multiples of 4, rows >= ceil(k / 32) (WT_E_ALIGN otherwise). */
+ * strides multiples of 4, rows >= ceil(k / 32) (WT_E_ALIGN otherwise). Scales are read in
+ * whole words of 4 bytes: up to 3 bytes behind a row's last scale are read and not used, so
+ * that the allocation has to reach to the end of the last row's last word. */
 typedef struct wt_mxfp4_product_desc {
   int64_t n_rows;          /* 0 .. 2^27 */
   int32_t n_experts;       /* 1 .. 1024 */

@@ -25,8 +25,10 @@ wt_status launch(const char *what, ProductArgs a, hipStream_t stream) {
   a.rests_last = grid <= 2 * kCus;
   if (grid > kMaxGrid) return operator_fail(what, "too many tiles");
   if (grid == 0) return WT_OK;
-  auto kernel = product_any_kernel<Form, Epi, false, 128, 128, 2, 2, 2>;
-  if constexpr (Aligned) kernel = product_kernel<Form, Epi, false, BM, BN, WM, WN, Split, Sub, Stages, false>;
+  auto kernel = [] {
+    if constexpr (Aligned) return product_kernel<Form, Epi, false, BM, BN, WM, WN, Split, Sub, Stages, false>;
+    else return product_any_kernel<Form, Epi, false, BM, BN, WM, WN, Sub>;
+  }();
   if constexpr (Aligned && Form == kTN)
     if (a.row_index) kernel = product_kernel<Form, Epi, false, BM, BN, WM, WN, Split, Sub, Stages, true>;
   hipLaunchKernelGGL(kernel, dim3((uint32_t)grid), dim3(64 * WM * WN * Split), 0, stream, a);
@@ -48,11 +50,16 @@ wt_status launch(const char *what, ProductArgs a, hipStream_t stream) {
 // A tile's way through shared memory is what bounds the small ones (a step of 64 x 128 takes 0.13 us, of 128 x 128 0.2 to
 // 0.25), so they pay as long as each has a CU of its own. Waves that split the sum shorten the chain of steps (two stages,
 // which leave room for two workgroups, are up to 7 % faster than four); 256 x 256 pays from one round of tiles on.
+// Any alignment (64 | 64 x 128 | 128): 2001 rows, 4001 x 777, NT 49 | 61 | 76, NN 68 | 76 | 106, its TN 56 | 57 | 61; 777 x 4001
+// NT 43 | 39 | 29; 333 rows, 501 x 1001 gated 9.4 | 12.1 | 16.9; 8001 rows, 4097 x 4097 655 | 538 | 437.
 template <int Form, Epilogue Epi>
 wt_status run_product(const char *what, const ProductArgs &a, hipStream_t stream) {
-  if (!product_aligned(a, Form, Epi)) return launch<Form, Epi, 128, 128, 2, 2, 1, 2, 2, false>(what, a, stream);
   const int64_t halves = Epi == Epilogue::kGated ? 2 : 1;  // of a tile's columns are out's
   auto tiles = [&](int rows, int columns) { return grid_of(a, Form, rows, (a.n * halves + columns - 1) / columns); };
+  if (!product_aligned(a, Form, Epi)) {
+    if (tiles(128, 128) >= kCus) return launch<Form, Epi, 128, 128, 2, 2, 1, 2, 2, false>(what, a, stream);
+    return launch<Form, Epi, 64, 64, Form == kNT ? 4 : 2, Form == kNT ? 1 : 2, 1, 2, 2, false>(what, a, stream);
+  }
   if constexpr (Form != kTN)
     if (tiles(16, 64) <= kCus) return launch<Form, Epi, 16, 64, 1, 1, 8, 2, 2, true>(what, a, stream);
   if (tiles(64, 64) <= kCus) return launch<Form, Epi, 64, 64, 1, 1, 4, 1, 2, true>(what, a, stream);

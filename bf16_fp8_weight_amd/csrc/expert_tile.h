@@ -23,7 +23,7 @@
 // random BF16 values. 8192 x 8192 x 8192: NT 1365 TFLOP/s, NN 1409, TN 1425, MXFP4 3730 to 3800. With few
 // rows it is bound by the weights' bytes (24 to 96 experts' weights at 6.3 to 6.9 TB/s), with few of both
 // by the chain of steps. product_any_kernel (any stride) is bound by loads that
-// straddle cache lines: 2001 rows x 777 x 4001 NT 76 us, NN 106.
+// straddle cache lines: 2001 rows, 4001 x 777, NT 49 us, NN 68; 8001 rows, 4097 x 4097, 437 us (615 TFLOP/s).
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -1,5 +1,6 @@
 """Sizes between those of test_gpu_expert_tiles: they reach the kernels of 64 x 128
-tiles, and MXFP4's of 64 rows whose waves split the sum."""
+tiles, MXFP4's of 64 rows whose waves split the sum, and with odd sizes the larger
+tiles of operands at any alignment."""
 import pytest
 
 import expert_ref as R
@@ -8,7 +9,8 @@ import test_gpu_expert_tiles as tiles
 pytestmark = pytest.mark.gpu
 
 SHAPES = [("64 x 128", R.Layout([701]), 2002, 202), ("64 x 128, experts", R.Layout([300, 0, 257, 65, 64, 1], lead=1, tail=70), 1102, 998),
-          ("64 x 128, few steps", R.Layout([1024]), 2048, 30)]
+          ("64 x 128, few steps", R.Layout([1024]), 2048, 30), ("odd", R.Layout([2101]), 2103, 133),
+          ("odd, experts", tiles.EIGHT, 3333, 71)]
 IDS = [s[0].replace(" ", "") for s in SHAPES]
 MX_SHAPES = [("64, split", R.Layout([500]), 2002, 1000), ("64, experts", R.Layout([100, 0, 77, 200, 65, 64], lead=2, tail=40), 1030, 3000),
              ("64, few steps", R.Layout([512]), 2048, 33)]
@@ -27,7 +29,8 @@ def test_products(wt, form, gathered, name, lay, n, k):
     tiles.test_products(wt, form, gathered, name, lay, n, k)
 
 
-@pytest.mark.parametrize("m,n,lay", [(702, 2000, R.Layout([300])), (260, 1002, R.Layout([100, 0, 33, 700])), (1024, 2048, R.Layout([31]))])
+@pytest.mark.parametrize("m,n,lay", [(702, 2000, R.Layout([300])), (260, 1002, R.Layout([100, 0, 33, 700])), (1024, 2048, R.Layout([31])),
+                                     (2101, 2049, R.Layout([77])), (801, 777, R.Layout([65, 0, 500, 64, 1, 129]))])
 @pytest.mark.parametrize("gathered", [False, True])
 def test_gradients_of_weights(wt, gathered, m, n, lay):
     tiles.test_gradients_of_weights(wt, gathered, m, n, lay)

@@ -590,7 +590,7 @@ def wt_dispatch_rows(index: int, n_tokens: int, top_k: int, n_experts: int, row_
                                 stream or None))
 
 
-# ------------------------------------------------------------- optimizer step
+# ------------------------------------------------------- experts' products, MXFP4
 def wt_product_desc_init() -> wt_product_desc:
     d = wt_product_desc()
     lib.wt_product_desc_init(ctypes.byref(d))
@@ -631,6 +631,7 @@ def wt_mxfp4_product(desc: wt_mxfp4_product_desc, stream: int = 0) -> None:
     _check(lib.wt_mxfp4_product(ctypes.byref(desc), stream or None))
 
 
+# ------------------------------------------------------------- optimizer step
 def wt_adamw_options_init() -> wt_adamw_options:
     o = wt_adamw_options()
     lib.wt_adamw_options_init(ctypes.byref(o))

@@ -550,7 +550,7 @@ wt_status wt_dispatch_rows(const int32_t *index, int64_t n_tokens, int32_t top_k
  *
  * Speed. Arrays whose addresses, row and expert strides are even numbers of
  * elements, with even sizes (NT: k; NN: k and n; TN: m and n) and spans below
- * 2^31 bytes (256 rows of any operand, a gathered array as a whole, an expert's gate
+ * 2^31 bytes (512 rows of any operand, a gathered array as a whole, an expert's gate
  * and up rows) are copied to shared memory 16 bytes at a time; all others pass through
  * registers, with the same results to rounding (2001 rows, k = 4001, n = 777, us: NT 49
  * against 28 for 2000 rows, k = 4000, n = 776; NN 68 against 26; 4001 x 777 weights' gradient 56 against 21).

@@ -49,8 +49,9 @@ wt_status launch(const char *what, ProductArgs a, hipStream_t stream) {
 //   256 rows of 96 experts, 7168 x 2048 gated: 945 | 986 | - | 868 | 859 | 981; 2048 x 7168: 492 | 532 | - | 418 | 445 | 462
 // A tile's way through shared memory is what bounds the small ones (a step of 64 x 128 takes 0.13 us, of 128 x 128 0.2 to
 // 0.25), so they pay as long as each has a CU of its own. Waves that split the sum shorten the chain of steps (two stages,
-// which leave room for two workgroups, are up to 7 % faster than four); 256 x 256 pays from one round of tiles on,
-// if experts fill them (rows an expert, 128 | 256): 24 x 7168 x 2048 gated: 83: 300 | 336, 250: 530 | 553, 400: 720 | 716, 500: 839 |
+// which leave room for two workgroups, are up to 7 % faster than four); 256 x 256 pays from two thirds of a round of
+// tiles on (128 | 256: 121 tiles, 2800 rows, 4096 x 2800 NT 62 | 78; 180, 2944 rows, 2048 x 3840 NT 53.5 | 46.5, NN 55 | 46.6; 203, 7312
+// rows, 2560 x 864 gated 74 | 62), if experts fill them (rows an expert, 128 | 256): 24 x 7168 x 2048 gated: 83: 300 | 336, 250: 530 | 553, 400: 720 | 716, 500: 839 |
 // 750; 16 x 4096 x 4096 NT: 200: 166 | 197, 256: 205 | 226, 400: 273 | 234. (256 x 128 and 128 x 256: 683 rows of 12 experts, 7168 x 2048
 // through the gate 365 and 342 against 346; 24 experts' gated batch 1139 and 1109 against 925.)
 // Any alignment (64 | 64 x 128 | 128): 2001 rows, 4001 x 777, NT 49 | 61 | 76, NN 68 | 76 | 106, its TN 56 | 57 | 61; 777 x 4001
@@ -67,7 +68,7 @@ wt_status run_product(const char *what, const ProductArgs &a, hipStream_t stream
     if (tiles(16, 64) <= kCus) return launch<Form, Epi, 16, 64, 1, 1, 8, 2, 2, true>(what, a, stream);
   if (tiles(64, 64) <= kCus) return launch<Form, Epi, 64, 64, 1, 1, 4, 1, 2, true>(what, a, stream);
   if (tiles(64, 128) <= kCus) return launch<Form, Epi, 64, 128, 2, 2, 1, 1, 4, true>(what, a, stream);
-  if (tiles(256, 256) >= kCus && (Form == kTN || a.n_rows > 256 * (int64_t)a.n_experts))
+  if (3 * tiles(256, 256) >= 2 * kCus && (Form == kTN || a.n_rows > 256 * (int64_t)a.n_experts))
     return launch<Form, Epi, 256, 256, 2, 4, 1, 1, 4, true>(what, a, stream);
   return tiles(128, 128) >= kCus ? launch<Form, Epi, 128, 128, 2, 2, 1, 2, 2, true>(what, a, stream)
                                  : launch<Form, Epi, 128, 128, 4, 2, 1, 1, 4, true>(what, a, stream);

@@ -150,7 +150,8 @@ wt_status launch(const char *what, ProductArgs a, hipStream_t stream) {
 // 7.1 | 8.3 | 12.1; 64 rows, 1024 x 2816 gated 6.3 | 6.5 | 7.9 | 9.9; 100 rows, 7168 x 4096 9.4 | 12.4 | 17.1 | 27.4; 256 rows, 2816 x 1024
 // gated 7.3 | 7.8 | 10.9 | 23.8; 512 rows, 2048 x 2048 10.4 | 7.1 | 9.2 | 19.1; 1024 rows 19.3 | 9.5 | 9.6 | 19.4; 2048 rows, 4096 x 4096
 // 94.5 | 47.2 | 26.2 | 33.0; 4096 rows - | - | 49.1 | 46.7; 256 rows of 96 experts, 7168 x 2048 gated 300 | - | 258 | 304; 2000 rows of 24
-// experts - | - | 100 | 108; 6000 rows 181 | 193; 9600 rows 241 | 246; 12000 rows 286 | 252; 8192 cubed - | - | 327 | 296.
+// experts - | - | 100 | 108; 6000 rows 181 | 193; 9600 rows 241 | 246; 12000 rows 286 | 252; 180 tiles of 256, 2944 rows, 7168 x 3840 59 |
+// 52.5, 2048 x 3840 22.8 | 24.1; 8192 cubed - | - | 327 | 296.
 template <Epilogue Epi>
 wt_status run(const char *what, const ProductArgs &a, hipStream_t stream) {
   const int64_t far = (int64_t)1 << 31;
@@ -162,7 +163,7 @@ wt_status run(const char *what, const ProductArgs &a, hipStream_t stream) {
   auto tiles = [&](int rows, int columns) { return grid_of(a, kNT, rows, (a.n * halves + columns - 1) / columns); };
   if (tiles(32, 64) <= kCus) return launch<Epi, 32, 64, 1, 1, 4, 2, 2, true>(what, a, stream);
   if (tiles(64, 64) <= kCus) return launch<Epi, 64, 64, 1, 1, 4, 1, 2, true>(what, a, stream);
-  if (tiles(256, 256) >= kCus && a.n_rows > 256 * (int64_t)a.n_experts) return launch<Epi, 256, 256, 2, 4, 1, 1, 4, true>(what, a, stream);
+  if (3 * tiles(256, 256) >= 2 * kCus && a.n_rows > 256 * (int64_t)a.n_experts) return launch<Epi, 256, 256, 2, 4, 1, 1, 4, true>(what, a, stream);
   return launch<Epi, 128, 128, 2, 2, 1, 2, 2, true>(what, a, stream);
 }
 

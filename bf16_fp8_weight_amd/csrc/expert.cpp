@@ -1,5 +1,5 @@
 // expert.cpp -- the checks of the experts' products: a description is refused
-// here or becomes the arguments of a kernel. No GPU call.
+// here or becomes the arguments of a kernel -- and which kernel that is. No GPU call.
 #include "expert.h"
 
 #include <cstring>
@@ -166,6 +166,64 @@ bool product_aligned(const ProductArgs &a, int form, Epilogue epi) {
   if (epi == Epilogue::kGated && (int64_t)(a.n + 512) * a.b_stride >= far) return false;
   if (tn) return a.m % 2 == 0 && a.n % 2 == 0;
   return a.k % 2 == 0 && (form == WT_PRODUCT_NT || a.n % 2 == 0);
+}
+
+int64_t grid_of(const ProductArgs &a, int form, int bm, int64_t n_tiles) {
+  if (form == WT_PRODUCT_TN) return (((int64_t)(a.m + bm - 1) / bm * n_tiles + kXcds - 1) / kXcds) * kXcds * a.n_experts;
+  // experts' last tiles; how many there are is known here for a dense layer
+  const int64_t rests = !a.offsets ? a.n_rows % bm != 0 : a.n_rows < a.n_experts ? a.n_rows : a.n_experts;
+  return ((a.n_rows / bm * n_tiles + kXcds - 1) / kXcds + (rests * n_tiles + kXcds - 1) / kXcds) * kXcds;
+}
+
+// Which kernel. All rules go by the number of tiles (an upper bound, since the rows of each expert are on the device)
+// against 256 CUs. Measured on MI355X, us (k x n; kernel 16 | 64 | 64w = 64 x 128 | 128x = eight waves | 128 | 256 = rows of a tile):
+//   64 rows, 2048 x 2048, NT: 6.7 | 9.0 | 13.0 | 12.6 | 16.1          64 rows, 1024 x 2816 gated: 9.8 | 7.4 | - | 9.2 | 11.3 | 13.2
+//   200 rows, 512 x 512, NN: 6.3 | 5.9 | 6.9 | 8.8 | 8.3              256 rows, 2816 x 1024 gated: 26.5 | 11.6 | 16.5 | 23.0 | 22.5
+//   512 rows, 2048 x 2048, NT: - | 12.2 | 13.3 | 18.0 | 17.6          256 rows, 1024 x 2816 gated: - | 11.0 | 9.6 | 12.3 | 12.1
+//   1024 rows, 2048 x 2048, NT: 49.7 | 21.1 | 15.5 | 20.3 | 24.5      1024 rows, 2816 x 1024 gated: - | 28.4 | 21.3 | 27.2 | 32.3
+//   1003 rows of 5 experts, NN, 2736 x 1000: 41.4 | 29.8 | 21.8 | 30.9 | 36.6 | 54.8; 2048 rows, NT, 2048 x 1536: - | 30.6 | 25.2 | 20.8 | 24.9
+//   4096 rows, 4096 x 4096, NT: - | - | - | 152 | 114 | 106           TN: - | - | - | 132 | 117 | 102
+//   2000 rows of 24 experts, 7168 x 2048 gated: - | - | - | 372 | 300 | 336; 8192 cubed, NT: - | - | - | 1196 | 1010 | 804
+//   256 rows of 96 experts, 7168 x 2048 gated: 945 | 986 | - | 868 | 859 | 981; 2048 x 7168: 492 | 532 | - | 418 | 445 | 462
+// A tile's way through shared memory is what bounds the small ones (a step of 64 x 128 takes 0.13 us, of 128 x 128 0.2 to
+// 0.25), so they pay as long as each has a CU of its own. Waves that split the sum shorten the chain of steps (two stages,
+// which leave room for two workgroups, are up to 7 % faster than four); 256 x 256 pays from two thirds of a round of
+// tiles on (128 | 256: 121 tiles, 2800 rows, 4096 x 2800 NT 62 | 78; 180, 2944 rows, 2048 x 3840 NT 53.5 | 46.5, NN 55 | 46.6; 203, 7312
+// rows, 2560 x 864 gated 74 | 62), if experts fill them (rows an expert, 128 | 256): 24 x 7168 x 2048 gated: 83: 300 | 336, 250: 530 | 553, 400: 720 | 716, 500: 839 |
+// 750; 16 x 4096 x 4096 NT: 200: 166 | 197, 256: 205 | 226, 400: 273 | 234. (256 x 128 and 128 x 256: 683 rows of 12 experts, 7168 x 2048
+// through the gate 365 and 342 against 346; 24 experts' gated batch 1139 and 1109 against 925.)
+// Any alignment (64 | 64 x 128 | 128): 2001 rows, 4001 x 777, NT 49 | 61 | 76, NN 68 | 76 | 106, its TN 56 | 57 | 61; 777 x 4001
+// NT 43 | 39 | 29; 333 rows, 501 x 1001 gated 9.4 | 12.1 | 16.9; 8001 rows, 4097 x 4097 655 | 538 | 437.
+Kernel product_kernel_of(const ProductArgs &a, int form, Epilogue epi) {
+  const bool tn = form == WT_PRODUCT_TN;
+  const int64_t halves = epi == Epilogue::kGated ? 2 : 1;  // of a tile's columns are out's
+  auto tiles = [&](int rows, int columns) { return grid_of(a, form, rows, (a.n * halves + columns - 1) / columns); };
+  if (!product_aligned(a, form, epi)) return tiles(128, 128) >= kCus ? Kernel::kAny128 : Kernel::kAny64;
+  if (!tn && tiles(16, 64) <= kCus) return Kernel::k16Split;
+  if (tiles(64, 64) <= kCus) return Kernel::k64Split;
+  if (tiles(64, 128) <= kCus) return Kernel::k64x128;
+  if (3 * tiles(256, 256) >= 2 * kCus && (tn || a.n_rows > 256 * (int64_t)a.n_experts)) return Kernel::k256;
+  return tiles(128, 128) >= kCus ? Kernel::k128 : Kernel::k128Wide;
+}
+
+// Which kernel, as for product_kernel_of(). Measured on MI355X, us (k x n; kernel 32 | 64 | 128 | 256 = rows of a tile): one row, 2816 x 1024 6.6 |
+// 7.1 | 8.3 | 12.1; 64 rows, 1024 x 2816 gated 6.3 | 6.5 | 7.9 | 9.9; 100 rows, 7168 x 4096 9.4 | 12.4 | 17.1 | 27.4; 256 rows, 2816 x 1024
+// gated 7.3 | 7.8 | 10.9 | 23.8; 512 rows, 2048 x 2048 10.4 | 7.1 | 9.2 | 19.1; 1024 rows 19.3 | 9.5 | 9.6 | 19.4; 2048 rows, 4096 x 4096
+// 94.5 | 47.2 | 26.2 | 33.0; 4096 rows - | - | 49.1 | 46.7; 256 rows of 96 experts, 7168 x 2048 gated 300 | - | 258 | 304; 2000 rows of 24
+// experts - | - | 100 | 108; 6000 rows 181 | 193; 9600 rows 241 | 246; 12000 rows 286 | 252; 180 tiles of 256, 2944 rows, 7168 x 3840 59 |
+// 52.5, 2048 x 3840 22.8 | 24.1; 8192 cubed - | - | 327 | 296.
+Kernel mxfp4_kernel_of(const ProductArgs &a, Epilogue epi) {
+  const int64_t far = (int64_t)1 << 31;
+  // 31-bit offsets within a tile's rows, as in product_aligned()
+  const bool near = a.a_stride <= far / 512 && a.b_stride <= far / 512 && (int64_t)(a.n + 512) * a.b_stride < far &&
+                    a.a_scale_stride <= far / 512 && a.b_scale_stride <= far / 512 && (int64_t)(a.n + 512) * a.b_scale_stride < far;
+  if (!near) return Kernel::kAny128;
+  const int64_t halves = epi == Epilogue::kGated ? 2 : 1;
+  auto tiles = [&](int rows, int columns) { return grid_of(a, WT_PRODUCT_NT, rows, (a.n * halves + columns - 1) / columns); };
+  if (tiles(32, 64) <= kCus) return Kernel::k32Split;
+  if (tiles(64, 64) <= kCus) return Kernel::k64Split;
+  if (3 * tiles(256, 256) >= 2 * kCus && a.n_rows > 256 * (int64_t)a.n_experts) return Kernel::k256;
+  return Kernel::k128;
 }
 
 }  // namespace wt

@@ -1,5 +1,5 @@
 // expert.h -- what the experts' products share between their host checks
-// (expert.cpp, no GPU call) and their kernels (expert_tile.h, expert.hip,
+// (expert.cpp, no GPU call: checks, choice of a kernel) and their kernels (expert_tile.h, expert.hip,
 // mxfp4.hip).
 #pragma once
 
@@ -35,6 +35,18 @@ enum class Epilogue { kPlain, kGated, kGatedBack };
 // multiples of 4 bytes; a tile's rows, a gathered array and an expert's gate rows
 // span less than 2^31 bytes.
 bool product_aligned(const ProductArgs &a, int form, Epilogue epi);
+
+constexpr int kCus = 256;
+constexpr int kXcds = 8;
+
+// Workgroups that deal out all tiles of bm rows and n_tiles columns of tiles.
+int64_t grid_of(const ProductArgs &a, int form, int bm, int64_t n_tiles);
+
+// Which kernel a product takes: rows x columns of its tiles; kAny: operands of any alignment, kSplit: waves that split the sum,
+// kWide: eight waves to a tile of 128 x 128.
+enum class Kernel { kAny64, kAny128, k16Split, k32Split, k64Split, k64x128, k128, k128Wide, k256 };
+Kernel product_kernel_of(const ProductArgs &a, int form, Epilogue epi);
+Kernel mxfp4_kernel_of(const ProductArgs &a, Epilogue epi);
 
 // Fills *a from a description that it has checked; `what` names the call in the
 // thread's error text.

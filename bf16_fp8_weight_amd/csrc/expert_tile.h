@@ -131,7 +131,7 @@ __device__ __forceinline__ uint32_t last_lane(uint32_t x) { return (uint32_t)__b
 // Workgroups go round the 8 XCDs, each with an L2 of its own: tiles are dealt so that
 // an XCD's are neighbours. Up to kRowGroup row tiles take turns under one
 // column tile, so that what the XCD's 32 CUs read at a time are few rows of both operands.
-constexpr int kXcds = 8, kRowGroup = 8;
+constexpr int kRowGroup = 8;
 
 // Place u among m_tiles x n_tiles tiles.
 __device__ __forceinline__ void place_tile(uint32_t u, uint32_t m_tiles, uint32_t n_tiles, int &mt, int &nt) {
@@ -241,14 +241,6 @@ __device__ __forceinline__ bool find_matrix(const ProductArgs &a, uint32_t block
   }
   place_tile(u, m_tiles, n_tiles, mt, nt);
   return true;
-}
-
-// Workgroups that deal out all tiles.
-inline int64_t grid_of(const ProductArgs &a, int form, int bm, int64_t n_tiles) {
-  if (form == kTN) return (((int64_t)(a.m + bm - 1) / bm * n_tiles + kXcds - 1) / kXcds) * kXcds * a.n_experts;
-  // experts' last tiles; how many there are is known here for a dense layer
-  const int64_t rests = !a.offsets ? a.n_rows % bm != 0 : a.n_rows < a.n_experts ? a.n_rows : a.n_experts;
-  return ((a.n_rows / bm * n_tiles + kXcds - 1) / kXcds + (rests * n_tiles + kXcds - 1) / kXcds) * kXcds;
 }
 
 // ------------------------------------------------------------ shared memory

@@ -22,7 +22,6 @@
 namespace wt {
 namespace {
 
-constexpr int kCus = 256;
 constexpr int64_t kMaxGrid = ((int64_t)1 << 31) - 1;
 constexpr int kThreads = 256;
 constexpr int kLanes = 4;  // of a block, 8 elements each
@@ -146,25 +145,18 @@ wt_status launch(const char *what, ProductArgs a, hipStream_t stream) {
   return WT_OK;
 }
 
-// Which kernel, as in expert_run.h. Measured on MI355X, us (k x n; kernel 32 | 64 | 128 | 256 = rows of a tile): one row, 2816 x 1024 6.6 |
-// 7.1 | 8.3 | 12.1; 64 rows, 1024 x 2816 gated 6.3 | 6.5 | 7.9 | 9.9; 100 rows, 7168 x 4096 9.4 | 12.4 | 17.1 | 27.4; 256 rows, 2816 x 1024
-// gated 7.3 | 7.8 | 10.9 | 23.8; 512 rows, 2048 x 2048 10.4 | 7.1 | 9.2 | 19.1; 1024 rows 19.3 | 9.5 | 9.6 | 19.4; 2048 rows, 4096 x 4096
-// 94.5 | 47.2 | 26.2 | 33.0; 4096 rows - | - | 49.1 | 46.7; 256 rows of 96 experts, 7168 x 2048 gated 300 | - | 258 | 304; 2000 rows of 24
-// experts - | - | 100 | 108; 6000 rows 181 | 193; 9600 rows 241 | 246; 12000 rows 286 | 252; 180 tiles of 256, 2944 rows, 7168 x 3840 59 |
-// 52.5, 2048 x 3840 22.8 | 24.1; 8192 cubed - | - | 327 | 296.
+// The kernel that mxfp4_kernel_of() names.
 template <Epilogue Epi>
 wt_status run(const char *what, const ProductArgs &a, hipStream_t stream) {
-  const int64_t far = (int64_t)1 << 31;
-  // 31-bit offsets within a tile's rows, as in product_aligned()
-  const bool near = a.a_stride <= far / 512 && a.b_stride <= far / 512 && (int64_t)(a.n + 512) * a.b_stride < far &&
-                    a.a_scale_stride <= far / 512 && a.b_scale_stride <= far / 512 && (int64_t)(a.n + 512) * a.b_scale_stride < far;
-  if (!near) return launch<Epi, 128, 128, 2, 2, 1, 2, 2, false>(what, a, stream);
-  const int64_t halves = Epi == Epilogue::kGated ? 2 : 1;
-  auto tiles = [&](int rows, int columns) { return grid_of(a, kNT, rows, (a.n * halves + columns - 1) / columns); };
-  if (tiles(32, 64) <= kCus) return launch<Epi, 32, 64, 1, 1, 4, 2, 2, true>(what, a, stream);
-  if (tiles(64, 64) <= kCus) return launch<Epi, 64, 64, 1, 1, 4, 1, 2, true>(what, a, stream);
-  if (3 * tiles(256, 256) >= 2 * kCus && a.n_rows > 256 * (int64_t)a.n_experts) return launch<Epi, 256, 256, 2, 4, 1, 1, 4, true>(what, a, stream);
-  return launch<Epi, 128, 128, 2, 2, 1, 2, 2, true>(what, a, stream);
+  switch (mxfp4_kernel_of(a, Epi)) {
+    case Kernel::kAny128: return launch<Epi, 128, 128, 2, 2, 1, 2, 2, false>(what, a, stream);
+    case Kernel::k32Split: return launch<Epi, 32, 64, 1, 1, 4, 2, 2, true>(what, a, stream);
+    case Kernel::k64Split: return launch<Epi, 64, 64, 1, 1, 4, 1, 2, true>(what, a, stream);
+    case Kernel::k256: return launch<Epi, 256, 256, 2, 4, 1, 1, 4, true>(what, a, stream);
+    case Kernel::k128: return launch<Epi, 128, 128, 2, 2, 1, 2, 2, true>(what, a, stream);
+    default: break;
+  }
+  return operator_fail(what, "no kernel");
 }
 
 }  // namespace

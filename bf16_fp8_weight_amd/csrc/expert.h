@@ -26,6 +26,7 @@ struct ProductArgs {
   int32_t m, n, k;      // n: columns of out (of h in the gated forms)
   int32_t act, out_f32;
   int32_t rests_last;   // order of the tiles, see find_rows()
+  uint32_t first_group;  // of this launch among the call's workgroups
 };
 
 enum class Epilogue { kPlain, kGated, kGatedBack };

@@ -8,6 +8,7 @@
 
 #include "expert_tile.h"
 #include "hip_util.h"
+#include "wt_internal.h"
 
 namespace wt {
 
@@ -30,8 +31,12 @@ wt_status launch(const char *what, ProductArgs a, hipStream_t stream) {
   }();
   if constexpr (Aligned && Form == kTN)
     if (a.row_index) kernel = product_kernel<Form, Epi, false, BM, BN, WM, WN, Split, Sub, Stages, true>;
-  hipLaunchKernelGGL(kernel, dim3((uint32_t)grid), dim3(64 * WM * WN * Split), 0, stream, a);
-  const hipError_t e = hipGetLastError();
+  constexpr uint32_t threads = 64 * WM * WN * Split;
+  const hipError_t e = launch_parts(grid, threads, hipSuccess, [&](uint32_t first, uint32_t count) {
+    a.first_group = first;
+    hipLaunchKernelGGL(kernel, dim3(count), dim3(threads), 0, stream, a);
+    return hipGetLastError();
+  });
   if (e != hipSuccess) return operator_fail(what, hip_msg("launch", e), WT_E_HIP);
   return WT_OK;
 }

@@ -568,8 +568,8 @@ __global__ void __launch_bounds__(64 * WM * WN) product_any_kernel(ProductArgs a
   Rows r;
   int mt, nt;
   const uint32_t n_tiles = (uint32_t)(a.n + T::kColumns - 1) / T::kColumns;
-  const bool mine = Form == kTN ? find_matrix(a, blockIdx.x, (uint32_t)(a.m + BM - 1) / BM, n_tiles, r, mt, nt)
-                                : find_rows<BM>(a, blockIdx.x, n_tiles, r, mt, nt);
+  const bool mine = Form == kTN ? find_matrix(a, a.first_group + blockIdx.x, (uint32_t)(a.m + BM - 1) / BM, n_tiles, r, mt, nt)
+                                : find_rows<BM>(a, a.first_group + blockIdx.x, n_tiles, r, mt, nt);
   if (!mine) return;
   const int tid = threadIdx.x, wave = tid >> 6, wm = wave / WN, wn = wave % WN;
   const int m0 = mt * BM, n0 = nt * T::kColumns;
@@ -800,8 +800,8 @@ __global__ void __launch_bounds__(64 * WM * WN * Split, WM * WN * Split == 4 && 
   Rows r;
   int mt, nt;
   const uint32_t n_tiles = (uint32_t)(a.n + T::kColumns - 1) / T::kColumns;
-  const bool mine = Form == kTN ? find_matrix(a, blockIdx.x, (uint32_t)(a.m + BM - 1) / BM, n_tiles, r, mt, nt)
-                                : find_rows<BM>(a, blockIdx.x, n_tiles, r, mt, nt);
+  const bool mine = Form == kTN ? find_matrix(a, a.first_group + blockIdx.x, (uint32_t)(a.m + BM - 1) / BM, n_tiles, r, mt, nt)
+                                : find_rows<BM>(a, a.first_group + blockIdx.x, n_tiles, r, mt, nt);
   if (!mine) return;
   const int waves = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int part = Split > 1 ? waves : 0, wave = Split > 1 ? 0 : waves, wm = wave / WN, wn = wave % WN;

@@ -18,6 +18,7 @@
 #include "plan.h"
 #include "wave.h"
 #include "wt.h"
+#include "wt_internal.h"
 
 namespace wt {
 namespace {
@@ -31,6 +32,7 @@ struct RoundArgs {
   const int32_t *index;
   int64_t n_rows, n_out, cols, x_stride, code_stride, scale_stride;
   uint32_t nb, n_blocks;
+  uint32_t first_group;  // of this launch among the call's workgroups
 };
 
 // The first `valid` (at most 8) values from element `at` on, as fp32.
@@ -61,7 +63,7 @@ __device__ __forceinline__ float scale_of(int c) { return __uint_as_float(c > 0 
 
 template <bool F32>
 __global__ void __launch_bounds__(kThreads) mxfp4_quantize_kernel(RoundArgs a) {
-  const uint32_t block = blockIdx.x * (uint32_t)(kThreads / kLanes) + threadIdx.x / kLanes;
+  const uint32_t block = (a.first_group + blockIdx.x) * (uint32_t)(kThreads / kLanes) + threadIdx.x / kLanes;
   const int l = threadIdx.x % kLanes;
   uint32_t i = 0, b = 0;
   int64_t src = -1;
@@ -94,7 +96,7 @@ __global__ void __launch_bounds__(kThreads) mxfp4_quantize_kernel(RoundArgs a) {
 // A code's value times a power of two is exact: values have at most two digits.
 template <bool F32>
 __global__ void __launch_bounds__(kThreads) mxfp4_dequantize_kernel(RoundArgs a) {
-  const uint32_t block = blockIdx.x * (uint32_t)(kThreads / kLanes) + threadIdx.x / kLanes;
+  const uint32_t block = (a.first_group + blockIdx.x) * (uint32_t)(kThreads / kLanes) + threadIdx.x / kLanes;
   if (block >= a.n_blocks) return;
   const int l = threadIdx.x % kLanes;
   const uint32_t i = block / a.nb, b = block - i * a.nb;
@@ -128,6 +130,15 @@ wt_status check_round(const char *what, int32_t dtype, int64_t n_rows, int64_t n
   return WT_OK;
 }
 
+hipError_t launch_round(void (*kernel)(RoundArgs), RoundArgs a, hipStream_t stream) {
+  const uint32_t groups = (a.n_blocks + kThreads / kLanes - 1) / (kThreads / kLanes);
+  return launch_parts(groups, kThreads, hipSuccess, [&](uint32_t first, uint32_t count) {
+    a.first_group = first;
+    hipLaunchKernelGGL(kernel, dim3(count), dim3(kThreads), 0, stream, a);
+    return hipGetLastError();
+  });
+}
+
 template <Epilogue Epi, int BM, int BN, int WM, int WN, int Split, int Sub, int Stages, bool Near>
 wt_status launch(const char *what, ProductArgs a, hipStream_t stream) {
   constexpr int columns = Epi == Epilogue::kGated ? BN / 2 : BN;
@@ -136,11 +147,16 @@ wt_status launch(const char *what, ProductArgs a, hipStream_t stream) {
   a.rests_last = grid <= 2 * kCus;  // as in expert_run.h
   if (grid > kMaxGrid) return operator_fail(what, "too many tiles");
   if (grid == 0) return WT_OK;
-  if constexpr (Near)
-    hipLaunchKernelGGL((product_kernel<kNT, Epi, true, BM, BN, WM, WN, Split, Sub, Stages, false>), dim3((uint32_t)grid), dim3(64 * WM * WN * Split), 0, stream, a);
-  else
-    hipLaunchKernelGGL((product_any_kernel<kNT, Epi, true, BM, BN, WM, WN, Sub>), dim3((uint32_t)grid), dim3(64 * WM * WN * Split), 0, stream, a);
-  const hipError_t e = hipGetLastError();
+  auto kernel = [] {
+    if constexpr (Near) return product_kernel<kNT, Epi, true, BM, BN, WM, WN, Split, Sub, Stages, false>;
+    else return product_any_kernel<kNT, Epi, true, BM, BN, WM, WN, Sub>;
+  }();
+  constexpr uint32_t threads = 64 * WM * WN * Split;
+  const hipError_t e = launch_parts(grid, threads, hipSuccess, [&](uint32_t first, uint32_t count) {
+    a.first_group = first;
+    hipLaunchKernelGGL(kernel, dim3(count), dim3(threads), 0, stream, a);
+    return hipGetLastError();
+  });
   if (e != hipSuccess) return operator_fail(what, hip_msg("launch", e), WT_E_HIP);
   return WT_OK;
 }
@@ -179,12 +195,11 @@ wt_status wt_mxfp4_quantize(const void *x, int32_t dtype, int64_t n_rows, int64_
     if ((uintptr_t)row_index % 4) return operator_fail(what, "row_index misaligned", WT_E_ALIGN);
     if ((uintptr_t)codes % 4 || code_row_stride % 4) return operator_fail(what, "codes not 4-byte aligned", WT_E_ALIGN);
     RoundArgs a{(uint64_t)(uintptr_t)x, (uint64_t)(uintptr_t)codes, (uint64_t)(uintptr_t)scales, row_index, n_rows,
-                n_out, cols, x_row_stride, code_row_stride, scale_row_stride, (uint32_t)((cols + 31) / 32), 0};
+                n_out, cols, x_row_stride, code_row_stride, scale_row_stride, (uint32_t)((cols + 31) / 32), 0, 0};
     a.n_blocks = (uint32_t)(n_out * a.nb);
     const StreamDevice on((hipStream_t)stream);
     const auto kernel = dtype == WT_DT_F32 ? mxfp4_quantize_kernel<true> : mxfp4_quantize_kernel<false>;
-    hipLaunchKernelGGL(kernel, dim3((a.n_blocks + kThreads / kLanes - 1) / (kThreads / kLanes)), dim3(kThreads), 0, (hipStream_t)stream, a);
-    const hipError_t e = hipGetLastError();
+    const hipError_t e = launch_round(kernel, a, (hipStream_t)stream);
     if (e != hipSuccess) return operator_fail(what, hip_msg("launch", e), WT_E_HIP);
     return WT_OK;
   } catch (...) {
@@ -204,12 +219,11 @@ wt_status wt_mxfp4_dequantize(const void *codes, int64_t code_row_stride, const 
     if ((uintptr_t)out % (dtype == WT_DT_F32 ? 4 : 2)) return operator_fail(what, "out misaligned", WT_E_ALIGN);
     if ((uintptr_t)codes % 4 || code_row_stride % 4) return operator_fail(what, "codes not 4-byte aligned", WT_E_ALIGN);
     RoundArgs a{(uint64_t)(uintptr_t)out, (uint64_t)(uintptr_t)codes, (uint64_t)(uintptr_t)scales, nullptr, n_rows,
-                n_rows, cols, out_row_stride, code_row_stride, scale_row_stride, (uint32_t)((cols + 31) / 32), 0};
+                n_rows, cols, out_row_stride, code_row_stride, scale_row_stride, (uint32_t)((cols + 31) / 32), 0, 0};
     a.n_blocks = (uint32_t)(n_rows * a.nb);
     const StreamDevice on((hipStream_t)stream);
     const auto kernel = dtype == WT_DT_F32 ? mxfp4_dequantize_kernel<true> : mxfp4_dequantize_kernel<false>;
-    hipLaunchKernelGGL(kernel, dim3((a.n_blocks + kThreads / kLanes - 1) / (kThreads / kLanes)), dim3(kThreads), 0, (hipStream_t)stream, a);
-    const hipError_t e = hipGetLastError();
+    const hipError_t e = launch_round(kernel, a, (hipStream_t)stream);
     if (e != hipSuccess) return operator_fail(what, hip_msg("launch", e), WT_E_HIP);
     return WT_OK;
   } catch (...) {

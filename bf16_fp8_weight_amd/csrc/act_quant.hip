@@ -92,7 +92,7 @@ __device__ __forceinline__ BlockAt locate(const ActArgs &a, uint32_t gblk, uint3
 // byte stores.
 __global__ void __launch_bounds__(kActThreads) act_quant_kernel(ActArgs a) {
   const uint32_t l = threadIdx.x & 15;
-  const BlockAt p = locate(a, blockIdx.x * (uint32_t)kActGroups + (threadIdx.x >> 4), l);
+  const BlockAt p = locate(a, (a.first_group + blockIdx.x) * (uint32_t)kActGroups + (threadIdx.x >> 4), l);
   uint32_t w[4] = {0u, 0u, 0u, 0u};
   const uint64_t xrow = a.x + 2ull * (uint64_t)p.src * (uint64_t)a.x_stride;
   if (p.has) {
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kActThreads) act_quant_wide_kernel(ActArgs a) 
   constexpr int NC = E / 8;   // 16-byte chunks per lane
   constexpr int G = kActThreads / L;
   const uint32_t l = threadIdx.x & (L - 1);
-  const uint32_t gblk = blockIdx.x * (uint32_t)G + threadIdx.x / L;
+  const uint32_t gblk = (a.first_group + blockIdx.x) * (uint32_t)G + threadIdx.x / L;
   uint32_t i = 0, b = 0;
   int64_t src = -1;
   if (gblk < a.n_blocks) {
@@ -179,16 +179,14 @@ __global__ void __launch_bounds__(kActThreads) act_quant_wide_kernel(ActArgs a) 
 }  // namespace
 
 hipError_t launch_act_quant(const ActArgs &a, bool fast, hipStream_t stream) {
-  if (a.n_blocks == 0) return hipSuccess;
-  if (fast) {
-    constexpr int G = kActThreads / kActLanes;
-    const dim3 grid((a.n_blocks + G - 1) / G);
-    hipLaunchKernelGGL((act_quant_wide_kernel<kActLanes>), grid, dim3(kActThreads), 0, stream, a);
-  } else {
-    const dim3 grid((a.n_blocks + kActGroups - 1) / kActGroups);
-    hipLaunchKernelGGL(act_quant_kernel, grid, dim3(kActThreads), 0, stream, a);
-  }
-  return hipGetLastError();
+  const uint32_t per = fast ? kActThreads / kActLanes : kActGroups;  // blocks of a workgroup
+  const auto kernel = fast ? act_quant_wide_kernel<kActLanes> : act_quant_kernel;
+  return launch_parts((a.n_blocks + per - 1) / per, kActThreads, hipSuccess, [&](uint32_t first, uint32_t count) {
+    ActArgs part = a;
+    part.first_group = first;
+    hipLaunchKernelGGL(kernel, dim3(count), dim3(kActThreads), 0, stream, part);
+    return hipGetLastError();
+  });
 }
 
 }  // namespace wt

@@ -131,6 +131,7 @@ struct ActArgs {
   int64_t s_stride;
   uint32_t nb;        // blocks per row, ceil(cols / 128)
   uint32_t n_blocks;  // n_out * nb < 2^31
+  uint32_t first_group;  // of this launch among the call's workgroups
 };
 
 // One launch takes fewer than 2^32 threads: a grid of more is launched in parts. Calls launch(first, count) for each, in order,

@@ -1,5 +1,5 @@
 """Calls whose workgroups have 2^32 threads or more in all, which no single launch takes: the weights' gradients
-of many experts, MXFP4 and back, over more blocks than fit. Values are exact, so that every element can be compared."""
+of many experts, MXFP4 and back, FP8 activations, over more blocks than fit. Values are exact, so that every element can be compared."""
 import pytest
 import torch
 
@@ -53,6 +53,29 @@ def test_mxfp4_there_and_back(wt):
     torch.cuda.synchronize()
     want_back = R.mx_values(want_codes, want_scales)[:, :1].to(BF16)
     for name, got, want in (("codes", codes, want_codes), ("scales", scales, want_scales), ("back", back, want_back)):
+        want = want.cuda()
+        for at in range(0, rows, 10 ** 8):  # a multiple of the period
+            part = got[at:at + 10 ** 8]
+            whole = len(part) // period * period
+            assert bool((part[:whole].view(-1, *want.shape) == want).all()), f"{name} from {at} on"
+            assert torch.equal(part[whole:], want[: len(part) - whole]), f"{name}: the end"
+
+
+# blocks of 16 lanes (any alignment) and of 8 (rows of 8 elements)
+@pytest.mark.parametrize("rows,cols", [((1 << 28) + 1000, 1), ((1 << 29) + 1000, 8)])
+def test_fp8_activations(wt, rows, cols):
+    period = 1000
+    some = torch.randn(period, cols, generator=torch.Generator().manual_seed(cols)).to(BF16)
+    some[7] = 0
+    x = some.cuda().repeat(rows // period + 1, 1)[:rows].contiguous()
+    q = torch.full((rows, cols), 0xA5, dtype=torch.uint8, device="cuda")
+    scales = torch.full((rows,), -7.0, device="cuda")
+    wt.wt_quantize_act_b128(x.data_ptr(), rows, cols, cols, 0, rows, q.data_ptr(), cols, scales.data_ptr(), 4, _stream())
+    torch.cuda.synchronize()
+    amax = some.float().abs().amax(1)
+    want_scales = torch.where(amax > 0, amax / 448, torch.ones_like(amax))
+    want = (some.float() / want_scales[:, None]).to(torch.float8_e4m3fn).view(torch.uint8)
+    for name, got, want in (("codes", q, want), ("scales", scales, want_scales)):
         want = want.cuda()
         for at in range(0, rows, 10 ** 8):  # a multiple of the period
             part = got[at:at + 10 ** 8]

@@ -47,6 +47,6 @@ def test_parts_cover_the_grid_and_fit_a_launch(tmp_path):
 def test_launches_that_may_exceed_one_grid_go_through_it():
     """Every launch of a kernel whose grid grows with rows, columns and experts without a limit of its own."""
     csrc = os.path.join(ROOT, "bf16_fp8_weight_amd", "csrc")
-    for name, launches in (("expert_run.h", 1), ("mxfp4.hip", 2)):
+    for name, launches in (("expert_run.h", 1), ("mxfp4.hip", 2), ("act_quant.hip", 1)):
         text = open(os.path.join(csrc, name)).read()
         assert text.count("hipLaunchKernelGGL(") == launches == text.count("dim3(count)"), name

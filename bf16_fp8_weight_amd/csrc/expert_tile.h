@@ -106,10 +106,11 @@ __device__ __forceinline__ void expert_rows(const ProductArgs &a, int e, int &fi
     return;
   }
   const int lo = a.offsets[e];
-  const int n = a.counts ? a.counts[e] : a.offsets[e + 1] - lo;
+  // offsets may be any two numbers: their difference has 33 bits
+  const int64_t n = a.counts ? a.counts[e] : (int64_t)a.offsets[e + 1] - lo;
   first = min(max(lo, 0), n_rows);
   // a first row below 0 takes its part of the count along
-  const int64_t end = (int64_t)lo + max(n, 0);
+  const int64_t end = lo + max(n, (int64_t)0);
   count = (int)max((int64_t)0, min(end, (int64_t)n_rows) - first);
 }
 

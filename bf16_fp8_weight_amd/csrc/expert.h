@@ -40,7 +40,8 @@ bool product_aligned(const ProductArgs &a, int form, Epilogue epi);
 constexpr int kCus = 256;
 constexpr int kXcds = 8;
 
-// Workgroups that deal out all tiles of bm rows and n_tiles columns of tiles.
+// Workgroups that deal out all tiles of bm rows and n_tiles columns of tiles. The rows of each expert are on the device: the
+// grid holds the tiles of any experts whose rows add up to n_rows at most, and of more than that (they overlap) not all.
 int64_t grid_of(const ProductArgs &a, int form, int bm, int64_t n_tiles);
 
 // Which kernel a product takes: rows x columns of its tiles; kAny: operands of any alignment, kSplit: waves that split the sum,

@@ -519,8 +519,10 @@ wt_status wt_dispatch_rows(const int32_t *index, int64_t n_tokens, int32_t top_k
  * space of n_rows rows, as wt_dispatch_rows leaves them; offsets and counts stay
  * on the device. Other rows (padding, and what lies behind the last expert) are
  * neither read nor written. Offsets or counts that leave [0, n_rows] are cut to
- * it; experts whose rows overlap give meaningless results in those rows, but no
- * access outside the arrays.
+ * it. Experts whose rows overlap are for TN only: in NT and NN a row of several experts
+ * holds meaningless results, and if the experts' rows add up to more than n_rows, any
+ * expert's results may be left unwritten in part (tiles are dealt for n_rows rows). Rows of
+ * no expert stay as they were, and no access leaves the arrays.
  *
  * wt_expert_product, per expert e with rows r (BF16 operands, fp32 sums, rounded
  * once to out_dtype):

@@ -66,3 +66,45 @@ def test_offsets_are_any_numbers(wt, offsets, counts):
                 _check(f"expert {e}", out[lo:hi], want, R.bound(want, mag, 64, F32), (owners[lo:hi] == 1))
         if form != R.TN:
             _untouched("rows of no expert", out, owners == 0)
+
+
+# name, n_rows, first rows and counts: one expert apart from those that overlap; the kernels of 16 x 64, 64 x 64, 128 x 128 and 256 x 256
+OVERLAPS = [("within", 100, [0, 20, 60], [30, 20, 40]), ("few rows", 60, [0] * 6 + [40], [40] * 6 + [20]),
+            ("64 rows", 700, [0] * 10 + [600], [600] * 10 + [100]), ("many", 9000, [0] * 10 + [8000], [8000] * 10 + [1000]),
+            ("two of many", 9000, [0, 100, 8000], [8000, 7900, 1000])]
+
+
+@pytest.mark.parametrize("name,n_rows,first,counts", OVERLAPS, ids=[o[0].replace(" ", "") for o in OVERLAPS])
+@pytest.mark.parametrize("gated", [False, True])
+def test_experts_that_overlap(wt, gated, name, n_rows, first, counts):
+    """Rows of one expert hold its results or nothing new (where all experts' rows fit into n_rows: its results), rows of none
+    nothing new, and nothing behind the rows is written."""
+    n, k, E, g = 520, 64, len(counts), _gen(n_rows)
+    a, b = _normal(g, n_rows, k), _normal(g, E, n * (1 + gated), k, std=0.2)
+    buf = torch.full((n_rows + 64, n), -7.0, dtype=torch.bfloat16, device="cuda")
+    ga, gb = _place(a), _place(b)
+    off, cnt = torch.tensor(first + [0], dtype=torch.int32).cuda(), torch.tensor(counts, dtype=torch.int32).cuda()
+    d = wt.wt_product_desc_init()
+    d.n_rows, d.n_experts, d.offsets, d.counts = n_rows, E, off.data_ptr(), cnt.data_ptr()
+    d.form, d.n, d.k, d.act = R.NT, n, k, R.SILU
+    _operands(d, ga, gb, buf[:n_rows])
+    if gated:
+        wt.wt_gated_forward(d, 0, 0, _stream())
+    else:
+        wt.wt_expert_product(d, _stream())
+    torch.cuda.synchronize()
+    owners = torch.zeros(n_rows, dtype=torch.int32)
+    for f, c in zip(first, counts):
+        owners[f:f + c] += 1
+    got = buf.cpu()
+    assert bool((got[n_rows:] == -7).all()) and bool((got[:n_rows][owners == 0] == -7).all())
+    for e, (f, c) in enumerate(zip(first, counts)):
+        alone = torch.nonzero(owners[f:f + c] == 1)[:, 0] + f
+        lay = R.Layout([len(alone)])
+        if gated:
+            want, bound = R.gated(lay, a[alone], b[e:e + 1], R.SILU)["h"]
+        else:
+            want, mag, terms = R.product(R.NT, lay, a[alone], b[e:e + 1])
+            bound = R.bound(want, mag, terms, torch.bfloat16)
+        right = (got[alone].double() - want).abs() <= bound
+        assert bool((right | ((got[alone] == -7) if sum(counts) > n_rows else torch.zeros_like(right))).all()), f"expert {e}"

@@ -747,15 +747,20 @@ __global__ void __launch_bounds__(64 * WM * WN) product_any_kernel(ProductArgs a
 // memory: rows behind the last, and offsets set to kNowhere.
 constexpr uint32_t kNowhere = 0x80000000u;
 
-// The compiler does not count these loads: wait_for_copies() waits for them.
+// The compiler does not count these loads: wait_for_copies() waits for them. It is told of M0, which it uses for operations of
+// its own (messages, indexed registers), none of them in these kernels now. (It warns
+// that it does not save M0 itself, which nothing here expects.)
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 template <int Add>
 __device__ __forceinline__ void copy16(u32x4 buffer, uint32_t lds, uint32_t offset) {
-  asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(buffer), "n"(Add) : "memory", "scc");
+  asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(buffer), "n"(Add) : "memory", "scc", "m0");
 }
 template <int Add>
 __device__ __forceinline__ void copy4(u32x4 buffer, uint32_t lds, uint32_t offset) {
-  asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(buffer), "n"(Add) : "memory", "scc");
+  asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(offset), "s"(buffer), "n"(Add) : "memory", "scc", "m0");
 }
+#pragma clang diagnostic pop
 
 // All but the last `Pending` of this wave's copies have arrived and what it read has been read; then the workgroup meets.
 template <int Pending, bool Meet>

@@ -194,15 +194,31 @@ int64_t grid_of(const ProductArgs &a, int form, int bm, int64_t n_tiles) {
 // through the gate 365 and 342 against 346; 24 experts' gated batch 1139 and 1109 against 925.)
 // Any alignment (64 | 64 x 128 | 128): 2001 rows, 4001 x 777, NT 49 | 61 | 76, NN 68 | 76 | 106, its TN 56 | 57 | 61; 777 x 4001
 // NT 43 | 39 | 29; 333 rows, 501 x 1001 gated 9.4 | 12.1 | 16.9; 8001 rows, 4097 x 4097 655 | 538 | 437.
+// Weights' gradients: tiles are the matrices' own (the grid rounds each expert's up to 8, which count for nothing), and a tile whose grid
+// has room for twice the results or more is too large: workgroups without a tile still wait for a CU's shared memory. Measured (out,
+// rows an expert; 64 | 64w | 128 | 128x | 256): 63 x (48 x 40): 10: 7.1 | 6.5 | 7.3 | 8.5 | 8.6, 100: 7.5 | 7.5 | 8.6 | 9.7 | 12.1; 32 x (256 x 256): 100: 7.2 |
+// 7.1 | 8.1 | 8.2 | 13.9, 700: 18.9 | 19.4 | 25.7 | 21.9 | 43.0; 300 x (64 x 64): 10: 10.6 | 7.6 | 12.1 | 10.9 | 21.4; 300 x (512 x 256): 100: 70 | 34.1 | 35.1 |
+// 34.8 | 51.3; 24 x (640 x 640): 83: 24.8 | 12.7 | 13.9 | 14.2 | 17.5, 333: 32.3 | 20.5 | 20.8 | 20.5 | 26.4; 50 x (128 x 512): 13.0 | 8.3 | 9.7 | 10.7 | 14.0.
+// From two thirds of a round of tiles on that are filled, 256 x 256 (128 | 128x | 256): 12 x (7168 x 4096): 50: 264 | 267 | 202, 100: 300 | 332 | 241,
+// 200: 385 | 393 | 303, 400: 527 | 479 | 404, 683: 708 | 654 | 538; 12 x (1024 x 2048): 100: 20.9 | 21.3 | 21.5, 400: 35.7 | 35.2 | 33.7, 683: 45.7 | 47.2 | 43.8;
+// 24 x (1368 x 1000): 83: 32.5 | 30.8 | 30.9, 333: 55.0 | 47.5 | 45.4; dense, 4096 rows: 3328 x 3328 97.5 | 95.1 | 81.8, 2816 x 2816 (121 tiles) 59.8 | 66.0 | 80.2; 8192 x
+// 8192: 100 rows 37.6 | 42.4 | 42.9, 2000 rows 249 | 267 | 211. Any alignment (64 | 128): 63 x (41 x 49): 7.7 | 10.5; 300 x (65 x 65): 10.0 | 20.2; 32 x (255 x
+// 255): 12.5 | 18.8; 5 x (1001 x 2735): 30.5 | 28.3.
 Kernel product_kernel_of(const ProductArgs &a, int form, Epilogue epi) {
   const bool tn = form == WT_PRODUCT_TN;
   const int64_t halves = epi == Epilogue::kGated ? 2 : 1;  // of a tile's columns are out's
-  auto tiles = [&](int rows, int columns) { return grid_of(a, form, rows, (a.n * halves + columns - 1) / columns); };
-  if (!product_aligned(a, form, epi)) return tiles(128, 128) >= kCus ? Kernel::kAny128 : Kernel::kAny64;
+  auto across = [&](int columns) { return (a.n * halves + columns - 1) / columns; };
+  auto tiles = [&](int rows, int columns) {
+    return tn ? ((int64_t)a.m + rows - 1) / rows * across(columns) * a.n_experts : grid_of(a, form, rows, across(columns));
+  };
+  auto too_large = [&](int edge) {
+    return tn && grid_of(a, form, edge, across(edge)) * edge * edge >= 2 * (int64_t)a.m * a.n * a.n_experts;
+  };
+  if (!product_aligned(a, form, epi)) return tiles(128, 128) >= kCus && !too_large(128) ? Kernel::kAny128 : Kernel::kAny64;
   if (!tn && tiles(16, 64) <= kCus) return Kernel::k16Split;
   if (tiles(64, 64) <= kCus) return Kernel::k64Split;
-  if (tiles(64, 128) <= kCus) return Kernel::k64x128;
-  if (3 * tiles(256, 256) >= 2 * kCus && (tn || a.n_rows > 256 * (int64_t)a.n_experts)) return Kernel::k256;
+  if (tiles(64, 128) <= kCus || too_large(128)) return Kernel::k64x128;
+  if (3 * tiles(256, 256) >= 2 * kCus && (tn ? !too_large(256) : a.n_rows > 256 * (int64_t)a.n_experts)) return Kernel::k256;
   return tiles(128, 128) >= kCus ? Kernel::k128 : Kernel::k128Wide;
 }
 

@@ -29,14 +29,20 @@ GRADIENTS = [
     ("any64", R.Layout([77, 0, 300]), 131, 77),
     ("any128", R.Layout([77]), 2101, 2049),
     ("any128", ODD, 2101, 777),
+    ("any64", R.Layout([10, 0, 12] * 21), 41, 49),
+    ("any64", R.Layout([5, 0, 3] * 100), 65, 65),
+    ("64split", R.Layout([10, 0, 12] * 21), 40, 48),
     ("64split", R.Layout([3000]), 130, 200),
     ("64split", SIX, 194, 130),
     ("64x128", R.Layout([300]), 702, 2000),
     ("64x128", R.Layout([31]), 1024, 2048),
+    ("64x128", R.Layout([5, 0, 3] * 100), 64, 64),
+    ("64x128", R.Layout([70, 9] * 20), 200, 200),
     ("128wide", R.Layout([300]), 1030, 2052),
     ("128wide", R.Layout([513, 0, 130, 257], lead=2, tail=9), 642, 1030),
     ("128", R.Layout([333]), 2050, 2052),
     ("128", R.Layout([300, 0, 500, 33, 7]), 1026, 1030),
+    ("128", R.Layout([70, 100] * 12), 640, 640),
     ("256", R.Layout([70]), 4100, 4106),
     ("256", EIGHT, 1026, 2052),
 ]

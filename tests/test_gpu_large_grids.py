@@ -20,7 +20,7 @@ def _stream():
     return torch.cuda.current_stream().cuda_stream
 
 
-# 1024 experts x 2^21 rows of out; one column: tiles of 128 x 128, 2^24 workgroups of 256; two: 256 x 256, 2^23 of 512
+# 1024 experts x 2^21 rows of out: 2^25 tiles, 2^33 threads; one column: the kernel of any alignment
 @pytest.mark.parametrize("n", [1, 2])
 def test_gradients_of_many_weights(wt, n):
     m, E = 1 << 21, 1024

@@ -226,8 +226,12 @@ Kernel product_kernel_of(const ProductArgs &a, int form, Epilogue epi) {
 // 7.1 | 8.3 | 12.1; 64 rows, 1024 x 2816 gated 6.3 | 6.5 | 7.9 | 9.9; 100 rows, 7168 x 4096 9.4 | 12.4 | 17.1 | 27.4; 256 rows, 2816 x 1024
 // gated 7.3 | 7.8 | 10.9 | 23.8; 512 rows, 2048 x 2048 10.4 | 7.1 | 9.2 | 19.1; 1024 rows 19.3 | 9.5 | 9.6 | 19.4; 2048 rows, 4096 x 4096
 // 94.5 | 47.2 | 26.2 | 33.0; 4096 rows - | - | 49.1 | 46.7; 256 rows of 96 experts, 7168 x 2048 gated 300 | - | 258 | 304; 2000 rows of 24
-// experts - | - | 100 | 108; 6000 rows 181 | 193; 9600 rows 241 | 246; 12000 rows 286 | 252; 180 tiles of 256, 2944 rows, 7168 x 3840 59 |
-// 52.5, 2048 x 3840 22.8 | 24.1; 8192 cubed - | - | 327 | 296.
+// experts - | - | 100 | 108; 6000 rows 181 | 193; 9600 rows 241 | 246; 12000 rows 286 | 252; 8192 cubed - | - | 327 | 296.
+// Tiles of 256 want sums of 3584 terms or more besides (28 steps). By the sum's length, 1024 | 2048 | 2816 | 3584 | 4096 | 7168 | 14336, tiles of 128 and of
+// 256 rows: 2944 rows x 3840, 180 tiles: 16.4 18.3 | 22.9 24.1 | 28.1 28.4 | 33.4 32.6 | 37.1 35.4 | 59.4 52.4 | 110 92.6; 3328 x 4096: - | 27.3 26.1 | 33.1
+// 31.2 | 39.9 36.1 | 43.4 39.5 | 67.5 58.1; 8192 x 8192: 67.6 80.3 | 105 112 | 133 136 | 163 157 | 182 172; 4096 x 4096 gated: - | 55.2 57.4 | 69.0 69.4 |
+// 82.8 80.9 | 93.0 87.5; 8192 rows of 12 experts x 2048: - | 35.3 42.3 | - | 53.2 57.7 | 59.0 63.3 | 91.8 98.5; 16384 rows of 24 experts x 2048 gated, 4096: 214
+// 198; 12288 rows of 12 experts x 7168, 2048: 159 156.
 Kernel mxfp4_kernel_of(const ProductArgs &a, Epilogue epi) {
   const int64_t far = (int64_t)1 << 31;
   // 31-bit offsets within a tile's rows, as in product_aligned()
@@ -238,7 +242,7 @@ Kernel mxfp4_kernel_of(const ProductArgs &a, Epilogue epi) {
   auto tiles = [&](int rows, int columns) { return grid_of(a, WT_PRODUCT_NT, rows, (a.n * halves + columns - 1) / columns); };
   if (tiles(32, 64) <= kCus) return Kernel::k32Split;
   if (tiles(64, 64) <= kCus) return Kernel::k64Split;
-  if (3 * tiles(256, 256) >= 2 * kCus && a.n_rows > 256 * (int64_t)a.n_experts) return Kernel::k256;
+  if (a.k >= 3584 && 3 * tiles(256, 256) >= 2 * kCus && a.n_rows > 256 * (int64_t)a.n_experts) return Kernel::k256;
   return Kernel::k128;
 }
 

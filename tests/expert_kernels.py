@@ -69,8 +69,10 @@ MXFP4 = [
     ("64split", SIX, 1032, 3000),
     ("128", R.Layout([1030]), 2600, 200),
     ("128", R.Layout([70] * 30 + [0, 129], align=128), 1100, 1300),
-    ("256", R.Layout([4100]), 4104, 1000),
-    ("256", EIGHT, 4000, 330),
+    ("128", R.Layout([4100]), 4104, 1000),
+    ("128", EIGHT, 4000, 3583),
+    ("256", R.Layout([4100]), 4104, 3584),
+    ("256", EIGHT, 4000, 3633),
 ]
 
 

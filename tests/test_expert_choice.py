@@ -73,3 +73,13 @@ def test_mxfp4(choose):
         assert got == [c[0] for c in K.MXFP4]
         assert set(got) == {"32split", "64split", "128", "256"}  # any128: test_mxfp4_rows_far_apart
         assert choose([("m", int(gated), 33, 1, 0, 24, 70, 2 ** 22 + 16, 4, 2 ** 22 + 16, 4)]) == ["any128"]
+
+
+def test_mxfp4_weights_beyond_31_bits(choose):
+    """A plain product's tiles reach 256 rows, however long the matrix is; gated ones from the gate rows to the up rows."""
+    rows, k = 2 ** 18 + 8, 2 ** 14  # 2 GiB of codes
+    line = lambda gated, n, b_stride, scale: ("m", gated, 200, 1, 0, n, k, k // 2, k // 32, b_stride, scale)
+    assert choose([line(0, rows, k // 2, k // 32), line(0, rows, k // 2, 2 ** 14), line(1, rows // 2 + 8, k // 2, k // 32)]) == ["128"] * 3
+    assert choose([line(1, rows, k // 2, k // 32), line(1, rows, k // 2, 2 ** 14), line(0, 40, 2 ** 22 + 16, k // 32),
+                   line(0, 40, k // 2, 2 ** 22 + 4)]) == ["any128"] * 4
+    assert choose([line(0, 40, 2 ** 22, k // 32), line(0, 40, k // 2, 2 ** 22)]) != ["any128"] * 2

@@ -65,11 +65,13 @@ constexpr int kScaleRow = 16;
 // ------------------------------------------------------------- activations
 // Both are x s(y) with s(y) = 1 / (1 + exp(-y)): SiLU y = x; GELU's
 // (1 + tanh(z)) / 2 = s(2 z). With t = exp(-|y|) both s and 1 - s are t / (1 + t) or
-// 1 / (1 + t), without a difference that cancels or an exponential that overflows.
+// 1 / (1 + t), without a difference that cancels or an exponential that overflows. t is taken as the square of h =
+// exp(-|y| / 2), and x and the slope's factor meet one h before the other: below y = -87.3 t leaves the normal numbers
+// (exp2 gives 0 for those), while x s still is one of BF16's, down to 2^-133.
 // exp2 and the reciprocal are good to a last place of fp32 and exp2's argument to
 // 2^-22 |y|, far below the BF16 result's 2^-8.
 struct Act {
-  float value, slope;
+  float value, slope, scale;  // the activation is value scale, its slope is slope scale
 };
 
 __device__ __forceinline__ Act activation(int act, float x) {
@@ -80,13 +82,15 @@ __device__ __forceinline__ Act activation(int act, float x) {
     y = kC * x * (1.0f + 0.044715f * x2);
     dy = kC * (1.0f + 3.0f * 0.044715f * x2);
   }
-  const float t = __builtin_amdgcn_exp2f(-kLog2e * fabsf(y)), r = __builtin_amdgcn_rcpf(1.0f + t), q = t * r;
-  const float s = y >= 0.0f ? r : q, rest = y >= 0.0f ? q : r;  // a NaN is in both
+  const float h = __builtin_amdgcn_exp2f(-0.5f * kLog2e * fabsf(y)), t = h * h, r = __builtin_amdgcn_rcpf(1.0f + t);
+  // s = p (p r) and 1 - s; a NaN is in all of them
+  const float p = y >= 0.0f ? 1.0f : h, rest = y >= 0.0f ? t * r : r;
   Act f;
+  f.scale = p * r;
   // -FLT_MAX times a logistic of 0 is the limit 0, where -infinity would make a NaN
-  f.value = fmaxf(x, -FLT_MAX) * s;
-  // s (1 - s) is 0 in fp32 long before x dy could overflow
-  f.slope = s + s * rest * (fminf(fmaxf(x, -1e4f), 1e4f) * fminf(dy, 1e9f));
+  f.value = fmaxf(x, -FLT_MAX) * p;
+  // s (1 + (1 - s) x dy); where x dy passes these limits, t is 0, and with it 1 - s or p
+  f.slope = (1.0f + rest * __builtin_amdgcn_fmed3f(x * dy, -1e13f, 1e13f)) * p;
   return f;
 }
 
@@ -494,7 +498,10 @@ __device__ __forceinline__ void finish8(const ProductArgs &a, uint64_t out, int6
     }
     float h[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = activation(a.act, s[i]).value * up[i];
+    for (int i = 0; i < 8; ++i) {
+      const Act t = activation(a.act, s[i]);
+      h[i] = t.value * t.scale * up[i];
+    }
     store8<__bf16>(out, row * a.out_stride + column, h, n);
   } else {
     float g[8], u[8], dg[8], du[8];
@@ -503,8 +510,9 @@ __device__ __forceinline__ void finish8(const ProductArgs &a, uint64_t out, int6
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const Act t = activation(a.act, g[i]);
-      dg[i] = s[i] * u[i] * t.slope;
-      du[i] = s[i] * t.value;
+      const float dh = s[i] * t.scale;
+      dg[i] = dh * u[i] * t.slope;
+      du[i] = dh * t.value;
     }
     store8<__bf16>(out, row * a.out_stride + column, dg, n);
     store8<__bf16>(out, row * a.out_stride + a.n + column, du, n);

@@ -185,8 +185,8 @@ int64_t grid_of(const ProductArgs &a, int form, int bm, int64_t n_tiles) {
 //   4096 rows, 4096 x 4096, NT: - | - | - | 152 | 114 | 106           TN: - | - | - | 132 | 117 | 102
 //   2000 rows of 24 experts, 7168 x 2048 gated: - | - | - | 372 | 300 | 336; 8192 cubed, NT: - | - | - | 1196 | 1010 | 804
 //   256 rows of 96 experts, 7168 x 2048 gated: 945 | 986 | - | 868 | 859 | 981; 2048 x 7168: 492 | 532 | - | 418 | 445 | 462
-// A tile's way through shared memory is what bounds the small ones (a step of 64 x 128 takes 0.13 us, of 128 x 128 0.2 to
-// 0.25), so they pay as long as each has a CU of its own. Waves that split the sum shorten the chain of steps (two stages,
+// A tile's way through shared memory is what bounds the small ones (32 terms of a sum take 0.19 us in a tile of 64 x 128, 0.23 in 128 x 128 with
+// eight waves, 0.33 with four, 0.72 in 256 x 256), so they pay as long as each has a CU of its own. Waves that split the sum shorten the chain of steps (two stages,
 // which leave room for two workgroups, are up to 7 % faster than four); 256 x 256 pays from two thirds of a round of
 // tiles on (128 | 256: 121 tiles, 2800 rows, 4096 x 2800 NT 62 | 78; 180, 2944 rows, 2048 x 3840 NT 53.5 | 46.5, NN 55 | 46.6; 203, 7312
 // rows, 2560 x 864 gated 74 | 62), if experts fill them (rows an expert, 128 | 256): 24 x 7168 x 2048 gated: 83: 300 | 336, 250: 530 | 553, 400: 720 | 716, 500: 839 |

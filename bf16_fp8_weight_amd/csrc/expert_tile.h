@@ -20,10 +20,11 @@
 //
 // product_kernel (aligned operands) is bound by the matrix units where there are tiles for
 // every CU, and there by power: matrix instructions alone, from registers, reach 1.61 PFLOP/s on
-// random BF16 values. 8192 x 8192 x 8192: NT 1365 TFLOP/s, NN 1409, TN 1425, MXFP4 3730 to 3800. With few
-// rows it is bound by the weights' bytes (24 to 96 experts' weights at 6.3 to 6.9 TB/s), with few of both
+// random BF16 values. 8192 x 8192 x 8192, from card to card: NT 1312 to 1375 TFLOP/s, NN 1354 to 1426, TN 1355 to 1433 (matrix units busy
+// 75 % of the time), MXFP4 3600 to 3740 (50 %; its 256 x 256 tiles spill 4 and 5 registers, reloaded in the first copies and the last steps).
+// With few rows it is bound by the weights' bytes (those of the experts that have rows at 5.1 to 6.2 TB/s), with few of both
 // by the chain of steps. product_any_kernel (any stride) is bound by loads that
-// straddle cache lines: 2001 rows, 4001 x 777, NT 49 us, NN 68; 8001 rows, 4097 x 4097, 437 us (615 TFLOP/s).
+// straddle cache lines: 2001 rows, 4001 x 777, NT 49 us, NN 68; 8001 rows, 4097 x 4097, 433 us (620 TFLOP/s).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -256,7 +257,7 @@ __device__ __forceinline__ uint32_t swizzle(uint32_t k) { return ((k & 3) | (N >
 
 // Rows along the sum, 64 or 128 bytes each: ds_read_b128 serves the lanes 0-3, 12-15, 20-23 and 24-27 together (then 4-11, 16-19 and
 // 28-31, and so on), which are rows 0-15 in two chunks for BF16 and the rows of these numbers for MXFP4. Without this split
-// MXFP4's reads took twice as long.
+// MXFP4's reads took twice as long. BF16 has no conflicts left in any form, MXFP4 in 38 % of shared memory's cycles (8192 x 8192 x 8192).
 template <bool F4, int Sub>
 __device__ __forceinline__ uint32_t swizzle_along(uint32_t row) { return Sub == 2 ? row >> 1 & 7 : F4 ? row >> 2 & 3 : row >> 1 & 3; }
 
@@ -504,6 +505,9 @@ __device__ __forceinline__ void finish8(const ProductArgs &a, uint64_t out, int6
     }
     store8<__bf16>(out, row * a.out_stride + column, h, n);
   } else {
+    // d(pre) leaves in BF16, as the operand of two products: in fp32 they would take it as two BF16 terms, twice the matrix
+    // instructions (1.1 of 1.66 ms of 8192 rows of 12 experts, 7168, 2048). What it costs: 0.00235 of the gradients' norm against
+    // 0.00166 with d(pre) in fp32; the results themselves are BF16, of which 0.00166 is the rounding.
     float g[8], u[8], dg[8], du[8];
     load_pre(a.pre, row * a.pre_stride + column, n, g);
     load_pre(a.pre, row * a.pre_stride + a.n + column, n, u);

@@ -541,14 +541,16 @@ wt_status wt_dispatch_rows(const int32_t *index, int64_t n_tokens, int32_t top_k
  * wt_gated_backward (form NN, a = the gradient of the block's output, b_e = the
  * weights back, [k x n]): dh = a[r] . b_e[:, j], g and u from pre,
  *   out[r, j] = dh u act'(g), out[r, n + j] = dh act(g), in BF16 (out has 2n columns).
+ *   Rounded, since it is an operand of the products below: the gradients of rows and gate_up weights
+ *   differ from 64 bits by 0.0023 to 0.0024 of their norm, and by 0.0017 if it is kept in fp32.
  * The rest of the block's backward pass are products of `out`: NN with the
  * gate_up weights for the rows' gradient, TN with the rows for the weights'.
  *   act = WT_ACT_SILU: x / (1 + exp(-x)); WT_ACT_GELU: x / 2 (1 + tanh(sqrt(2 / pi)
  *   (x + 0.044715 x^3))); at an infinity their limits.
  *
  * A NaN or an infinity in an operand reaches exactly the results whose sum it is
- * part of. Sums run in an order that depends on the sizes alone: a call repeats
- * bit for bit.
+ * part of. Sums run in an order that depends on sizes, strides and alignment alone (and
+ * on whether offsets are given): a call repeats bit for bit, whichever rows the experts own.
  *
  * Speed. Arrays whose addresses, row and expert strides are even numbers of
  * elements, with even sizes (NT: k; NN: k and n; TN: m and n) and spans below

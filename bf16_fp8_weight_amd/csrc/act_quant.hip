@@ -16,6 +16,7 @@
 #include <hip/hip_runtime.h>
 
 #include "fp8_math.h"
+#include "launch_parts.h"
 #include "wave.h"
 #include "wt_internal.h"
 
@@ -87,12 +88,13 @@ __device__ __forceinline__ BlockAt locate(const ActArgs &a, uint32_t gblk, uint3
   return p;
 }
 
+// first_group: of the launch among the call's workgroups.
 // Unaligned path (any shape and alignment): one block per 16-lane group, lane
 // l owns channels [128 b + 8 l, +8), read with 2-byte loads and written with
 // byte stores.
-__global__ void __launch_bounds__(kActThreads) act_quant_kernel(ActArgs a) {
+__global__ void __launch_bounds__(kActThreads) act_quant_kernel(ActArgs a, uint32_t first_group) {
   const uint32_t l = threadIdx.x & 15;
-  const BlockAt p = locate(a, (a.first_group + blockIdx.x) * (uint32_t)kActGroups + (threadIdx.x >> 4), l);
+  const BlockAt p = locate(a, (first_group + blockIdx.x) * (uint32_t)kActGroups + (threadIdx.x >> 4), l);
   uint32_t w[4] = {0u, 0u, 0u, 0u};
   const uint64_t xrow = a.x + 2ull * (uint64_t)p.src * (uint64_t)a.x_stride;
   if (p.has) {
@@ -134,12 +136,12 @@ static_assert(kActLanes == 4 || kActLanes == 8 || kActLanes == 16, "lanes per bl
 // l, l + L, l + 2 L, ..., so that each load and store instruction covers
 // consecutive bytes across the lanes of a wave.
 template <int L>
-__global__ void __launch_bounds__(kActThreads) act_quant_wide_kernel(ActArgs a) {
+__global__ void __launch_bounds__(kActThreads) act_quant_wide_kernel(ActArgs a, uint32_t first_group) {
   constexpr int E = 128 / L;  // channels per lane
   constexpr int NC = E / 8;   // 16-byte chunks per lane
   constexpr int G = kActThreads / L;
   const uint32_t l = threadIdx.x & (L - 1);
-  const uint32_t gblk = (a.first_group + blockIdx.x) * (uint32_t)G + threadIdx.x / L;
+  const uint32_t gblk = (first_group + blockIdx.x) * (uint32_t)G + threadIdx.x / L;
   uint32_t i = 0, b = 0;
   int64_t src = -1;
   if (gblk < a.n_blocks) {
@@ -182,9 +184,7 @@ hipError_t launch_act_quant(const ActArgs &a, bool fast, hipStream_t stream) {
   const uint32_t per = fast ? kActThreads / kActLanes : kActGroups;  // blocks of a workgroup
   const auto kernel = fast ? act_quant_wide_kernel<kActLanes> : act_quant_kernel;
   return launch_parts((a.n_blocks + per - 1) / per, kActThreads, hipSuccess, [&](uint32_t first, uint32_t count) {
-    ActArgs part = a;
-    part.first_group = first;
-    hipLaunchKernelGGL(kernel, dim3(count), dim3(kActThreads), 0, stream, part);
+    hipLaunchKernelGGL(kernel, dim3(count), dim3(kActThreads), 0, stream, a, first);
     return hipGetLastError();
   });
 }

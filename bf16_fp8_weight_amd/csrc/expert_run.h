@@ -8,7 +8,7 @@
 
 #include "expert_tile.h"
 #include "hip_util.h"
-#include "wt_internal.h"
+#include "launch_parts.h"
 
 namespace wt {
 

@@ -15,10 +15,10 @@
 #include "expert_tile.h"
 #include "fp8_math.h"
 #include "hip_util.h"
+#include "launch_parts.h"
 #include "plan.h"
 #include "wave.h"
 #include "wt.h"
-#include "wt_internal.h"
 
 namespace wt {
 namespace {

@@ -1,4 +1,4 @@
-"""How a grid of more threads than a launch takes is cut into launches (wt_internal.h), on the CPU."""
+"""How a grid of more threads than a launch takes is cut into launches (launch_parts.h), on the CPU."""
 import os
 import subprocess
 
@@ -8,7 +8,7 @@ PROGRAM = r"""
 #include <cstdio>
 #include <cstdlib>
 #include <initializer_list>
-#include "wt_internal.h"
+#include "launch_parts.h"
 static void fail(const char *what, long long g, long long t) { std::printf("%s: %lld x %lld\n", what, g, t); std::exit(1); }
 int main() {
   const long long limit = 1LL << 32, most = (1LL << 31) - 1;

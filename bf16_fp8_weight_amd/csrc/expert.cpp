@@ -235,8 +235,8 @@ Kernel product_kernel_of(const ProductArgs &a, int form, Epilogue epi) {
 Kernel mxfp4_kernel_of(const ProductArgs &a, Epilogue epi) {
   const int64_t far = (int64_t)1 << 31;
   // 31-bit offsets within a tile's rows, as in product_aligned(): 256 of them, and gated from the gate rows to the up rows
-  const int64_t b_span = epi == Epilogue::kGated ? (int64_t)a.n + 512 : 512;
-  const bool near = a.a_stride <= far / 512 && b_span * a.b_stride <= far && a.a_scale_stride <= far / 512 && b_span * a.b_scale_stride <= far;
+  const int64_t most = far / 512, b_most = epi == Epilogue::kGated ? far / ((int64_t)a.n + 512) : most;
+  const bool near = a.a_stride <= most && a.b_stride <= b_most && a.a_scale_stride <= most && a.b_scale_stride <= b_most;
   if (!near) return Kernel::kAny128;
   const int64_t halves = epi == Epilogue::kGated ? 2 : 1;
   auto tiles = [&](int rows, int columns) { return grid_of(a, WT_PRODUCT_NT, rows, (a.n * halves + columns - 1) / columns); };

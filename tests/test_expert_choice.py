@@ -18,7 +18,7 @@ PLAIN, GATED, GATED_BACK = range(3)
 @pytest.fixture(scope="module")
 def choose(tmp_path_factory):
     exe = str(tmp_path_factory.mktemp("choice") / "expert_choice")
-    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-I", os.path.join(ROOT, "include"), "-I", CSRC, *SOURCES, "-o", exe,
+    subprocess.run(["g++", "-std=c++17", "-O1", "-ftrapv", "-Wall", "-I", os.path.join(ROOT, "include"), "-I", CSRC, *SOURCES, "-o", exe,
                     "-lpthread"], check=True)
 
     def run(lines):
@@ -83,3 +83,20 @@ def test_mxfp4_weights_beyond_31_bits(choose):
     assert choose([line(1, rows, k // 2, k // 32), line(1, rows, k // 2, 2 ** 14), line(0, 40, 2 ** 22 + 16, k // 32),
                    line(0, 40, k // 2, 2 ** 22 + 4)]) == ["any128"] * 4
     assert choose([line(0, 40, 2 ** 22, k // 32), line(0, 40, k // 2, 2 ** 22)]) != ["any128"] * 2
+
+
+def test_the_largest_strides_and_sizes(choose):
+    """No sum or product of the rule passes 64 bits (-ftrapv ends the program), and far rows take the kernels that reach them."""
+    far = 2 ** 58
+    for gated in (0, 1):
+        base = ["m", gated, 2, 1, 0, 2 - gated, 70, 48, 4, 48, 4]
+        lines = []
+        for at in (7, 8, 9, 10):
+            lines.append(base[:at] + [far] + base[at + 1:])
+        assert choose(lines) == ["any128"] * 4
+    big = 2 ** 24
+    assert choose([("m", 0, 2 ** 20, 1024, 1, big, big, big // 2, big // 32, big // 2, big // 32)]) == ["any128"]
+    assert choose([("p", R.TN, PLAIN, 2 ** 27, 1024, 1, -1, 2 ** 12, 2 ** 12, 0, 2 ** 12, 2 ** 12)]) == ["256"]
+    assert choose([("p", R.TN, PLAIN, 2, 1, 0, -1, big, big, 0, far, far)]) == ["any128"]
+    assert choose([("p", R.NT, PLAIN, 2 ** 20, 1024, 1, -1, 0, 2 ** 20, 64, 64, 64)]) == ["256"]
+    assert choose([("p", R.NT, PLAIN, 2, 1, 0, 5, 0, 2, 64, 2 ** 56, far)]) == ["any64"]
